@@ -54,13 +54,15 @@ typedef enum {
   FLAMIA_ERR_WORKSPACE_TOO_SMALL = 3,
   FLAMIA_ERR_CUDA = 4,
   FLAMIA_ERR_TIMEOUT = 5,
-  FLAMIA_ERR_BAD_SEQLENS = 6
+  FLAMIA_ERR_BAD_SEQLENS = 6,
+  FLAMIA_ERR_NO_PAGES = 7, /* paged cache: the free stack has too few pages */
+  FLAMIA_ERR_BAD_PAGE = 8  /* paged cache: a page id, slot or free count out of range */
 } flamia_status_t;
 
 /* [SUM] §3.4: the two default training paths. */
 typedef enum { FLAMIA_PATH_MXFP8 = 0, FLAMIA_PATH_NVFP4_FP8 = 1 } flamia_path_t;
 
-typedef enum { FLAMIA_F32 = 0, FLAMIA_BF16 = 1 } flamia_dtype_t;
+typedef enum { FLAMIA_F32 = 0, FLAMIA_BF16 = 1, FLAMIA_E4M3 = 2 /* paged caches only */ } flamia_dtype_t;
 
 typedef enum { FLAMIA_ROLE_QKV = 0, FLAMIA_ROLE_DO = 1 } flamia_role_t;
 
@@ -289,18 +291,24 @@ flamia_status_t flamia_debug_withhold_first_item(int32_t on);
  *                         operands, UE8M0 scales (one per 32 K-elements);
  *     FLAMIA_MMA_MXF4NVF4 kind::mxf4nvf4.block_scale.scale_vec::4X, E2M1
  *                         operands, UE4M3 scales (one per 16 K-elements);
+ *     FLAMIA_MMA_BF16     kind::f16, BF16 x BF16, fp32 accumulator;
  *   for an M x N tile (cta_group::1: M = 64 with N a multiple of 8, or
  *   M = 128 with N a multiple of 16; 8 or 16 <= N <= 256).  a_mn / b_mn = 1
  *   selects an MN-major operand (0 or 1; 0 for the E2M1 kind), a_sf_id /
  *   b_sf_id the scale-factor ids of the block-scaled kinds (0..3; 0 for the
- *   E2M1 kind, 0 for kind::f8f6f4).  Writes *out and returns FLAMIA_OK;
+ *   E2M1 kind, 0 for kind::f8f6f4 and kind::f16).  Writes *out and returns FLAMIA_OK;
  *   FLAMIA_ERR_INVALID_ARG for a NULL out or an argument outside these
  *   ranges (then *out is untouched).
  * flamia_debug_smem_desc: the 64-bit shared-memory matrix descriptor for a
  *   tile at shared address saddr with leading- and stride-dimension byte
  *   offsets lbo / sbo (all multiples of 16 below 2^18) and swizzle mode
  *   FLAMIA_SWZ_NONE / _128B / _64B / _32B.  Same return rules. */
-typedef enum { FLAMIA_MMA_F8F6F4 = 0, FLAMIA_MMA_MXF8F6F4 = 1, FLAMIA_MMA_MXF4NVF4 = 2 } flamia_mma_kind_t;
+typedef enum {
+  FLAMIA_MMA_F8F6F4 = 0,
+  FLAMIA_MMA_MXF8F6F4 = 1,
+  FLAMIA_MMA_MXF4NVF4 = 2,
+  FLAMIA_MMA_BF16 = 4 /* the paged chunk kernel's */
+} flamia_mma_kind_t;
 typedef enum { FLAMIA_SWZ_NONE = 0, FLAMIA_SWZ_128B = 2, FLAMIA_SWZ_64B = 4, FLAMIA_SWZ_32B = 6 } flamia_swizzle_t;
 flamia_status_t flamia_debug_mma_idesc(int32_t kind, uint32_t M, uint32_t N, int32_t a_mn, int32_t b_mn,
                                        int32_t a_sf_id, int32_t b_sf_id, uint32_t* out);
@@ -331,6 +339,150 @@ flamia_status_t flamia_debug_smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sb
  * and must be serialised by the caller. */
 flamia_status_t flamia_plan_noalloc(const flamia_problem_t* p, int2* fwd_items, int2* bwd_items, int32_t* n_items,
                                     cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Serving from a paged key/value cache (this library's own addition; the
+ * method's pages stop at the training call and the inference exponential).
+ *
+ * One serving step is, on one CUDA stream:
+ *   flamia_paged_plan    once per step: pages, slots and the attention's work split
+ *   per layer:
+ *     flamia_paged_append  this step's K and V rows into the layer's cache
+ *     flamia_paged_fwd     attention of this step's queries over the cache
+ *
+ * The cache of a layer is a pool of pages; a page holds `page_size`
+ * consecutive tokens of one request for all key/value heads, head-major, so
+ * that one head's tokens of a page are one contiguous run:
+ *   K, V codes  [n_pages][Hkv][page_size][d]   bf16 or E4M3
+ *   scales      [n_pages][Hkv][page_size]      E4M3 only: the UE8M0 byte of
+ *               each (token, head) row, as flamia_quantize's exact option
+ *               writes them: the row's value is code * 2^(byte - 127).  Byte
+ *               255 marks a row that holds a NaN or an infinity: all of it
+ *               reads as NaN.  (A NaN code 0x7F or 0xFF under any other byte is
+ *               not written by flamia_paged_append and must not occur.)
+ * Token j of request r lies in page block_table[r][j / page_size], row
+ * j % page_size; its slot is page * page_size + row.
+ *
+ * Problem description (host struct; pointers are device pointers).
+ *   n_req        requests of the step, 1..8192
+ *   T            rows of the packed per-token tensors (capacity).  Request r
+ *                owns the rows [cu_q[r], cu_q[r+1]) of q, k, v, O and the slot
+ *                map; rows behind cu_q[n_req] <= T belong to no request and
+ *                are neither read nor written (their slots are set to -1).
+ *   max_q        upper bound of a request's new tokens, 1..T (0 selects T).  The
+ *                kernel is chosen by it: up to max_q * H / Hkv = 16 rows a
+ *                (request, key/value head) take the decode kernel.
+ *   H, Hkv, d    query heads, key/value heads (H % Hkv == 0), head dimension
+ *                64 or 128
+ *   page_size    16, 32, 64 or 128
+ *   n_pages      pages of the pool; n_pages * page_size < 2^31
+ *   max_pages    columns of the block table
+ *   cache_dtype  FLAMIA_BF16 or FLAMIA_E4M3
+ *   in_dtype     dtype of the K and V rows given to flamia_paged_append:
+ *                FLAMIA_BF16 or FLAMIA_F32
+ *   causal       1: new token i of a request, at position kv_len - q_len + i,
+ *                sees the keys up to its own position; 0: all kv_len keys
+ *   softmax_scale  0 selects 1/sqrt(d)
+ *   cu_q         int32 [n_req + 1], cu_q[0] = 0, non-decreasing
+ *   kv_len       int32 [n_req]: the request's cached tokens after this step,
+ *                its new ones included.  A request may have new tokens and
+ *                kv_len 0 (an inactive slot of a captured batch), or fewer
+ *                cached than new ones: rows without a key get O = 0 and
+ *                lse = -inf, and slot -1.
+ *   block_table  int32 [n_req][max_pages]; entries past a request's pages
+ *                are not read
+ *   q_stride, kv_stride  elements between two tokens' rows of q (and of k and
+ *                v): 0 selects contiguous rows (H * d, Hkv * d); otherwise at
+ *                least that, and a multiple of 16 bytes, so rows of a fused
+ *                QKV projection can be passed in place
+ * Conventions as above (16-byte alignment; the int32 arrays 4-byte).  cu_q,
+ * kv_len and block_table must not change between flamia_paged_plan and the
+ * last launch that uses its workspace.  One workspace serves one step at a
+ * time: launches that may overlap (other streams, other graphs) need one each. */
+typedef struct {
+  int32_t n_req, T, max_q, H, Hkv, d;
+  int32_t page_size, n_pages, max_pages;
+  int32_t cache_dtype, in_dtype, causal;
+  float softmax_scale;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int32_t* block_table;
+  int64_t q_stride, kv_stride;
+} flamia_paged_t;
+
+/* One layer's cache (device pointers, caller-owned; k_scales and v_scales
+ * are NULL for bf16).  page_stride: elements between two pages of k and of v
+ * (0: Hkv * page_size * d, contiguous; else at least that, a multiple of 16
+ * bytes), so that K and V pages can be interleaved in one buffer. */
+typedef struct {
+  void* k;
+  void* v;
+  void* k_scales;
+  void* v_scales;
+  int64_t page_stride;
+} flamia_cache_t;
+
+/* Bytes of device workspace for `p` (0 if `p` is invalid). */
+size_t flamia_paged_workspace_size(const flamia_paged_t* p);
+
+/* Builds, in one launch, the step's block tables, slot map and attention
+ * work split from the request lengths.  Clears the workspace's status word.
+ *
+ * Page management (old_len not NULL): request r held ceil(old_len[r] /
+ * page_size) pages and needs ceil(kv_len[r] / page_size).  With
+ * S = free_pages[0 .. *n_free) followed by the pages that shrinking requests
+ * give back (request order, then table order), growing requests take pages
+ * from the end of S (request order, then table order) and their new table
+ * entries are written; what is left of S stays in free_pages and its length
+ * goes to *n_free_out.  So a finished request passes kv_len 0, one whose
+ * drafted tokens were rejected a smaller kv_len.  Pages must belong to one
+ * request only.  Table entries outside the taken pages are not written.
+ *   old_len     int32 [n_req]
+ *   free_pages  int32 [n_pages] stack of free page ids
+ *   n_free, n_free_out  int32 [1]; may be the same word
+ * If old_len is NULL, so must these three be: the table is used as it is.
+ *
+ * slot_map (may be NULL): int32 [T], the slot of each new token, -1 for rows
+ * behind cu_q[n_req] and for positions below 0.
+ *
+ * Device-side conditions, all checked before anything is written:
+ * FLAMIA_ERR_BAD_SEQLENS (cu_q, old_len or kv_len inconsistent, more than
+ * max_q new tokens or more than max_pages pages), FLAMIA_ERR_BAD_PAGE (*n_free
+ * outside [0, n_pages], or more pages given back than the stack has room
+ * for), FLAMIA_ERR_NO_PAGES (fewer pages than the step needs).  Then no page
+ * moves, *n_free_out = *n_free, every slot is -1, and launches that use the
+ * workspace write nothing.  A new token whose page id (of the table or the
+ * stack) lies outside [0, n_pages) gets slot -2, which flamia_paged_append
+ * reports. */
+flamia_status_t flamia_paged_plan(const flamia_paged_t* p, int32_t* slot_map, const int32_t* old_len,
+                                  int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream);
+
+/* Writes the step's K and V rows (in_dtype, [T][Hkv][d], kv_stride) into
+ * their slots: rounded to bf16, or as E4M3 codes with the row's no-clamp
+ * exponent (the smallest e with max|x| <= 448 2^e, clamped to [-127, 127]; 0
+ * for a zero row), byte for byte those of flamia_quantize with `exact` for
+ * finite rows.  A slot of -1 skips the row; slots must be distinct.  Any
+ * other slot outside the pool is skipped and sets FLAMIA_ERR_BAD_PAGE.  Requires
+ * flamia_paged_plan on the same workspace. */
+flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, const void* v, const int32_t* slot_map,
+                                    const flamia_cache_t* cache, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Attention of the step's queries over the cache: with x_ij = softmax_scale
+ * <q_i, k_j> over the keys j that row i sees,
+ *   O_i = sum_j exp(x_ij - lse_i) v_j,   lse_i = ln sum_j exp(x_ij).
+ * Query head h reads key/value head h / (H / Hkv).  Scores, softmax
+ * statistics and accumulators are fp32; the weights are rounded to bf16 for
+ * the P V product (decode kernel: to two bf16 terms).
+ *   q    device bf16 [T][H][d] (q_stride)
+ *   O    device bf16 [T][H][d], contiguous
+ *   lse  device float [H][T], natural logarithm (may be NULL)
+ * A table entry outside [0, n_pages) sets FLAMIA_ERR_BAD_PAGE and leaves the
+ * request's O and lse undefined; nothing outside the pool is read.  Requires
+ * flamia_paged_plan on the same workspace; results do not depend on anything
+ * else the workspace held. */
+flamia_status_t flamia_paged_fwd(const flamia_paged_t* p, const void* q, const flamia_cache_t* cache, void* O,
+                                 float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Static description of a status code. */
 const char* flamia_status_string(flamia_status_t s);

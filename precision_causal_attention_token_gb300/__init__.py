@@ -15,16 +15,19 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libflamia.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE_TOO_SMALL, ERR_CUDA, ERR_TIMEOUT, ERR_BAD_SEQLENS = range(7)
+ERR_NO_PAGES, ERR_BAD_PAGE = 7, 8
 PATH_MXFP8, PATH_NVFP4_FP8 = 0, 1
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 ROLE_QKV, ROLE_DO = 0, 1
 
 EXPORTED = ("flamia_workspace_size", "flamia_plan", "flamia_quantize", "flamia_fwd", "flamia_bwd",
             "flamia_get_device_status", "flamia_clear_device_status", "flamia_status_string",
             "flamia_debug_set_phat_dump", "flamia_debug_withhold_first_item", "flamia_debug_workspace_offset",
-            "flamia_plan_noalloc", "flamia_debug_mma_idesc", "flamia_debug_smem_desc")
+            "flamia_plan_noalloc", "flamia_debug_mma_idesc", "flamia_debug_smem_desc",
+            "flamia_paged_workspace_size", "flamia_paged_plan", "flamia_paged_append", "flamia_paged_fwd")
 WS_FWD_ITEMS, WS_BWD_ITEMS, WS_DQ_PRESCALE = range(3)
 MMA_F8F6F4, MMA_MXF8F6F4, MMA_MXF4NVF4 = range(3)
+MMA_BF16 = 4
 SWZ_NONE, SWZ_128B, SWZ_64B, SWZ_32B = 0, 2, 4, 6
 
 
@@ -46,6 +49,20 @@ class Problem(ctypes.Structure):
 class Operand(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("codes4", ctypes.c_void_p),
                 ("scales4", ctypes.c_void_p), ("gscale4", ctypes.c_void_p)]
+
+
+class Paged(ctypes.Structure):
+    _fields_ = [("n_req", ctypes.c_int32), ("T", ctypes.c_int32), ("max_q", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("cache_dtype", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("kv_stride", ctypes.c_int64)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("page_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -86,6 +103,11 @@ def load_library(path: str = LIB_PATH):
                                          ctypes.POINTER(ctypes.c_uint64)]
     L.flamia_plan_noalloc.restype = i32
     L.flamia_plan_noalloc.argtypes = [P, vp, vp, vp, vp]
+    G, K = ctypes.POINTER(Paged), ctypes.POINTER(Cache)
+    L.flamia_paged_workspace_size.restype, L.flamia_paged_workspace_size.argtypes = sz, [G]
+    L.flamia_paged_plan.restype, L.flamia_paged_plan.argtypes = i32, [G, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.flamia_paged_append.restype, L.flamia_paged_append.argtypes = i32, [G, vp, vp, vp, K, vp, sz, vp]
+    L.flamia_paged_fwd.restype, L.flamia_paged_fwd.argtypes = i32, [G, vp, K, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -201,6 +223,65 @@ def flamia_debug_smem_desc(saddr: int, lbo: int, sbo: int, swizzle: int) -> int:
 
 def flamia_clear_device_status(ws, stream=None):
     _check(load_library().flamia_clear_device_status(_ptr(ws), _stream(stream)), "flamia_clear_device_status")
+
+
+def make_paged(T, H, Hkv, d, cu_q, kv_len, block_table, *, page_size, n_pages, max_q=0, cache_dtype=BF16,
+               in_dtype=BF16, causal=True, softmax_scale=0.0, q_stride=0, kv_stride=0) -> Paged:
+    """One serving step over a paged cache (see include/flamia.h).  cu_q [n_req + 1], kv_len [n_req] and
+    block_table [n_req, max_pages]: contiguous int32 device tensors, kept referenced by the caller."""
+    for t in (cu_q, kv_len, block_table):
+        _int32(t)
+    n_req = kv_len.numel()
+    if cu_q.numel() != n_req + 1 or block_table.dim() != 2 or block_table.shape[0] != n_req:
+        raise ValueError("cu_q must hold n_req + 1 offsets and block_table n_req rows")
+    return Paged(n_req, int(T), int(max_q), int(H), int(Hkv), int(d), int(page_size), int(n_pages),
+                 block_table.shape[1], int(cache_dtype), int(in_dtype), int(bool(causal)), float(softmax_scale),
+                 cu_q.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), int(q_stride), int(kv_stride))
+
+
+def _int32(t, n=None):
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"expected a contiguous int32 tensor{'' if n is None else f' of {n}'}, got {tuple(t.shape)} "
+                         f"{t.dtype}")
+
+
+def paged_cache(k, v, k_scales=None, v_scales=None) -> Cache:
+    """One layer's pool: k, v [n_pages, Hkv, page_size, d] (bf16, or uint8 E4M3 codes with uint8 scales
+    [n_pages, Hkv, page_size]).  Pages may be strided (k = pool[:, 0], v = pool[:, 1]); a page is contiguous."""
+    if k.shape != v.shape or k.stride() != v.stride() or k.dim() != 4 or k.dtype != v.dtype:
+        raise ValueError("k and v must be [n_pages, Hkv, page_size, d] of one type and layout")
+    if k[0].is_contiguous() is False:
+        raise ValueError("the pages of k and v must be contiguous")
+    for s in (k_scales, v_scales):
+        if s is not None and (s.shape != k.shape[:3] or s.element_size() != 1 or not s.is_contiguous()):
+            raise ValueError("scales must be contiguous bytes [n_pages, Hkv, page_size]")
+    stride = k.stride(0) if k.shape[0] > 1 else 0
+    return Cache(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), stride)
+
+
+def flamia_paged_workspace_size(prob: Paged) -> int:
+    return int(load_library().flamia_paged_workspace_size(ctypes.byref(prob)))
+
+
+def flamia_paged_plan(prob: Paged, ws, slot_map=None, old_len=None, free_pages=None, n_free=None, n_free_out=None,
+                      stream=None):
+    """Once per step: block table, free stack, slot map and the attention's work split."""
+    _check(load_library().flamia_paged_plan(ctypes.byref(prob), _ptr(slot_map), _ptr(old_len), _ptr(free_pages),
+                                            _ptr(n_free), _ptr(n_free_out), _ptr(ws), ws.numel() * ws.element_size(),
+                                            _stream(stream)), "flamia_paged_plan")
+
+
+def flamia_paged_append(prob: Paged, k, v, slot_map, cache: Cache, ws, stream=None):
+    _check(load_library().flamia_paged_append(ctypes.byref(prob), _ptr(k), _ptr(v), _ptr(slot_map),
+                                              ctypes.byref(cache), _ptr(ws), ws.numel() * ws.element_size(),
+                                              _stream(stream)), "flamia_paged_append")
+
+
+def flamia_paged_fwd(prob: Paged, q, cache: Cache, O, lse, ws, stream=None):
+    _check(load_library().flamia_paged_fwd(ctypes.byref(prob), _ptr(q), ctypes.byref(cache), _ptr(O), _ptr(lse),
+                                           _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "flamia_paged_fwd")
 
 
 @dataclass

@@ -16,8 +16,9 @@ ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libflamia.so")
-UNITS = ["api.cu", "plan.cu", "quantize.cu", "fwd.cu", "bwd.cu"]
-HEADERS = ["common.cuh", "attn_common.cuh", "kernels.h"]
+UNITS = ["api.cu", "plan.cu", "quantize.cu", "fwd.cu", "bwd.cu", "paged_api.cu", "paged_plan.cu", "paged_append.cu",
+         "paged_decode.cu", "paged_chunk.cu"]
+HEADERS = ["common.cuh", "attn_common.cuh", "kernels.h", "paged.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

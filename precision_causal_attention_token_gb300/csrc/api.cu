@@ -9,6 +9,7 @@
 #include <cudaTypedefs.h>
 
 #include "kernels.h"
+#include "paged.cuh"
 
 using namespace flamia;
 
@@ -158,6 +159,8 @@ const char* flamia_status_string(flamia_status_t s) {
     case FLAMIA_ERR_CUDA: return "CUDA launch error";
     case FLAMIA_ERR_TIMEOUT: return "device wait timed out";
     case FLAMIA_ERR_BAD_SEQLENS: return "cu_seqlens inconsistent with T";
+    case FLAMIA_ERR_NO_PAGES: return "too few free cache pages";
+    case FLAMIA_ERR_BAD_PAGE: return "cache page, slot or free count out of range";
   }
   return "unknown status";
 }
@@ -407,6 +410,10 @@ flamia_status_t flamia_debug_mma_idesc(int32_t kind, uint32_t M, uint32_t N, int
     case FLAMIA_MMA_MXF4NVF4:
       if (a_mn || b_mn || a_sf_id || b_sf_id) return FLAMIA_ERR_INVALID_ARG;
       *out = idesc_mxf4nvf4(M, N);
+      return FLAMIA_OK;
+    case FLAMIA_MMA_BF16:
+      if (a_sf_id || b_sf_id) return FLAMIA_ERR_INVALID_ARG;
+      *out = bf16_idesc(M, N, (uint32_t)a_mn, (uint32_t)b_mn);
       return FLAMIA_OK;
   }
   return FLAMIA_ERR_INVALID_ARG;

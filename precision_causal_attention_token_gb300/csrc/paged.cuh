@@ -1,0 +1,156 @@
+// paged.cuh — what the paged-cache kernels share: parameters, workspace
+// layout, the split of the attention's work, fp8 -> 16-bit conversions.
+#pragma once
+#include "common.cuh"
+
+namespace flamia {
+
+// ---------------------------------------------------------------------------
+// The split of the attention's work.  A tile is up to `rows` query rows (token
+// major, the G = H/Hkv query heads of a key/value head side by side) of one
+// request and one key/value head; its keys are visited in blocks of `blk`.
+// All blocks of all tiles in the order (request, head, tile, block) form one
+// line of `cost` blocks, and worker w (a CTA) takes the blocks
+// [floor(cost w / W), floor(cost (w + 1) / W)).  So the work is even to one
+// block whatever the lengths, a long context is split over as many SMs as
+// there are, and a worker leaves at most two unfinished tiles, whose partial
+// results (fp32) go to its two slots of the workspace: slot 2w for a tile that
+// an earlier worker began, 2w + 1 for one that it begins itself.  The last
+// worker of a tile to finish adds the partials up in worker order, so the
+// result does not depend on who is last.
+// ---------------------------------------------------------------------------
+enum { kPathDecode8 = 0, kPathDecode16 = 1, kPathChunk = 2 };
+constexpr int kDecodeBlk = 64, kChunkBlk = 128, kChunkRows = 256;
+constexpr int kMaxWorkers = 640;
+constexpr int kMaxReq = 8192;
+
+struct PagedHeader {
+  WsHeader base;       // status words first, as flamia_get_device_status reads them
+  int64_t cost;        // blocks in all
+  int32_t ok;          // 1: the plan's inputs were consistent
+  int32_t rows;        // cu_q[n_req]
+  int32_t workers;     // W
+  int32_t n_free_new;  // for a plan whose n_free and n_free_out are one word
+  int32_t pad[10];
+  unsigned int count[2 * kMaxWorkers];  // partials written, per tile (by its first worker) and half
+};
+
+struct ReqRec {
+  int32_t q0, q_len, kv_len, tiles;
+  int64_t base;      // first block of the request on the line
+  int32_t per_head;  // blocks of one head's tiles
+  int32_t pad;
+};
+struct WorkerRec {
+  int32_t r, h, tile, blk;  // where it starts
+  int32_t n;                // its blocks
+  int32_t tile_off;         // blocks of the head's earlier tiles
+  int32_t pad[2];
+};
+
+struct PagedLayout {
+  size_t header, reqs, workers, part_ml, part_o, total;
+  int path, part_rows;
+};
+
+struct PagedParams {
+  int n_req, T, max_q, H, Hkv, G, page_size, page_shift, n_pages, max_pages, causal, path;
+  int W_max;      // workers at most
+  int tile_toks;  // tokens of a tile (kPathChunk)
+  float c_log2;   // softmax_scale * log2(e)
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int32_t* block_table;
+  int64_t q_stride, kv_stride;  // elements
+  PagedHeader* hdr;
+  ReqRec* reqs;
+  WorkerRec* workers;
+  float2* part_ml;  // [2 W][rows] (reference, sum)
+  float* part_o;    // [2 W][rows][d] (decode), [2 W][d / 4][rows][4] (chunk)
+  // plan
+  int32_t* slot_map;
+  const int32_t* old_len;
+  int32_t* free_pages;
+  const int32_t* n_free;
+  int32_t* n_free_out;
+  // append, forward
+  const void* k_new;
+  const void* v_new;
+  const int32_t* slots;
+  const __nv_bfloat16* q;
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int64_t page_bytes;  // between pages of k (and of v)
+  __nv_bfloat16* O;
+  float* lse;
+};
+
+cudaError_t launch_paged_plan(const PagedParams& p, cudaStream_t st);
+cudaError_t launch_paged_append(const PagedParams& p, int d, bool e4m3, bool in_bf16, int sms, cudaStream_t st);
+cudaError_t launch_paged_decode(const PagedParams& p, int d, bool e4m3, cudaStream_t st);
+cudaError_t launch_paged_chunk(const PagedParams& p, int d, bool e4m3, const CUtensorMap& mk, const CUtensorMap& mv,
+                               cudaStream_t st);
+// Workers of a launch on a GPU with `sms` SMs: what the kernel keeps resident.
+int paged_decode_workers(int sms, int path);
+
+// Keys that the rows of tokens [.., tok] of a request see (tok: its last token).
+__host__ __device__ __forceinline__ int visible_keys(int causal, int q_len, int kv_len, int tok) {
+  if (!causal) return kv_len;
+  const int n = kv_len - q_len + tok + 1;
+  return n < 0 ? 0 : n;
+}
+
+// Worker that owns block x of a line of `cost` blocks split over W.
+__device__ __forceinline__ int worker_of(int64_t x, int64_t cost, int W) { return (int)(((x + 1) * W - 1) / cost); }
+
+// 2^(b - 127) for a UE8M0 byte: b = 0 is subnormal, 255 is NaN.
+__device__ __forceinline__ float ue8m0(uint32_t b) {
+  return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23);
+}
+
+// Two E4M3FN codes (low byte first) -> f16x2, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
+  return r;
+}
+// Two E4M3 codes in bits 8-15 and 24-31 of `t` -> bf16x2 values times 2^-120
+// (other bits of t are ignored).  The code's exponent and mantissa moved to
+// the top of bf16's exponent field's low end keep their meaning, subnormal
+// codes included, with the bias 127 in place of 7; the caller multiplies by
+// 2^120 times the row's scale, which is exact for every code.
+__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t t) {
+  return ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two fp32 -> bf16x2 (RNE), `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+
+// Instruction descriptor, kind::f16 (bf16 x bf16 -> fp32): c_format (4-5) 1 =
+// F32, a_format (7-9) and b_format (10-12) 1 = BF16, a_major (15), b_major
+// (16), N >> 3 in 17-22, M >> 4 in 24-28.
+__host__ __device__ constexpr uint32_t bf16_idesc(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ float lg2_f(float x) { return __log2f(x); }
+
+}  // namespace flamia

@@ -1,0 +1,201 @@
+// paged_api.cu — the C ABI of serving from a paged cache (include/flamia.h):
+// host-side validation, workspace layout, TMA descriptors and launches.
+#include <cmath>
+#include <cudaTypedefs.h>
+
+#include "kernels.h"
+#include "paged.cuh"
+
+using namespace flamia;
+
+namespace {
+
+constexpr int kChunkMaxWorkers = 160;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool dev16(const void* p) { return p && aligned(p, 16); }
+bool dev4(const void* p) { return p && aligned(p, 4); }
+
+int max_q_of(const flamia_paged_t* p) { return p->max_q ? p->max_q : p->T; }
+
+// Up to 16 query rows of a key/value head: the decode kernel, whose MMAs have
+// 8 or 16 columns for them and which is bound by the cache's bytes alone.
+// More rows: 256-row tiles on the tensor cores.
+int path_of(const flamia_paged_t* p) {
+  const int64_t rows = (int64_t)max_q_of(p) * (p->H / p->Hkv);
+  return rows <= 8 ? kPathDecode8 : rows <= 16 ? kPathDecode16 : kPathChunk;
+}
+
+flamia_status_t validate(const flamia_paged_t* p) {
+  if (!p) return FLAMIA_ERR_INVALID_ARG;
+  if (p->n_req < 1 || p->T < 1 || p->H < 1 || p->Hkv < 1 || p->max_q < 0 || p->max_q > p->T || p->n_pages < 1 ||
+      p->max_pages < 1 || p->H % p->Hkv != 0 || !dev4(p->cu_q) || !dev4(p->kv_len) || !dev4(p->block_table))
+    return FLAMIA_ERR_INVALID_ARG;
+  if (p->d != 64 && p->d != 128) return FLAMIA_ERR_UNSUPPORTED;
+  if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) return FLAMIA_ERR_UNSUPPORTED;
+  if (p->cache_dtype != FLAMIA_BF16 && p->cache_dtype != FLAMIA_E4M3) return FLAMIA_ERR_UNSUPPORTED;
+  if (p->in_dtype != FLAMIA_BF16 && p->in_dtype != FLAMIA_F32) return FLAMIA_ERR_UNSUPPORTED;
+  if (p->n_req > kMaxReq || p->T > (1 << 30) || p->H / p->Hkv > kChunkRows) return FLAMIA_ERR_UNSUPPORTED;
+  if ((int64_t)p->T * p->H * p->d >= (int64_t)1 << 40) return FLAMIA_ERR_UNSUPPORTED;
+  if ((int64_t)p->n_pages * p->page_size > INT32_MAX || (int64_t)p->max_pages * p->page_size > INT32_MAX ||
+      (int64_t)p->n_req * p->max_pages > INT32_MAX)
+    return FLAMIA_ERR_UNSUPPORTED;
+  if (!(p->softmax_scale >= 0.f) || std::isinf(p->softmax_scale)) return FLAMIA_ERR_INVALID_ARG;
+  const int64_t kv_el = p->in_dtype == FLAMIA_BF16 ? 8 : 4;  // elements of 16 bytes
+  if (p->q_stride && (p->q_stride < (int64_t)p->H * p->d || p->q_stride % 8)) return FLAMIA_ERR_INVALID_ARG;
+  if (p->kv_stride && (p->kv_stride < (int64_t)p->Hkv * p->d || p->kv_stride % kv_el)) return FLAMIA_ERR_INVALID_ARG;
+  return FLAMIA_OK;
+}
+
+PagedLayout layout(const flamia_paged_t& p) {
+  PagedLayout L{};
+  L.path = path_of(&p);
+  L.part_rows = L.path == kPathDecode8 ? 8 : L.path == kPathDecode16 ? 16 : kChunkRows;
+  const size_t slots = 2 * (size_t)(L.path == kPathChunk ? kChunkMaxWorkers : kMaxWorkers);
+  auto a256 = [](size_t x) { return (x + 255) & ~size_t(255); };
+  size_t o = 0;
+  L.header = o; o = a256(o + sizeof(PagedHeader));
+  L.reqs = o; o = a256(o + sizeof(ReqRec) * p.n_req);
+  L.workers = o; o = a256(o + sizeof(WorkerRec) * kMaxWorkers);
+  L.part_ml = o; o = a256(o + sizeof(float2) * slots * L.part_rows);
+  L.part_o = o; o = a256(o + sizeof(float) * slots * L.part_rows * p.d);
+  L.total = o;
+  return L;
+}
+
+flamia_status_t fill(const flamia_paged_t* p, void* ws, size_t ws_bytes, PagedParams* a) {
+  flamia_status_t s = validate(p);
+  if (s != FLAMIA_OK) return s;
+  const PagedLayout L = layout(*p);
+  if (!dev16(ws)) return FLAMIA_ERR_INVALID_ARG;
+  if (ws_bytes < L.total) return FLAMIA_ERR_WORKSPACE_TOO_SMALL;
+  *a = PagedParams{};
+  a->n_req = p->n_req;
+  a->T = p->T;
+  a->max_q = max_q_of(p);
+  a->H = p->H;
+  a->Hkv = p->Hkv;
+  a->G = p->H / p->Hkv;
+  a->page_size = p->page_size;
+  a->page_shift = p->page_size == 16 ? 4 : p->page_size == 32 ? 5 : p->page_size == 64 ? 6 : 7;
+  a->n_pages = p->n_pages;
+  a->max_pages = p->max_pages;
+  a->causal = p->causal != 0;
+  a->path = L.path;
+  const int sms = sm_count();
+  const int w = L.path == kPathChunk ? sms : paged_decode_workers(sms, L.path);
+  const int cap = L.path == kPathChunk ? kChunkMaxWorkers : kMaxWorkers;
+  a->W_max = w < cap ? w : cap;
+  a->tile_toks = kChunkRows / a->G;
+  const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)p->d);
+  a->c_log2 = scale * 1.44269504088896341f;
+  a->cu_q = p->cu_q;
+  a->kv_len = p->kv_len;
+  a->block_table = p->block_table;
+  a->q_stride = p->q_stride ? p->q_stride : (int64_t)p->H * p->d;
+  a->kv_stride = p->kv_stride ? p->kv_stride : (int64_t)p->Hkv * p->d;
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  a->hdr = reinterpret_cast<PagedHeader*>(b + L.header);
+  a->reqs = reinterpret_cast<ReqRec*>(b + L.reqs);
+  a->workers = reinterpret_cast<WorkerRec*>(b + L.workers);
+  a->part_ml = reinterpret_cast<float2*>(b + L.part_ml);
+  a->part_o = reinterpret_cast<float*>(b + L.part_o);
+  return FLAMIA_OK;
+}
+
+flamia_status_t fill_cache(const flamia_paged_t* p, const flamia_cache_t* c, PagedParams* a) {
+  if (!c || !dev16(c->k) || !dev16(c->v)) return FLAMIA_ERR_INVALID_ARG;
+  const bool e4m3 = p->cache_dtype == FLAMIA_E4M3;
+  if (e4m3 ? !dev16(c->k_scales) || !dev16(c->v_scales) : c->k_scales || c->v_scales) return FLAMIA_ERR_INVALID_ARG;
+  const int64_t page = (int64_t)p->Hkv * p->page_size * p->d, el = e4m3 ? 1 : 2;
+  if (c->page_stride && (c->page_stride < page || c->page_stride * el % 16)) return FLAMIA_ERR_INVALID_ARG;
+  a->page_bytes = (c->page_stride ? c->page_stride : page) * el;
+  a->k = static_cast<uint8_t*>(c->k);
+  a->v = static_cast<uint8_t*>(c->v);
+  a->k_scales = static_cast<uint8_t*>(c->k_scales);
+  a->v_scales = static_cast<uint8_t*>(c->v_scales);
+  return FLAMIA_OK;
+}
+
+// 4-D map over bf16 pages [n_pages][Hkv][page_size][d]: box = one page and
+// head, 64 channels (128 bytes, 128B swizzle).
+bool make_pages_map(CUtensorMap* m, void* ptr, const flamia_paged_t* p, int64_t page_bytes) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return false;
+    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }
+  cuuint64_t dims[4] = {(cuuint64_t)p->d, (cuuint64_t)p->page_size, (cuuint64_t)p->Hkv, (cuuint64_t)p->n_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)p->d * 2, (cuuint64_t)p->page_size * p->d * 2, (cuuint64_t)page_bytes};
+  cuuint32_t box[4] = {64, (cuuint32_t)p->page_size, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+flamia_status_t of(cudaError_t e) { return e == cudaSuccess ? FLAMIA_OK : FLAMIA_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+size_t flamia_paged_workspace_size(const flamia_paged_t* p) { return validate(p) == FLAMIA_OK ? layout(*p).total : 0; }
+
+flamia_status_t flamia_paged_plan(const flamia_paged_t* p, int32_t* slot_map, const int32_t* old_len, int32_t* free_pages,
+                                  const int32_t* n_free, int32_t* n_free_out, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream) {
+  PagedParams a;
+  flamia_status_t s = fill(p, ws, ws_bytes, &a);
+  if (s != FLAMIA_OK) return s;
+  const bool manage = old_len || free_pages || n_free || n_free_out;
+  if (manage && (!dev4(old_len) || !dev4(free_pages) || !dev4(n_free) || !dev4(n_free_out))) return FLAMIA_ERR_INVALID_ARG;
+  if (!aligned(slot_map, 4)) return FLAMIA_ERR_INVALID_ARG;
+  a.slot_map = slot_map;
+  a.old_len = old_len;
+  a.free_pages = free_pages;
+  a.n_free = n_free;
+  // every CTA of the launch reads *n_free: a result for the same word goes
+  // through the workspace
+  const bool same = manage && n_free == n_free_out;
+  a.n_free_out = same ? &a.hdr->n_free_new : n_free_out;
+  cudaError_t e = launch_paged_plan(a, stream);
+  if (e == cudaSuccess && same) e = cudaMemcpyAsync(n_free_out, a.n_free_out, sizeof(int32_t), cudaMemcpyDeviceToDevice, stream);
+  return of(e);
+}
+
+flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, const void* v, const int32_t* slot_map,
+                                    const flamia_cache_t* cache, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  PagedParams a;
+  flamia_status_t s = fill(p, ws, ws_bytes, &a);
+  if (s != FLAMIA_OK) return s;
+  if ((s = fill_cache(p, cache, &a)) != FLAMIA_OK) return s;
+  if (!dev16(k) || !dev16(v) || !dev4(slot_map)) return FLAMIA_ERR_INVALID_ARG;
+  a.k_new = k;
+  a.v_new = v;
+  a.slots = slot_map;
+  return of(launch_paged_append(a, p->d, p->cache_dtype == FLAMIA_E4M3, p->in_dtype == FLAMIA_BF16, sm_count(), stream));
+}
+
+flamia_status_t flamia_paged_fwd(const flamia_paged_t* p, const void* q, const flamia_cache_t* cache, void* O, float* lse,
+                                 void* ws, size_t ws_bytes, cudaStream_t stream) {
+  PagedParams a;
+  flamia_status_t s = fill(p, ws, ws_bytes, &a);
+  if (s != FLAMIA_OK) return s;
+  if ((s = fill_cache(p, cache, &a)) != FLAMIA_OK) return s;
+  if (!dev16(q) || !dev16(O) || !aligned(lse, 4)) return FLAMIA_ERR_INVALID_ARG;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.O = static_cast<__nv_bfloat16*>(O);
+  a.lse = lse;
+  const bool e4m3 = p->cache_dtype == FLAMIA_E4M3;
+  if (a.path != kPathChunk) return of(launch_paged_decode(a, p->d, e4m3, stream));
+  CUtensorMap mk{}, mv{};
+  if (!e4m3 && (!make_pages_map(&mk, a.k, p, a.page_bytes) || !make_pages_map(&mv, a.v, p, a.page_bytes)))
+    return FLAMIA_ERR_CUDA;
+  return of(launch_paged_chunk(a, p->d, e4m3, mk, mv, stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,661 @@
+// paged_chunk.cu — attention of a chunk of new tokens over a paged cache on
+// the tensor cores: S = Q K^T and O += P V as tcgen05 kind::f16 MMAs in bf16
+// with fp32 accumulators in tensor memory.
+//
+// A CTA works on tiles of up to 256 query rows (two halves of 128, one per
+// TMEM lane) against 128-key blocks of one key/value head: the rows are the
+// tokens of the chunk times the G = H / Hkv heads that share that head, so a
+// K/V block is fetched once for all of them.  Per block and half the tensor
+// cores need 2 x 128 x 128 x d multiply-adds, the softmax 128 x 128
+// exponentials; the halves alternate, so one half's products run under the
+// other half's softmax.  Warp roles (512 threads, one CTA per SM):
+//   warps 0-3, 4-7  softmax of half 0 and 1: a thread owns a row.  It reads
+//              the row's 128 scores from tensor memory, masks, moves its
+//              reference when a score passes it by 2^8 (then it rescales the
+//              row's accumulator), and writes the weights back as bf16 over
+//              the scores, from where the P V product reads them as its A
+//              operand: P never touches shared memory.
+//   warps 8-11 loaders: the tile's queries (any row stride and G) into
+//              swizzled shared memory.  E4M3: also each block's codes from
+//              the raw ring into bf16 tiles, times the row's scale (exact).
+//              They put zeros in rows past the request's last key, where
+//              pages hold what an earlier owner left: 0 x NaN is NaN.
+//   warp 12    producer: the block's pages, one copy per page and 64 channels
+//              (bf16, TMA into the swizzled tile) or one per page (E4M3 codes
+//              and scale bytes, into the raw ring).
+//   warp 13    MMA issuer.
+//   warp 14    scheduler: the worker's tiles (the plan's split).
+// The row's weights are rounded to bf16 once (2^-9 relative); sums use the
+// unrounded ones.
+#include "paged.cuh"
+
+namespace flamia {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr uint32_t kRegSoftmax = 192, kRegLoad = 80, kRegCtl = 48;
+static_assert(256 * kRegSoftmax + 128 * kRegLoad + 128 * kRegCtl <= kThreads * 128, "register split");
+constexpr int kWarpProd = 12, kWarpMma = 13, kWarpSched = 14;
+constexpr int kFragRing = 2;
+constexpr int kFragConsumers = 8 + 4 + 1 + 1;  // warps that read a fragment
+constexpr uint32_t kColS = 0, kColO = 256;     // half h: + 128 h
+
+// One worker's share of one tile.
+struct Frag {
+  int r, h, tile, kb0;       // first key block
+  int n0, n1;                // blocks of each half
+  int load;                  // blocks fetched: the larger
+  int q0, q_len, kv_len, tok0, rows;
+  int whole, starts, w0, parts;  // parts: workers that share the tile
+  int end;
+};
+
+template <int D, bool FP8>
+struct Cfg {
+  static constexpr int kTileB = 128 * D * 2;        // bytes of a bf16 tile of 128 rows
+  static constexpr int kStages = FP8 ? 4 : 5;       // K/V tiles
+  static constexpr int kRaw = FP8 ? 2 : 0;          // raw E4M3 tiles
+  static constexpr int kRawB = 128 * D;
+};
+
+template <int D, bool FP8>
+struct __align__(1024) Tiles {
+  uint8_t q[2 * Cfg<D, FP8>::kTileB];
+  uint8_t kv[Cfg<D, FP8>::kStages][Cfg<D, FP8>::kTileB];
+  uint8_t raw[FP8 ? Cfg<D, FP8>::kRaw : 1][FP8 ? Cfg<D, FP8>::kRawB : 16];
+};
+
+struct Ctl {
+  uint8_t scales[2][128];  // raw ring: scale bytes
+  uint64_t q_full, q_empty, kv_full[5], kv_empty[5], raw_full[2], raw_empty[2];
+  uint64_t s_full[2], p_full[2], o_full[2], fix, wg[2];
+  uint64_t f_full[kFragRing], f_empty[kFragRing];
+  Frag frag[kFragRing];
+  int last[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int D, bool FP8>
+constexpr size_t smem_bytes() { return sizeof(Tiles<D, FP8>) + sizeof(Ctl) + 1024; }
+
+// D[tmem] (+)= A[smem] * B[smem], bf16, fp32 accumulate.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// A from tensor memory: row m at lane m, two bf16 a column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// S[half] = Q[half] K^T: both K-major, 128-byte swizzled rows of 64 channels.
+template <int D>
+__device__ __forceinline__ void issue_s(uint32_t d, const uint8_t* q, const uint8_t* k) {
+  const uint32_t qa = smem_u32(q), ka = smem_u32(k);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (kk / 4) * 128 * 128 + (kk % 4) * 32;
+    mma_ss(d, smem_desc(qa + off, 16, 1024, kSwz128), smem_desc(ka + off, 16, 1024, kSwz128), bf16_idesc(128, 128, 0, 0), kk > 0);
+  }
+}
+// O[half] += P[half] V: P in tensor memory, V's rows are keys (MN-major B):
+// 64 channels a 128-byte row, the next 64 channels 16 KB on (leading
+// offset), the next 8 keys 1 KB on (stride offset).
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, const uint8_t* v, bool acc) {
+  const uint32_t va = smem_u32(v);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts(d, pcol + 8 * kk, smem_desc(va + kk * 16 * 128, 128 * 128, 1024, kSwz128), bf16_idesc(128, D, 0, 1), acc || kk > 0);
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_chunk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  using C = Cfg<D, FP8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_base_1k(smem_raw);
+  Tiles<D, FP8>& tl = *reinterpret_cast<Tiles<D, FP8>*>(base);
+  Ctl& c = *reinterpret_cast<Ctl*>(base + sizeof(Tiles<D, FP8>));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  WsHeader* hdr = &p.hdr->base;
+  volatile int* abort_flag = &c.abort_flag;
+  if (!p.hdr->ok || (int)blockIdx.x >= p.hdr->workers) return;
+
+  if (tid == 0) {
+    mbar_init(&c.q_full, 128);
+    mbar_init(&c.q_empty, 1);
+    for (int s = 0; s < 5; ++s) {
+      mbar_init(&c.kv_full[s], FP8 ? 128 : 1);
+      mbar_init(&c.kv_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&c.raw_full[s], 1);
+      mbar_init(&c.raw_empty[s], 128);
+      mbar_init(&c.s_full[s], 1);
+      mbar_init(&c.p_full[s], 128);
+      mbar_init(&c.o_full[s], 1);
+      mbar_init(&c.wg[s], 128);
+    }
+    mbar_init(&c.fix, 128);
+    for (int s = 0; s < kFragRing; ++s) {
+      mbar_init(&c.f_full[s], 1);
+      mbar_init(&c.f_empty[s], kFragConsumers);
+    }
+    c.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(&c.tmem_base, 512);
+  if (!FP8 && warp == kWarpProd && lane == 0) {
+    prefetch_tensormap(&map_k);
+    prefetch_tensormap(&map_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = c.tmem_base;
+  // a warp's next fragment (lane 0 frees the slot once all lanes have read it)
+  auto next_frag = [&](uint32_t n, Frag& f, bool& ok, uint32_t where) {
+    const int s = n % kFragRing;
+    if (!(ok = mbar_wait_warp(&c.f_full[s], (n / kFragRing) & 1, abort_flag, hdr, where))) return false;
+    f = c.frag[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.f_empty[s]);
+    return !f.end;
+  };
+
+  if (warp >= 12) {
+    setmaxnreg_dec<kRegCtl>();
+    if (warp == kWarpSched && lane == 0) {
+      // ------------------------------------------------------------ scheduler
+      const int64_t cost = p.hdr->cost;
+      const int W = p.hdr->workers, w = blockIdx.x;
+      const WorkerRec rec = p.workers[w];
+      int left = rec.n, r = rec.r, h = rec.h, tile = rec.tile, blk = rec.blk, off = rec.tile_off;
+      bool ok = true;
+      for (uint32_t n = 0; ok; ++n) {
+        const int s = n % kFragRing;
+        if (!(ok = mbar_wait(&c.f_empty[s], ((n / kFragRing) & 1) ^ 1, abort_flag, hdr, 0x801))) break;
+        Frag& f = c.frag[s];
+        if (left <= 0) {
+          f.end = 1;
+          mbar_arrive(&c.f_full[s]);
+          break;
+        }
+        ReqRec rq = p.reqs[r];
+        while (rq.tiles == 0) rq = p.reqs[++r];  // no new tokens
+        const int tok0 = tile * p.tile_toks, toks = min(p.tile_toks, rq.q_len - tok0), rows = toks * p.G;
+        int nb[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int last = min(toks - 1, (128 * hf + 127) / p.G);  // last token of the half
+          nb[hf] = 128 * hf < rows
+                       ? (visible_keys(p.causal, rq.q_len, rq.kv_len, tok0 + last) + kChunkBlk - 1) / kChunkBlk : 0;
+        }
+        const int all = max(1, max(nb[0], nb[1])), take = min(left, all - blk);
+        f.r = r;
+        f.h = h;
+        f.tile = tile;
+        f.kb0 = blk;
+        f.n0 = max(0, min(nb[0], blk + take) - blk);
+        f.n1 = max(0, min(nb[1], blk + take) - blk);
+        f.load = max(f.n0, f.n1);
+        f.q0 = rq.q0;
+        f.q_len = rq.q_len;
+        f.kv_len = rq.kv_len;
+        f.tok0 = tok0;
+        f.rows = rows;
+        f.whole = take == all;
+        f.starts = blk == 0;
+        f.w0 = f.parts = 0;
+        if (!f.whole) {
+          const int64_t x = rq.base + (int64_t)h * rq.per_head + off;
+          f.w0 = worker_of(x, cost, W);
+          f.parts = worker_of(x + all - 1, cost, W) - f.w0 + 1;
+        }
+        f.end = 0;
+        mbar_arrive(&c.f_full[s]);
+        left -= take;
+        blk = 0;
+        off += all;
+        if (++tile == rq.tiles) {
+          tile = off = 0;
+          if (++h == p.Hkv) {
+            h = 0;
+            ++r;
+          }
+        }
+      }
+    } else if (warp == kWarpProd) {
+      // ------------------------------------------------------------ producer
+      uint32_t it = 0;
+      bool ok = true;
+      Frag f;
+      for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x802); ++n) {
+        const int ps = p.page_size, per = kChunkBlk >> p.page_shift;  // pages of a block (<= 8)
+        const int32_t* table = p.block_table + (int64_t)f.r * p.max_pages;
+        const int pages = (f.kv_len + ps - 1) >> p.page_shift;
+        auto page_at = [&](int blk) {
+          const int k = blk * per + lane;
+          int id = lane < per && k < pages ? __ldg(table + k) : 0;
+          if ((unsigned)id >= (unsigned)p.n_pages) {
+            report(hdr, FLAMIA_ERR_BAD_PAGE, 0x822);
+            id = 0;
+          }
+          return id;
+        };
+        int id = f.load ? page_at(f.kb0) : 0;
+        for (int b = 0; ok && b < f.load; ++b) {
+          const int blk = f.kb0 + b;
+          const int id_next = b + 1 < f.load ? page_at(blk + 1) : 0;
+          const int np = min(per, pages - blk * per);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++it) {
+            if constexpr (FP8) {
+              const int s = it % 2;
+              if (!(ok = mbar_wait_warp(&c.raw_empty[s], ((it / 2) & 1) ^ 1, abort_flag, hdr, 0x803))) break;
+              if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[s], np * ps * (D + 1));
+              __syncwarp();
+              if (lane < np) {
+                bulk_load(tl.raw[s] + lane * ps * D, (kv ? p.v : p.k) + id * p.page_bytes + (int64_t)f.h * ps * D, ps * D,
+                          &c.raw_full[s]);
+                bulk_load(c.scales[s] + lane * ps, (kv ? p.v_scales : p.k_scales) + ((int64_t)id * p.Hkv + f.h) * ps, ps,
+                          &c.raw_full[s]);
+              }
+            } else {
+              const int s = it % C::kStages;
+              if (!(ok = mbar_wait_warp(&c.kv_empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag, hdr, 0x804))) break;
+              if (lane == 0) mbar_arrive_expect_tx(&c.kv_full[s], np * ps * D * 2);
+              __syncwarp();
+              if (lane < np) {
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j)
+                  tma_load_4d(tl.kv[s] + j * 128 * 128 + lane * ps * 128, kv ? &map_v : &map_k, &c.kv_full[s], 64 * j, 0, f.h,
+                              id);
+              }
+            }
+          }
+          id = id_next;
+        }
+      }
+    } else if (warp == kWarpMma) {
+      // ------------------------------------------------------------ MMA issuer
+      uint32_t it = 0, pc[2] = {0, 0}, fixes = 0;
+      bool ok = true;
+      const uint32_t elected = elect_one();
+      Frag f;
+      for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x805); ++n) {
+        const int nh[2] = {f.n0, f.n1};
+        // one thread waits and issues; the warp stays together at the fragment's end
+        if (elected) {
+          do {
+            if (!(ok = mbar_wait(&c.q_full, n & 1, abort_flag, hdr, 0x806))) break;
+            auto full = [&](uint32_t i) {
+              return mbar_wait(&c.kv_full[i % C::kStages], (i / C::kStages) & 1, abort_flag, hdr, 0x807);
+            };
+            if (f.load) {
+              if (!(ok = full(it))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+                if (nh[hf]) {
+                  issue_s<D>(tb + kColS + 128 * hf, tl.q + hf * C::kTileB, tl.kv[it % C::kStages]);
+                  tc_commit(&c.s_full[hf]);
+                }
+              tc_commit(&c.kv_empty[it % C::kStages]);
+            }
+            for (int b = 0; ok && b < f.load; ++b) {
+              const uint32_t vi = it + 2 * b + 1, ki = vi + 1;
+              const uint8_t* vt = tl.kv[vi % C::kStages];
+              const uint8_t* kt = tl.kv[ki % C::kStages];
+              const bool more = b + 1 < f.load;
+              if (!(ok = full(vi))) break;
+              if (!FP8 && (f.kb0 + b + 1) * kChunkBlk > f.kv_len) {  // the loaders clear the rows past the last key
+                if (!(ok = mbar_wait(&c.fix, fixes & 1, abort_flag, hdr, 0x808))) break;
+                ++fixes;
+              }
+              bool k_in = false;
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                if (ok && b < nh[hf]) {
+                  ok = mbar_wait(&c.p_full[hf], pc[hf] & 1, abort_flag, hdr, 0x809);
+                  if (!ok) continue;
+                  ++pc[hf];
+                  tc_fence_after();
+                  issue_pv<D>(tb + kColO + 128 * hf, tb + kColS + 128 * hf, vt, b > 0);
+                  if (b + 1 == nh[hf]) tc_commit(&c.o_full[hf]);
+                }
+                if (ok && b + 1 < nh[hf]) {
+                  if (!k_in) {
+                    ok = full(ki);
+                    if (!ok) continue;
+                    k_in = true;
+                    tc_fence_after();
+                  }
+                  issue_s<D>(tb + kColS + 128 * hf, tl.q + hf * C::kTileB, kt);
+                  tc_commit(&c.s_full[hf]);
+                }
+              }
+              if (!ok) break;
+              tc_commit(&c.kv_empty[vi % C::kStages]);
+              if (more) tc_commit(&c.kv_empty[ki % C::kStages]);
+            }
+            if (!ok) break;
+            tc_commit(&c.q_empty);
+            it += 2 * f.load;
+          } while (false);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+  } else if (warp >= 8) {
+    setmaxnreg_dec<kRegLoad>();
+    // -------------------------------------------------------------- loaders
+    const int lt = tid - 256;
+    uint32_t it = 0;
+    bool ok = true;
+    Frag f;
+    for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x80a); ++n) {
+      if (!(ok = mbar_wait_warp(&c.q_empty, (n & 1) ^ 1, abort_flag, hdr, 0x80b))) break;
+      constexpr int kCh = D / 8;  // 16-byte chunks of a row
+#pragma unroll 4
+      for (int i = lt; i < 256 * kCh; i += 128) {
+        const int row = i / kCh, ch = i % kCh;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < f.rows) {
+          const int tok = row / p.G;
+          x = __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)(f.q0 + f.tok0 + tok) * p.q_stride +
+                                                   (int64_t)(f.h * p.G + row - tok * p.G) * D) + ch);
+        }
+        *reinterpret_cast<uint4*>(tl.q + (row >> 7) * C::kTileB + (ch / 8) * 128 * 128 + sw128_off(row & 127, ch % 8)) = x;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&c.q_full);
+      if constexpr (FP8) {
+        for (int b = 0; ok && b < 2 * f.load; ++b, ++it) {
+          const int rs = it % 2, s = it % C::kStages;
+          const int keys = f.kv_len - (f.kb0 + b / 2) * kChunkBlk;  // rows from here on are cleared
+          if (!(ok = mbar_wait_warp(&c.raw_full[rs], (it / 2) & 1, abort_flag, hdr, 0x80c))) break;
+          if (!(ok = mbar_wait_warp(&c.kv_empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag, hdr, 0x80d))) break;
+          constexpr int kRawCh = D / 16;  // 16-code chunks of a row
+#pragma unroll 2
+          for (int i = lt; i < 128 * kRawCh; i += 128) {
+            const int row = i / kRawCh, ch = i % kRawCh;
+            uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (row < keys) {
+              const uint4 x = *reinterpret_cast<const uint4*>(tl.raw[rs] + row * D + ch * 16);
+              // 2^120 undoes the conversion's bias; a scale above 2^7 is applied in two factors
+              const uint32_t sb = c.scales[rs][row];
+              const uint32_t up = sb == 255u ? 0x7FC0u : (min(sb, 134u) + 120u) << 7;
+              const uint32_t f2 = up * 0x10001u;
+              const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+              uint32_t y[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                y[2 * k] = bf16x2_mul(e4m3_hi_to_bf16x2(prmt(wd[k], 0u, 0x1404u)), f2);
+                y[2 * k + 1] = bf16x2_mul(e4m3_hi_to_bf16x2(prmt(wd[k], 0u, 0x3424u)), f2);
+              }
+              if (sb > 134u && sb != 255u) {
+                const uint32_t f3 = ((sb - 134u + 127u) << 7) * 0x10001u;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = bf16x2_mul(y[k], f3);
+              }
+              out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+              out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+            // the second half of a row's lanes write their chunks in the other
+            // order: the two 64-channel columns share their banks
+            const int flip = D == 128 ? (ch >> 2) & 1 : 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int cc = 2 * ch + (k ^ flip);
+              *reinterpret_cast<uint4*>(tl.kv[s] + (cc / 8) * 128 * 128 + sw128_off(row, cc % 8)) = flip ? out[k ^ 1] : out[k];
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&c.kv_full[s]);
+          mbar_arrive(&c.raw_empty[rs]);
+        }
+      } else {
+        const int lb = f.load - 1, keys = f.kv_len - (f.kb0 + lb) * kChunkBlk;
+        if (f.load && keys < kChunkBlk) {  // V's rows past the last key
+          const uint32_t vi = it + 2 * lb + 1;
+          const int s = vi % C::kStages;
+          if (!(ok = mbar_wait_warp(&c.kv_full[s], (vi / C::kStages) & 1, abort_flag, hdr, 0x80e))) break;
+          for (int i = lt; i < 128 * (D / 8); i += 128) {
+            const int row = i / (D / 8), ch = i % (D / 8);
+            if (row >= keys) *reinterpret_cast<uint4*>(tl.kv[s] + (ch / 8) * 128 * 128 + sw128_off(row, ch % 8)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&c.fix);
+        }
+        it += 2 * f.load;
+      }
+    }
+  } else {
+    setmaxnreg_inc<kRegSoftmax>();
+    // -------------------------------------------------------------- softmax
+    const int hf = warp >> 2, row = tid & 127;
+    const uint32_t ts = taddr(tb, (warp & 3) * 32, kColS + 128 * hf), to = taddr(tb, (warp & 3) * 32, kColO + 128 * hf);
+    uint32_t sc = 0, oc = 0, wgc = 0;
+    bool ok = true;
+    Frag f;
+    for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x810); ++n) {
+      const int R = 128 * hf + row;
+      if (128 * hf >= f.rows) continue;  // the half is empty
+      const int n_blk = hf ? f.n1 : f.n0;
+      const bool row_ok = R < f.rows;
+      const int tok = R / p.G, hq = f.h * p.G + (R - tok * p.G);
+      const int vis = row_ok ? min(f.kv_len, visible_keys(p.causal, f.q_len, f.kv_len, f.tok0 + tok)) : f.kv_len;
+      const int vis_min = __reduce_min_sync(0xffffffffu, vis);
+      float m = -INFINITY, l = 0.f;
+      for (int b = 0; ok && b < n_blk; ++b, ++sc) {
+        if (!(ok = mbar_wait_warp(&c.s_full[hf], sc & 1, abort_flag, hdr, 0x811))) break;
+        tc_fence_after();
+        uint32_t s0[32], s1[32], s2[32], s3[32];
+        tmem_ld32(ts, s0);
+        tmem_ld32(ts + 32, s1);
+        tmem_ld32(ts + 64, s2);
+        tmem_ld32(ts + 96, s3);
+        tmem_ld_wait_regs(s0, s1);
+        tmem_ld_wait_regs(s2, s3);
+        const int key0 = (f.kb0 + b) * kChunkBlk;
+        if (key0 + kChunkBlk > vis_min) {
+          const int nv = vis - key0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j >= nv) s0[j] = 0xFF800000u;
+            if (32 + j >= nv) s1[j] = 0xFF800000u;
+            if (64 + j >= nv) s2[j] = 0xFF800000u;
+            if (96 + j >= nv) s3[j] = 0xFF800000u;
+          }
+        }
+        float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          t0 = fmax3(t0, __uint_as_float(s0[j]), __uint_as_float(s0[j + 1]));
+          t1 = fmax3(t1, __uint_as_float(s1[j]), __uint_as_float(s1[j + 1]));
+          t2 = fmax3(t2, __uint_as_float(s2[j]), __uint_as_float(s2[j + 1]));
+          t3 = fmax3(t3, __uint_as_float(s3[j]), __uint_as_float(s3[j + 1]));
+        }
+        const float top = fmaxf(fmax3(t0, t1, t2), t3) * p.c_log2;
+        const bool up = top > m + 8.f;
+        if (__any_sync(0xffffffffu, up)) {
+          const float a = up ? ex2_approx(m - top) : 1.f;  // 0 from an empty reference
+          if (up) m = top;
+          l *= a;
+          if (b > 0) {  // s_full follows this half's previous P V
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+              uint32_t o[32];
+              tmem_ld32(to + 32 * j, o);
+              tmem_ld_wait_regs(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+              tmem_st32(to + 32 * j, o);
+            }
+          }
+        }
+        const float mref = m == -INFINITY ? 0.f : m;
+        const uint64_t c2 = f2_pack(p.c_log2, p.c_log2), m2 = f2_pack(-mref, -mref);
+        uint64_t sum0 = 0, sum1 = 0;
+        auto weights = [&](uint32_t (&x)[32], uint32_t* out) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float a0, a1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), c2, m2), a0, a1);
+            a0 = ex2_approx(a0);
+            a1 = ex2_approx(a1);
+            if (j & 2) sum1 = f2_add(sum1, f2_pack(a0, a1));
+            else sum0 = f2_add(sum0, f2_pack(a0, a1));
+            out[j / 2] = pack_bf16x2(a0, a1);
+          }
+        };
+        uint32_t w0[32];
+        weights(s0, w0);
+        weights(s1, w0 + 16);
+        tmem_st32(ts, w0);
+        uint32_t w1[32];
+        weights(s2, w1);
+        weights(s3, w1 + 16);
+        tmem_st32(ts + 32, w1);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&c.p_full[hf]);
+        float u0, u1, u2, u3;
+        f2_unpack(sum0, u0, u1);
+        f2_unpack(sum1, u2, u3);
+        l += (u0 + u1) + (u2 + u3);
+      }
+      if (!ok) break;
+      // ------------------------------------------------------------ the row's result
+      float acc[D];
+      if (n_blk) {
+        if (!(ok = mbar_wait_warp(&c.o_full[hf], oc & 1, abort_flag, hdr, 0x812))) break;
+        ++oc;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * j, o);
+          tmem_ld_wait_regs(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) acc[32 * j + k] = __uint_as_float(o[k]);
+        }
+        tc_fence_before();
+      } else {
+#pragma unroll
+        for (int k = 0; k < D; ++k) acc[k] = 0.f;
+      }
+      bool write = f.whole;
+      if (!f.whole) {
+        const int64_t slot = f.starts ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x;
+        float4* po = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * kChunkRows + R;
+#pragma unroll
+        for (int k = 0; k < D / 4; ++k)
+          __stcg(po + k * kChunkRows, make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]));
+        __stcg(p.part_ml + slot * kChunkRows + R, make_float2(m, l));
+        __threadfence();
+        mbar_arrive(&c.wg[hf]);
+        if (!(ok = mbar_wait_warp(&c.wg[hf], wgc & 1, abort_flag, hdr, 0x813))) break;
+        ++wgc;
+        unsigned int* ctr = &p.hdr->count[2 * f.w0 + hf];
+        if (row == 0) {
+          const bool last = atomicAdd(ctr, 1u) == (unsigned)(f.parts - 1);
+          if (last) *ctr = 0;
+          c.last[hf] = last;
+        }
+        mbar_arrive(&c.wg[hf]);
+        if (!(ok = mbar_wait_warp(&c.wg[hf], wgc & 1, abort_flag, hdr, 0x814))) break;
+        ++wgc;
+        write = *reinterpret_cast<volatile int*>(&c.last[hf]) != 0;
+        if (write) {
+          __threadfence();
+          auto slot_of = [&](int i) { return (int64_t)(i == 0 ? 2 * f.w0 + 1 : 2 * (f.w0 + i)); };
+          m = -INFINITY;
+          for (int i = 0; i < f.parts; ++i) m = fmaxf(m, __ldcg(p.part_ml + slot_of(i) * kChunkRows + R).x);
+          l = 0.f;
+#pragma unroll
+          for (int k = 0; k < D; ++k) acc[k] = 0.f;
+          for (int i = 0; i < f.parts; ++i) {
+            const float2 ml = __ldcg(p.part_ml + slot_of(i) * kChunkRows + R);
+            const float a = ml.x == m ? 1.f : ex2_approx(ml.x - m);
+            l += a * ml.y;
+            const float4* src = reinterpret_cast<const float4*>(p.part_o) + slot_of(i) * (D / 4) * kChunkRows + R;
+#pragma unroll
+            for (int k = 0; k < D / 4; ++k) {
+              const float4 x = __ldcg(src + k * kChunkRows);
+              acc[4 * k] += a * x.x;
+              acc[4 * k + 1] += a * x.y;
+              acc[4 * k + 2] += a * x.z;
+              acc[4 * k + 3] += a * x.w;
+            }
+          }
+        }
+      }
+      if (write && row_ok) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays
+        const int64_t t = f.q0 + f.tok0 + tok;
+        uint4* dst = reinterpret_cast<uint4*>(p.O + (t * p.H + hq) * D);
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k)
+          dst[k] = make_uint4(pack_bf16x2(acc[8 * k] * inv, acc[8 * k + 1] * inv), pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
+                              pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv), pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
+        if (p.lse) p.lse[(int64_t)hq * p.T + t] = (m + lg2_f(l)) * 0.69314718055994531f;
+      }
+    }
+  }
+  __syncwarp();  // single-thread roles rejoin their warp
+  tc_fence_before();
+  __syncthreads();
+  drain_after_abort(abort_flag);
+  if (warp == kWarpMma) tmem_dealloc(tb, 512);
+}
+
+template <int D, bool FP8>
+cudaError_t launch(const PagedParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  constexpr size_t smem = smem_bytes<D, FP8>();
+  static_assert(smem <= 232448, "shared memory");
+  using T = Tiles<D, FP8>;
+  static_assert(offsetof(T, kv) % 1024 == 0 && offsetof(T, raw) % 1024 == 0, "tile alignment");
+  static bool attr_set[64] = {};  // per device: raised once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(paged_chunk_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  paged_chunk_kernel<D, FP8><<<p.W_max, kThreads, smem, st>>>(p, mk, mv);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const PagedParams& p, int d, bool e4m3, const CUtensorMap& mk, const CUtensorMap& mv,
+                               cudaStream_t st) {
+  if (d == 128) return e4m3 ? launch<128, true>(p, mk, mv, st) : launch<128, false>(p, mk, mv, st);
+  return e4m3 ? launch<64, true>(p, mk, mv, st) : launch<64, false>(p, mk, mv, st);
+}
+
+}  // namespace flamia

@@ -1,0 +1,295 @@
+// paged_plan.cu — one serving step's pages, slots and attention work split,
+// built on the GPU from the request lengths in one launch.
+//
+// Three prefix sums over the requests (pages taken, pages given back, blocks
+// of attention work) fix everything else, and they are small, so every CTA
+// forms the first two in its own shared memory and nothing is passed between
+// CTAs: page k of the step is the k-th from the end of the free stack, which
+// is a page the step gives back or a word of free_pages, so each thread can
+// tell any new token's page by itself, before the table entry is written.
+// CTA 0 forms the work split; the others share the table entries and slots.
+// The launch moves a few bytes per request and token and is bound by its
+// chain of dependent steps (loads, scan, search, store), not by bandwidth.
+#include "paged.cuh"
+
+namespace flamia {
+
+namespace {
+
+constexpr int kPlanThreads = 512;
+
+__device__ __forceinline__ int pages_of(int len, int shift) { return (len + (1 << shift) - 1) >> shift; }
+
+// Exclusive scan of one 64-bit value per thread; *total: the sum.
+__device__ int64_t block_scan(int64_t v, int64_t* sm, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, s);
+    if (lane >= s) x += y;
+  }
+  if (lane == 31) sm[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = lane < kPlanThreads / 32 ? sm[lane] : 0;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, w, s);
+      if (lane >= s) w += y;
+    }
+    sm[lane] = w;
+  }
+  __syncthreads();
+  *total = sm[31];
+  const int64_t before = warp ? sm[warp - 1] : 0;
+  __syncthreads();
+  return before + x - v;
+}
+
+// The request r with pre[r] <= i < pre[r + 1] (pre[0] = 0 <= i < pre[n]).
+template <typename I>
+__device__ __forceinline__ int find(const I* pre, int n, int64_t i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Blocks of one tile.
+__device__ __forceinline__ int tile_blocks(const PagedParams& p, int q_len, int kv_len, int tile) {
+  if (p.path != kPathChunk) return max(1, (kv_len + kDecodeBlk - 1) / kDecodeBlk);
+  const int last = min(q_len, (tile + 1) * p.tile_toks) - 1;
+  return max(1, (visible_keys(p.causal, q_len, kv_len, last) + kChunkBlk - 1) / kChunkBlk);
+}
+__device__ __forceinline__ int tiles_of(const PagedParams& p, int q_len) {
+  if (p.path != kPathChunk) return q_len > 0;
+  return (q_len + p.tile_toks - 1) / p.tile_toks;
+}
+
+// The work split (one CTA).  pre: [n_req + 1] blocks before each request.
+__device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* pre, int64_t* sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.n_req;
+  constexpr int kSerial = 4;  // tiles that a thread adds up alone; longer chunks take a warp
+  for (int r = tid; r < n; r += kPlanThreads) {
+    const int ql = cu[r + 1] - cu[r], kv = p.kv_len[r], nt = tiles_of(p, ql);
+    int64_t sum = 0;
+    if (nt <= kSerial)
+      for (int i = 0; i < nt; ++i) sum += tile_blocks(p, ql, kv, i);
+    pre[r] = sum;
+  }
+  __syncthreads();
+  if (p.path == kPathChunk) {
+    for (int r = warp; r < n; r += kPlanThreads / 32) {
+      const int ql = cu[r + 1] - cu[r], nt = tiles_of(p, ql);
+      if (nt <= kSerial) continue;
+      const int kv = p.kv_len[r];
+      int64_t sum = 0;
+      for (int i = lane; i < nt; i += 32) sum += tile_blocks(p, ql, kv, i);
+#pragma unroll
+      for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+      if (lane == 0) pre[r] = sum;
+    }
+    __syncthreads();
+  }
+  const int seg = (n + kPlanThreads - 1) / kPlanThreads, r0 = min(n, tid * seg), r1 = min(n, r0 + seg);
+  int64_t mine = 0, cost;
+  for (int r = r0; r < r1; ++r) mine += pre[r] * p.Hkv;
+  int64_t at = block_scan(mine, sm, &cost);
+  for (int r = r0; r < r1; ++r) {
+    const int64_t per_head = pre[r];
+    ReqRec q;
+    q.q0 = cu[r];
+    q.q_len = cu[r + 1] - cu[r];
+    q.kv_len = p.kv_len[r];
+    q.tiles = tiles_of(p, q.q_len);
+    q.base = at;
+    q.per_head = (int)per_head;
+    q.pad = 0;
+    p.reqs[r] = q;
+    pre[r] = at;
+    at += per_head * p.Hkv;
+  }
+  if (tid == 0) pre[n] = cost;
+  __syncthreads();
+  // Fewer workers than fit the GPU where a share would be too small to pay
+  // for joining its partial results.
+  const int64_t share = p.path == kPathChunk ? 2 : 4;
+  const int W = (int)max((int64_t)(cost > 0), min((int64_t)p.W_max, cost / share));
+  if (tid == 0) {
+    p.hdr->cost = cost;
+    p.hdr->workers = W;
+    p.hdr->rows = cu[n];
+  }
+  for (int w = warp; w < W; w += kPlanThreads / 32) {
+    const int64_t x0 = cost * w / W, x1 = cost * (w + 1) / W;
+    const int r = find(pre, n, x0);
+    const int ql = cu[r + 1] - cu[r], kv = p.kv_len[r], nt = tiles_of(p, ql);
+    const int per_head = (int)((pre[r + 1] - pre[r]) / p.Hkv);
+    const int64_t y = x0 - pre[r];
+    WorkerRec rec{};
+    rec.r = r;
+    rec.h = (int)(y / per_head);
+    int z = (int)(y - (int64_t)rec.h * per_head);
+    rec.n = (int)(x1 - x0);
+    // the tile that holds block z of the head: 32 tiles at a time
+    int off = 0;
+    for (int t0 = 0; t0 < nt; t0 += 32) {
+      const int nb = t0 + lane < nt ? tile_blocks(p, ql, kv, t0 + lane) : 0;
+      int incl = nb;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += o;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, off + incl > z);
+      if (hit) {
+        const int k = __ffs(hit) - 1;
+        rec.tile = t0 + k;
+        rec.tile_off = off + __shfl_sync(0xffffffffu, incl - nb, k);
+        break;
+      }
+      off += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    rec.blk = z - rec.tile_off;
+    if (lane == 0) p.workers[w] = rec;
+  }
+}
+
+// smem: cu [n + 1], taken [n + 1], given [n + 1] (int32), pre [n + 1] (int64)
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedParams p) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  __shared__ int64_t sm[32];
+  const int n = p.n_req, tid = threadIdx.x, sh = p.page_shift;
+  int64_t* pre = reinterpret_cast<int64_t*>(raw);
+  int32_t* cu = reinterpret_cast<int32_t*>(pre + (n + 1));
+  int32_t* taken = cu + (n + 1);
+  int32_t* given = taken + (n + 1);
+  const bool manage = p.old_len != nullptr;
+  const bool first = blockIdx.x == 0;
+
+  if (first) {
+    if (tid == 0) {
+      p.hdr->base.status = 0;
+      p.hdr->base.status_where = 0;
+      p.hdr->ok = 0;
+    }
+    for (int i = tid; i < 2 * kMaxWorkers; i += kPlanThreads) p.hdr->count[i] = 0;
+  }
+  // lengths in, checked
+  int bad = 0;
+  for (int i = tid; i <= n; i += kPlanThreads) cu[i] = p.cu_q[i];
+  __syncthreads();
+  const int seg = (n + kPlanThreads - 1) / kPlanThreads, r0 = min(n, tid * seg), r1 = min(n, r0 + seg);
+  if (tid == 0 && (cu[0] != 0 || cu[n] < 0 || cu[n] > p.T)) bad = 1;
+  const int cap = p.max_pages << sh;
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const int ql = cu[r + 1] - cu[r], kv = p.kv_len[r], old = manage ? p.old_len[r] : 0;
+    if (cu[r + 1] < cu[r] || cu[r] < 0 || ql > p.max_q || kv < 0 || kv > cap || old < 0 || old > cap) {
+      bad = 1;
+    } else if (manage) {
+      const int d = pages_of(kv, sh) - pages_of(old, sh);
+      mine += d > 0 ? (int64_t)d << 32 : (int64_t)-d;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  uint32_t why = bad ? FLAMIA_ERR_BAD_SEQLENS : FLAMIA_OK;
+  int n_free = 0, n_taken = 0, n_given = 0;
+  if (manage && !bad) {
+    n_free = *p.n_free;
+    int64_t sum;
+    int64_t at = block_scan(mine, sm, &sum);
+    n_taken = (int)(sum >> 32);
+    n_given = (int)(sum & 0xFFFFFFFF);
+    for (int r = r0; r < r1; ++r) {
+      taken[r] = (int)(at >> 32);
+      given[r] = (int)(at & 0xFFFFFFFF);
+      const int d = pages_of(p.kv_len[r], sh) - pages_of(p.old_len[r], sh);
+      at += d > 0 ? (int64_t)d << 32 : (int64_t)-d;
+    }
+    if (tid == 0) {
+      taken[n] = n_taken;
+      given[n] = n_given;
+    }
+    if (n_free < 0 || n_free > p.n_pages || (int64_t)n_free + n_given > p.n_pages) why = FLAMIA_ERR_BAD_PAGE;
+    else if (n_taken > n_free + n_given) why = FLAMIA_ERR_NO_PAGES;
+  }
+  __syncthreads();
+  const int top = n_free + n_given;
+  if (first) {
+    if (tid == 0) {
+      if (manage) *p.n_free_out = why ? *p.n_free : top - n_taken;
+      if (why) report(&p.hdr->base, why, 0x700);
+    }
+    if (!why) {
+      split_work(p, cu, pre, sm);
+      if (tid == 0) p.hdr->ok = 1;
+    }
+    if (gridDim.x > 1) return;
+  }
+  const int part = gridDim.x > 1 ? (int)blockIdx.x - 1 : 0, parts = max(1, (int)gridDim.x - 1);
+  const int i0 = part * kPlanThreads + tid, step = parts * kPlanThreads;
+  if (why) {
+    if (p.slot_map)
+      for (int t = i0; t < p.T; t += step) p.slot_map[t] = -1;
+    return;
+  }
+  // page k counted from the bottom of the stack S
+  auto given_page = [&](int j) {
+    const int r = find(given, n, j);
+    return p.block_table[(int64_t)r * p.max_pages + pages_of(p.kv_len[r], sh) + (j - given[r])];
+  };
+  auto stack_at = [&](int k) { return k < n_free ? p.free_pages[k] : given_page(k - n_free); };
+  if (manage) {
+    for (int i = i0; i < n_taken; i += step) {
+      const int r = find(taken, n, i);
+      p.block_table[(int64_t)r * p.max_pages + pages_of(p.old_len[r], sh) + (i - taken[r])] = stack_at(top - 1 - i);
+    }
+    for (int j = i0; j < n_given - n_taken; j += step) p.free_pages[n_free + j] = given_page(j);
+  }
+  if (!p.slot_map) return;
+  for (int t = i0; t < p.T; t += step) {
+    int slot = -1;
+    if (t < cu[n]) {
+      const int r = find(cu, n, t);
+      const int pos = p.kv_len[r] - (cu[r + 1] - t);
+      if (pos >= 0) {
+        const int k = pos >> sh, had = manage ? pages_of(p.old_len[r], sh) : 0;
+        const int page = manage && k >= had ? stack_at(top - 1 - (taken[r] + k - had))
+                                            : p.block_table[(int64_t)r * p.max_pages + k];
+        // -2: the append kernel reports it (a report from here could come
+        // before CTA 0 clears the status word)
+        slot = (unsigned)page < (unsigned)p.n_pages ? (page << sh) + (pos & (p.page_size - 1)) : -2;
+      }
+    }
+    p.slot_map[t] = slot;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_plan(const PagedParams& p, cudaStream_t st) {
+  const size_t smem = (size_t)(p.n_req + 1) * (8 + 3 * 4);
+  static bool attr_set[64] = {};  // per device: raised once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kMaxReq + 1) * 20);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  int helpers = 0;
+  if (p.slot_map || p.old_len) {
+    helpers = (p.T + kPlanThreads - 1) / kPlanThreads;
+    if (p.old_len && helpers < (p.n_req + 31) / 32) helpers = (p.n_req + 31) / 32;
+    helpers = helpers < 1 ? 1 : helpers > 151 ? 151 : helpers;
+  }
+  paged_plan_kernel<<<1 + helpers, kPlanThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace flamia

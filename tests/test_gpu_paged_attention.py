@@ -1,0 +1,221 @@
+"""flamia_paged_fwd against plain attention in 64 bits over the same cache."""
+import math
+
+import pytest
+import torch
+
+import precision_causal_attention_token_gb300 as fl
+from paged_ref import Step
+
+pytestmark = pytest.mark.gpu
+
+CACHES = ["bf16", "e4m3"]
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ps", [16, 32, 64, 128])
+def test_decode_lengths(cache, d, ps):
+    """One new token: lengths from one on, around the page, chunk and block edges."""
+    kv = [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 300, 1000]
+    Step([1] * len(kv), kv, H=4, Hkv=2, d=d, ps=ps, cache=cache, seed=ps + d, max_q=1).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (8, 1), (12, 4), (5, 1), (16, 1), (28, 2), (11, 1)])
+def test_decode_head_groups(cache, H, Hkv):
+    Step([1, 1, 1], [70, 333, 5], H=H, Hkv=Hkv, cache=cache, seed=H, max_q=1).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_long_context_is_split(cache, d):
+    """One request over many workers, whose partial results are joined."""
+    Step([1], [20011], H=8, Hkv=2, d=d, ps=64, cache=cache, seed=3, max_q=1).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("causal", [True, False])
+def test_drafted_tokens(cache, causal):
+    """A few new tokens a request, the decode kernel's 16 rows full and not, rows without a key."""
+    Step([4, 1, 3, 2, 4], [200, 1, 3, 1, 77], H=8, Hkv=2, cache=cache, causal=causal, seed=5, max_q=4).check()
+    Step([2, 1, 2], [129, 64, 1], H=4, Hkv=1, d=64, cache=cache, causal=causal, seed=6, max_q=2).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_chunk_lengths(cache, d, causal):
+    """Chunks of many sizes over contexts of many sizes, some rows without a key, one request without tokens."""
+    q = [1, 17, 64, 65, 130, 300, 0, 33, 20]
+    kv = [1, 17, 100, 65, 700, 300, 50, 5, 128]
+    Step(q, kv, H=4, Hkv=2, d=d, ps=16, cache=cache, causal=causal, pad=5, seed=d).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (6, 2), (7, 1), (16, 2), (12, 1), (40, 1)])
+def test_chunk_head_groups(cache, H, Hkv):
+    """Query heads a key/value head: powers of two and not, more than a half tile's worth of heads."""
+    Step([50, 1, 90], [60, 200, 140], H=H, Hkv=Hkv, d=128, ps=32, cache=cache, seed=H).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_chunk_head_group_of_256(cache):
+    Step([3, 1], [60, 200], H=256, Hkv=1, d=64, ps=32, cache=cache, seed=1).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("ps", [16, 32, 64, 128])
+def test_chunk_page_sizes(cache, ps):
+    Step([100, 257, 5], [1000, 300, 129], H=2, Hkv=1, ps=ps, cache=cache, seed=ps).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunk_long_context_is_split(cache, d):
+    """One tile's keys over many workers."""
+    Step([40], [9000], H=8, Hkv=2, d=d, ps=64, cache=cache, seed=9).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_mixed_batch(cache):
+    """Chunks, decoding requests, inactive slots and a padded tail in one call."""
+    q = [1, 150, 1, 1, 64, 1, 1, 1, 0, 1]
+    kv = [500, 150, 0, 77, 1024, 1, 2048, 640, 0, 129]
+    Step(q, kv, H=8, Hkv=2, ps=64, cache=cache, pad=9, seed=2).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_no_keys_at_all(cache, kind):
+    s = Step([1, 1] if kind == "decode" else [20, 30], [0, 0], cache=cache, max_q=1 if kind == "decode" else 0)
+    O, lse = s.run()
+    assert (O == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+@pytest.mark.parametrize("fill", [math.nan, math.inf])
+def test_stale_slots_are_not_read_as_values(cache, kind, fill):
+    """Slots past a request's last token hold what an earlier owner left: NaN and infinities there change nothing."""
+    q, kv = ([1, 1, 1], [1, 130, 77]) if kind == "decode" else ([30, 1, 140], [30, 130, 333])
+    for ps in (16, 128):
+        Step(q, kv, ps=ps, cache=cache, fill=fill, seed=4, max_q=1 if kind == "decode" else 0, pad=2).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_nan_reaches_only_rows_that_see_it(cache, kind):
+    """A NaN key, or a NaN value, of one request makes its rows NaN and no other's."""
+    for which in ("k", "v"):
+        s = Step([1, 1] if kind == "decode" else [20, 30], [50, 60], cache=cache, seed=8,
+                 max_q=1 if kind == "decode" else 0)
+        page, off = s.table_host[0][1], 3  # token 19 of request 0
+        if cache == "bf16":
+            (s.k if which == "k" else s.v)[page, :, off, 5] = math.nan
+        else:
+            (s.ks if which == "k" else s.vs)[page, :, off] = 255
+        O, lse = s.run()
+        n = s.q_len[0]
+        bad = torch.isnan(O[:n])
+        assert bad[..., 5].all() if which == "v" and cache == "bf16" else bad.all()
+        assert torch.isnan(lse[:, :n]).all() if which == "k" else torch.isfinite(lse[:, :n]).all()
+        wO, wl, tO, tl = s.reference(2.0 ** -8)
+        assert ((O[n:].double() - wO[n:]).abs() <= tO[n:]).all() and torch.isfinite(lse[:, n:]).all()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_layouts(cache, kind):
+    """K and V pages interleaved in one buffer, queries as columns of a wider projection, another softmax scale."""
+    q, kv = ([1, 1], [100, 300]) if kind == "decode" else ([40, 130], [100, 300])
+    Step(q, kv, H=4, Hkv=2, ps=32, cache=cache, strided=True, q_extra=2 * 2 * 128, scale=0.05, seed=7,
+         max_q=1 if kind == "decode" else 0).check()
+
+
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_wide_range_of_scales(kind):
+    """E4M3 rows whose exponents span many binades, far above 2^7 too; peaked and flat softmax rows."""
+    s = Step([1, 1] if kind == "decode" else [40, 9], [150, 64], cache="e4m3", seed=11,
+             max_q=1 if kind == "decode" else 0)
+    g = torch.Generator().manual_seed(5)
+    s.vs.copy_(torch.randint(100, 160, s.vs.shape, generator=g, dtype=torch.uint8))
+    s.ks.copy_(torch.randint(110, 124, s.ks.shape, generator=g, dtype=torch.uint8))
+    s.check()
+
+
+def test_results_do_not_depend_on_the_run():
+    """The same call twice gives the same bits (joins happen in a fixed order), whatever the workspace held."""
+    for q, kv, mq in (([1] * 5, [9000, 3, 500, 4000, 77], 1), ([64, 1, 30], [5000, 2000, 3000], 0)):
+        s = Step(q, kv, H=8, Hkv=2, seed=1, max_q=mq)
+        a, la = (x.clone() for x in s.run())
+        for i in range(5):
+            s.ws.fill_(17 * i)
+            b, lb = s.run()
+            assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_captured_step_replays_with_new_lengths():
+    """Plan and forward in a CUDA graph; the lengths change between replays."""
+    s = Step([1, 1, 1], [100, 200, 300], H=8, Hkv=2, max_q=1, seed=3)
+    s.run()
+    torch.cuda.synchronize()
+    O, lse = torch.zeros_like(s.O), torch.zeros_like(s.lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fl.flamia_paged_plan(s.prob, s.ws)
+        fl.flamia_paged_fwd(s.prob, s.q, s.pool, O, lse, s.ws)
+    for kv in ([100, 200, 300], [7, 1, 250], [0, 64, 33]):
+        s.kv_len = kv
+        s.kv.copy_(torch.tensor(kv))
+        graph.replay()
+        s.run()
+        assert torch.equal(O, s.O) and torch.equal(lse, s.lse)
+        s.check()
+
+
+def test_other_streams():
+    """Two steps on two streams, each with its own workspace."""
+    a, b = Step([1, 1], [3000, 70], H=8, Hkv=2, max_q=1, seed=1), Step([90], [500], H=8, Hkv=2, seed=2)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(sa):
+            a.run()
+        with torch.cuda.stream(sb):
+            b.run()
+    torch.cuda.synchronize()
+    got = a.O.clone(), b.O.clone()
+    a.check()
+    b.check()
+    assert torch.equal(got[0], a.O) and torch.equal(got[1], b.O)
+
+
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_bad_page_is_reported(kind):
+    """A table entry outside the pool sets the status word; other requests are served."""
+    s = Step([1, 1] if kind == "decode" else [20, 30], [50, 60], seed=8, max_q=1 if kind == "decode" else 0)
+    for bad in (-1, s.n_pages, 2 ** 31 - 1):
+        s.table[0, 1] = bad
+        O, _ = s.run()
+        torch.cuda.synchronize()
+        assert fl.flamia_get_device_status(s.ws) == fl.ERR_BAD_PAGE
+        s.table[0, 1] = s.table_host[0][1]
+        n = s.q_len[0]
+        wO, _, tO, _ = s.reference(2.0 ** -8)
+        assert ((O[n:].double() - wO[n:]).abs() <= tO[n:]).all()
+
+
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_inconsistent_lengths_write_nothing(kind):
+    for field, at, val in (("cu_q", 0, 1), ("cu_q", 1, 10 ** 6), ("cu_q", 2, -5), ("kv", 0, -1), ("kv", 1, 10 ** 8)):
+        s = Step([1, 1] if kind == "decode" else [20, 30], [50, 60], max_q=1 if kind == "decode" else 0)
+        getattr(s, field)[at] = val
+        O, lse = s.run()
+        torch.cuda.synchronize()
+        assert fl.flamia_get_device_status(s.ws) == fl.ERR_BAD_SEQLENS, (field, at, val)
+        assert (O == 77).all() and (lse == 77).all()
+    s = Step([3, 1], [50, 60], max_q=2)  # more new tokens than max_q
+    O, lse = s.run()
+    torch.cuda.synchronize()
+    assert fl.flamia_get_device_status(s.ws) == fl.ERR_BAD_SEQLENS and (O == 77).all()
