@@ -19,7 +19,10 @@
 //              swizzled shared memory.  E4M3: also each block's codes from
 //              the raw ring into bf16 tiles, times the row's scale (exact).
 //              They put zeros in rows past the request's last key, where
-//              pages hold what an earlier owner left: 0 x NaN is NaN.
+//              pages hold what an earlier owner left: 0 x NaN is NaN.  For
+//              the same reason they take infinities and NaN out of V in the
+//              blocks that some row sees in part, and leave word of the first
+//              such key, so that the rows that do see it get them back.
 //   warp 12    producer: the block's pages, one copy per page and 64 channels
 //              (bf16, TMA into the swizzled tile) or one per page (E4M3 codes
 //              and scale bytes, into the raw ring).
@@ -27,6 +30,8 @@
 //   warp 14    scheduler: the worker's tiles (the plan's split).
 // The row's weights are rounded to bf16 once (2^-9 relative); sums use the
 // unrounded ones.
+#include <climits>
+
 #include "paged.cuh"
 
 namespace flamia {
@@ -37,7 +42,7 @@ constexpr int kThreads = 512;
 constexpr uint32_t kRegSoftmax = 192, kRegLoad = 80, kRegCtl = 48;
 static_assert(256 * kRegSoftmax + 128 * kRegLoad + 128 * kRegCtl <= kThreads * 128, "register split");
 constexpr int kWarpProd = 12, kWarpMma = 13, kWarpSched = 14;
-constexpr int kFragRing = 2;
+constexpr int kFragRing = 2;  // odd_key's four slots go by it
 constexpr int kFragConsumers = 8 + 4 + 1 + 1;  // warps that read a fragment
 constexpr uint32_t kColS = 0, kColO = 256;     // half h: + 128 h
 
@@ -54,8 +59,8 @@ struct Frag {
 template <int D, bool FP8>
 struct Cfg {
   static constexpr int kTileB = 128 * D * 2;        // bytes of a bf16 tile of 128 rows
-  static constexpr int kStages = FP8 ? 4 : 5;       // K/V tiles
-  static constexpr int kRaw = FP8 ? 2 : 0;          // raw E4M3 tiles
+  static constexpr int kStages = FP8 ? 3 : 5;       // K/V tiles
+  static constexpr int kRaw = FP8 ? 4 : 0;          // raw E4M3 tiles
   static constexpr int kRawB = 128 * D;
 };
 
@@ -67,12 +72,13 @@ struct __align__(1024) Tiles {
 };
 
 struct Ctl {
-  uint8_t scales[2][128];  // raw ring: scale bytes
-  uint64_t q_full, q_empty, kv_full[5], kv_empty[5], raw_full[2], raw_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2], fix, wg[2];
+  uint8_t scales[4][128];  // raw ring: scale bytes
+  uint64_t q_full, q_empty, kv_full[5], kv_empty[5], raw_full[4], raw_empty[4];
+  uint64_t s_full[2], p_full[2], o_full[2], fix[5], wg[2];
   uint64_t f_full[kFragRing], f_empty[kFragRing];
   Frag frag[kFragRing];
   int last[2];
+  int odd_key[4];  // per fragment (mod 4): the first key whose V was taken out for not being finite
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -106,6 +112,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
+
+// 16 bytes to shared memory; of them `bytes` (16 or 0) are read, the rest is zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // S[half] = Q[half] K^T: both K-major, 128-byte swizzled rows of 64 channels.
 template <int D>
@@ -147,16 +159,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 5; ++s) {
       mbar_init(&c.kv_full[s], FP8 ? 128 : 1);
       mbar_init(&c.kv_empty[s], 1);
+      mbar_init(&c.fix[s], 128);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&c.raw_full[s], 1);
       mbar_init(&c.raw_empty[s], 128);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&c.s_full[s], 1);
       mbar_init(&c.p_full[s], 128);
       mbar_init(&c.o_full[s], 1);
       mbar_init(&c.wg[s], 128);
     }
-    mbar_init(&c.fix, 128);
+    for (int s = 0; s < 4; ++s) c.odd_key[s] = INT_MAX;
     for (int s = 0; s < kFragRing; ++s) {
       mbar_init(&c.f_full[s], 1);
       mbar_init(&c.f_empty[s], kFragConsumers);
@@ -173,6 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = c.tmem_base;
+  // Keys from here on are not seen by every row of the tile: V's tiles from
+  // this one's block on go through the loaders.
+  auto seen_by_all = [&](const Frag& f) { return min(f.kv_len, visible_keys(p.causal, f.q_len, f.kv_len, f.tok0)); };
   // a warp's next fragment (lane 0 frees the slot once all lanes have read it)
   auto next_frag = [&](uint32_t n, Frag& f, bool& ok, uint32_t where) {
     const int s = n % kFragRing;
@@ -271,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++it) {
             if constexpr (FP8) {
-              const int s = it % 2;
-              if (!(ok = mbar_wait_warp(&c.raw_empty[s], ((it / 2) & 1) ^ 1, abort_flag, hdr, 0x803))) break;
+              const int s = it % C::kRaw;
+              if (!(ok = mbar_wait_warp(&c.raw_empty[s], ((it / C::kRaw) & 1) ^ 1, abort_flag, hdr, 0x803))) break;
               if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[s], np * ps * (D + 1));
               __syncwarp();
               if (lane < np) {
@@ -299,12 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------ MMA issuer
-      uint32_t it = 0, pc[2] = {0, 0}, fixes = 0;
+      uint32_t it = 0, pc[2] = {0, 0}, fixed = 0;  // fixed: phase bits of fix[]
       bool ok = true;
       const uint32_t elected = elect_one();
       Frag f;
       for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x805); ++n) {
         const int nh[2] = {f.n0, f.n1};
+        const int all_see = seen_by_all(f);
         // one thread waits and issues; the warp stays together at the fragment's end
         if (elected) {
           do {
@@ -323,15 +342,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               tc_commit(&c.kv_empty[it % C::kStages]);
             }
+            // the queries are free once the last block's scores are formed: the
+            // next tile's come in under this one's last weights and products
+            if (f.load <= 1) tc_commit(&c.q_empty);
             for (int b = 0; ok && b < f.load; ++b) {
               const uint32_t vi = it + 2 * b + 1, ki = vi + 1;
               const uint8_t* vt = tl.kv[vi % C::kStages];
               const uint8_t* kt = tl.kv[ki % C::kStages];
               const bool more = b + 1 < f.load;
               if (!(ok = full(vi))) break;
-              if (!FP8 && (f.kb0 + b + 1) * kChunkBlk > f.kv_len) {  // the loaders clear the rows past the last key
-                if (!(ok = mbar_wait(&c.fix, fixes & 1, abort_flag, hdr, 0x808))) break;
-                ++fixes;
+              if (!FP8 && (f.kb0 + b + 1) * kChunkBlk > all_see) {
+                const uint32_t s = vi % C::kStages;
+                if (!(ok = mbar_wait(&c.fix[s], (fixed >> s) & 1, abort_flag, hdr, 0x808))) break;
+                fixed ^= 1u << s;
               }
               bool k_in = false;
 #pragma unroll
@@ -358,9 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) break;
               tc_commit(&c.kv_empty[vi % C::kStages]);
               if (more) tc_commit(&c.kv_empty[ki % C::kStages]);
+              if (b + 2 == f.load) tc_commit(&c.q_empty);
             }
             if (!ok) break;
-            tc_commit(&c.q_empty);
             it += 2 * f.load;
           } while (false);
         }
@@ -376,59 +399,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     Frag f;
     for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x80a); ++n) {
       if (!(ok = mbar_wait_warp(&c.q_empty, (n & 1) ^ 1, abort_flag, hdr, 0x80b))) break;
-      constexpr int kCh = D / 8;  // 16-byte chunks of a row
-#pragma unroll 4
-      for (int i = lt; i < 256 * kCh; i += 128) {
-        const int row = i / kCh, ch = i % kCh;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < f.rows) {
-          const int tok = row / p.G;
-          x = __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)(f.q0 + f.tok0 + tok) * p.q_stride +
-                                                   (int64_t)(f.h * p.G + row - tok * p.G) * D) + ch);
-        }
-        *reinterpret_cast<uint4*>(tl.q + (row >> 7) * C::kTileB + (ch / 8) * 128 * 128 + sw128_off(row & 127, ch % 8)) = x;
+      // straight to shared memory, all of a thread's 16-byte pieces in flight
+      // (through registers, four at a time, a tile waited 8 us for its queries)
+      constexpr int kCh = D / 8;  // pieces of a row
+      const int ch = lt % kCh;
+      const uint32_t q_dst = smem_u32(tl.q) + (ch / 8) * 128 * 128;
+#pragma unroll 8
+      for (int row = lt / kCh; row < 256; row += 128 / kCh) {
+        const int tok = row / p.G;
+        const bool in = row < f.rows;
+        const __nv_bfloat16* src =
+            in ? p.q + (int64_t)(f.q0 + f.tok0 + tok) * p.q_stride + (int64_t)(f.h * p.G + row - tok * p.G) * D + ch * 8 : p.q;
+        cp_async16(q_dst + (row >> 7) * C::kTileB + sw128_off(row & 127, ch % 8), src, in ? 16 : 0);
       }
+      cp_async_wait_all();
+      // the slot of the fragment after this one.  Its last user, three back,
+      // is done: this fragment is published once every softmax warp has taken
+      // the one two back (the fragment ring), having finished the one before.
+      if (lt == 0) c.odd_key[(n + 1) % 4] = INT_MAX;
+      int* odd_key = &c.odd_key[n % 4];
       fence_proxy_async_smem();
       mbar_arrive(&c.q_full);
       if constexpr (FP8) {
         for (int b = 0; ok && b < 2 * f.load; ++b, ++it) {
-          const int rs = it % 2, s = it % C::kStages;
+          const int rs = it % C::kRaw, s = it % C::kStages;
           const int keys = f.kv_len - (f.kb0 + b / 2) * kChunkBlk;  // rows from here on are cleared
-          if (!(ok = mbar_wait_warp(&c.raw_full[rs], (it / 2) & 1, abort_flag, hdr, 0x80c))) break;
+          if (!(ok = mbar_wait_warp(&c.raw_full[rs], (it / C::kRaw) & 1, abort_flag, hdr, 0x80c))) break;
           if (!(ok = mbar_wait_warp(&c.kv_empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag, hdr, 0x80d))) break;
-          constexpr int kRawCh = D / 16;  // 16-code chunks of a row
-#pragma unroll 2
-          for (int i = lt; i < 128 * kRawCh; i += 128) {
-            const int row = i / kRawCh, ch = i % kRawCh;
-            uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            if (row < keys) {
-              const uint4 x = *reinterpret_cast<const uint4*>(tl.raw[rs] + row * D + ch * 16);
-              // 2^120 undoes the conversion's bias; a scale above 2^7 is applied in two factors
-              const uint32_t sb = c.scales[rs][row];
-              const uint32_t up = sb == 255u ? 0x7FC0u : (min(sb, 134u) + 120u) << 7;
-              const uint32_t f2 = up * 0x10001u;
-              const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+          // A thread takes the same 16 channels of every kStep-th row: its place
+          // in the swizzle (row mod 8) stays.  The upper 64 channels' lanes
+          // write their two 16-byte chunks in the other order: the two
+          // 64-channel columns share their banks.
+          constexpr int kRawCh = D / 16, kStep = 128 / kRawCh, kBatch = 4;
+          const int ch = lt % kRawCh, row0 = lt / kRawCh;
+          const int flip = (ch >> 2) & 1;
+          const uint8_t* src = tl.raw[rs] + row0 * D + ch * 16;
+          uint8_t* dst = tl.kv[s] + (ch / 4) * 128 * 128 + row0 * 128;
+          const uint32_t at0 = (((2 * ch) & 7) ^ (row0 & 7)) << 4, at1 = at0 ^ 16;
+          auto convert = [](const uint4& x, uint32_t f, uint32_t (&y)[8]) {
+            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              y[2 * k] = bf16x2_mul(e4m3_hi_to_bf16x2(prmt(wd[k], 0u, 0x1404u)), f);
+              y[2 * k + 1] = bf16x2_mul(e4m3_hi_to_bf16x2(prmt(wd[k], 0u, 0x3424u)), f);
+            }
+          };
+          auto put = [&](int i, const uint32_t (&y)[8]) {
+            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+            uint8_t* d = dst + i * kStep * 128;
+            *reinterpret_cast<uint4*>(d + (flip ? at1 : at0)) = flip ? hi : lo;
+            *reinterpret_cast<uint4*>(d + (flip ? at0 : at1)) = flip ? lo : hi;
+          };
+          uint32_t sb[kRawCh];
+          bool plain = keys >= kChunkBlk;
+#pragma unroll
+          for (int i = 0; i < kRawCh; ++i) {
+            sb[i] = c.scales[rs][row0 + i * kStep];
+            plain = plain && sb[i] <= 134u;
+          }
+          if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+            for (int i0 = 0; i0 < kRawCh; i0 += kBatch) {
+              uint4 x[kBatch];
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) x[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * kStep * D);
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                uint32_t y[8];
+                // 2^120 undoes the conversion's bias: (byte + 120) << 7 in both halves
+                convert(x[i], sb[i0 + i] * 0x00800080u + 120u * 0x00800080u, y);
+                put(i0 + i, y);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < kRawCh; ++i) {
+              const int row = row0 + i * kStep;
+              const uint32_t sc = c.scales[rs][row];
               uint32_t y[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                y[2 * k] = bf16x2_mul(e4m3_hi_to_bf16x2(prmt(wd[k], 0u, 0x1404u)), f2);
-                y[2 * k + 1] = bf16x2_mul(e4m3_hi_to_bf16x2(prmt(wd[k], 0u, 0x3424u)), f2);
-              }
-              if (sb > 134u && sb != 255u) {
-                const uint32_t f3 = ((sb - 134u + 127u) << 7) * 0x10001u;
+              for (int k = 0; k < 8; ++k) y[k] = 0u;
+              if (row < keys) {
+                if (sc != 255u) {  // a scale above 2^7: in two factors
+                  convert(*reinterpret_cast<const uint4*>(src + i * kStep * D), min(sc, 134u) * 0x00800080u + 120u * 0x00800080u, y);
+                  const uint32_t f2 = ((max(sc, 134u) - 134u + 127u) << 7) * 0x10001u;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = bf16x2_mul(y[k], f3);
-              }
-              out[0] = make_uint4(y[0], y[1], y[2], y[3]);
-              out[1] = make_uint4(y[4], y[5], y[6], y[7]);
-            }
-            // the second half of a row's lanes write their chunks in the other
-            // order: the two 64-channel columns share their banks
-            const int flip = D == 128 ? (ch >> 2) & 1 : 0;
+                  for (int k = 0; k < 8; ++k) y[k] = bf16x2_mul(y[k], f2);
+                } else if (b & 1) {
+                  atomicMin(odd_key, (f.kb0 + b / 2) * kChunkBlk + row);
+                } else {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int cc = 2 * ch + (k ^ flip);
-              *reinterpret_cast<uint4*>(tl.kv[s] + (cc / 8) * 128 * 128 + sw128_off(row, cc % 8)) = flip ? out[k ^ 1] : out[k];
+                  for (int k = 0; k < 8; ++k) y[k] = 0x7FC07FC0u;
+                }
+              }
+              put(i, y);
             }
           }
           fence_proxy_async_smem();
@@ -436,17 +500,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&c.raw_empty[rs]);
         }
       } else {
-        const int lb = f.load - 1, keys = f.kv_len - (f.kb0 + lb) * kChunkBlk;
-        if (f.load && keys < kChunkBlk) {  // V's rows past the last key
-          const uint32_t vi = it + 2 * lb + 1;
-          const int s = vi % C::kStages;
+        const int all_see = seen_by_all(f);
+        for (int b = max(0, all_see / kChunkBlk - f.kb0); ok && b < f.load; ++b) {
+          const int key0 = (f.kb0 + b) * kChunkBlk, keys = f.kv_len - key0;
+          const uint32_t vi = it + 2 * b + 1, s = vi % C::kStages;
           if (!(ok = mbar_wait_warp(&c.kv_full[s], (vi / C::kStages) & 1, abort_flag, hdr, 0x80e))) break;
+#pragma unroll 4
           for (int i = lt; i < 128 * (D / 8); i += 128) {
             const int row = i / (D / 8), ch = i % (D / 8);
-            if (row >= keys) *reinterpret_cast<uint4*>(tl.kv[s] + (ch / 8) * 128 * 128 + sw128_off(row, ch % 8)) = make_uint4(0, 0, 0, 0);
+            uint4* at = reinterpret_cast<uint4*>(tl.kv[s] + (ch / 8) * 128 * 128 + sw128_off(row, ch % 8));
+            if (row >= keys) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else {
+              uint4 x = *at;
+              uint32_t* wd = &x.x;
+              // an exponent field of ones carries into the sign's place
+              uint32_t odd = 0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) odd |= ((wd[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+              if (odd) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((wd[k] & 0x7F80u) == 0x7F80u) wd[k] &= 0xFFFF0000u;
+                  if ((wd[k] & 0x7F800000u) == 0x7F800000u) wd[k] &= 0xFFFFu;
+                }
+                *at = x;
+                atomicMin(odd_key, key0 + row);
+              }
+            }
           }
           fence_proxy_async_smem();
-          mbar_arrive(&c.fix);
+          mbar_arrive(&c.fix[s]);
         }
         it += 2 * f.load;
       }
@@ -504,14 +588,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (up) m = top;
           l *= a;
           if (b > 0) {  // s_full follows this half's previous P V
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-              uint32_t o[32];
-              tmem_ld32(to + 32 * j, o);
+            // 16 columns at a time: the 128 scores stay in registers meanwhile
+            // (32 at a time spill, and the whole kernel takes twice as long)
+#pragma unroll 1
+            for (int j = 0; j < D / 16; ++j) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * j, o);
               tmem_ld_wait_regs(o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-              tmem_st32(to + 32 * j, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+              tmem_st16(to + 16 * j, o);
             }
           }
         }
@@ -565,6 +651,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
 #pragma unroll
         for (int k = 0; k < D; ++k) acc[k] = 0.f;
+      }
+      // infinities and NaN that the loaders took out of V: a weight is above 0
+      const int odd = f.load ? *reinterpret_cast<volatile int*>(&c.odd_key[n % 4]) : INT_MAX;
+      if (odd < vis) {
+        if constexpr (FP8) {  // a whole row
+#pragma unroll
+          for (int k = 0; k < D; ++k) acc[k] = __uint_as_float(0x7FC00000u);
+        } else {
+          const int end = min(vis, (f.kb0 + n_blk) * kChunkBlk);
+          for (int j = odd; j < end; ++j) {
+            const int id = __ldg(p.block_table + (int64_t)f.r * p.max_pages + (j >> p.page_shift));
+            if ((unsigned)id >= (unsigned)p.n_pages) continue;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.v + id * p.page_bytes + ((int64_t)f.h * p.page_size + (j & (p.page_size - 1))) * D * 2);
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+              const uint4 x = __ldg(src + k);
+              const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((wd[e] & 0x7F80u) == 0x7F80u) acc[8 * k + 2 * e] += bf16_lo(wd[e]);
+                if ((wd[e] & 0x7F800000u) == 0x7F800000u) acc[8 * k + 2 * e + 1] += bf16_hi(wd[e]);
+              }
+            }
+          }
+        }
       }
       bool write = f.whole;
       if (!f.whole) {

@@ -24,6 +24,8 @@
 //
 // The softmax reference of a column moves only when a score passes it by 2^8,
 // so most chunks need no shuffles; sums and accumulators are fp32.
+#include <climits>
+
 #include "paged.cuh"
 
 namespace flamia {
@@ -240,6 +242,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
 
     float o[C::kMT][NT][4];
     float m[NT][2], l[NT][2];
+    // bf16: an infinity in V times the lower term, or times the weight 0 of a
+    // row that may not see it, gives a NaN that the formula does not have.  So
+    // a warp that ends with a NaN takes its keys once more, carefully.
+    bool careful = false;
+  again:
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
@@ -370,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
             for (int e = 0; e < 2; ++e) {
               y[e] = ex2_approx(s[i][nt][2 * k + e] - (m[nt][e] == -INFINITY ? 0.f : m[nt][e]));
               l[nt][e] += y[e];
-              if constexpr (FP8) y[e] *= f[k];
+              // a NaN scale stays with the rows that see the key
+              if constexpr (FP8) y[e] = s[i][nt][2 * k + e] == -INFINITY ? 0.f : y[e] * f[k];
             }
             const uint32_t a = pack_bf16x2(y[0], y[1]);
             hi[i][nt][k] = transpose8(a);
@@ -378,33 +386,73 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
           }
       }
       // ---------------------------------------------- O^T += V^T P^T
+      // tok >= 0 (careful): only the columns of token tok, over the keys that
+      // it sees, and the lower terms over finite values
+      auto add_pv = [&](int tok) {
+        const int lim = tok < 0 ? INT_MAX : visible_keys(p.causal, rq.q_len, rq.kv_len, tok) - key0;
 #pragma unroll
-      for (int i = 0; i < C::kSub; ++i)
+        for (int i = 0; i < C::kSub; ++i) {
 #pragma unroll
-        for (int mt = 0; mt < C::kMT; ++mt) {
-          uint32_t a[4];
-          if constexpr (FP8) {
-            // channels 2 mt, 2 mt + 1 of the lane's run: bytes of one word
-            const int wd = mt >> 1, b = 2 * (mt & 1);
+          for (int mt = 0; mt < C::kMT; ++mt) {
+            uint32_t a[4];
+            if constexpr (FP8) {
+              // channels 2 mt, 2 mt + 1 of the lane's run: bytes of one word
+              const int wd = mt >> 1, b = 2 * (mt & 1);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t sel = (uint32_t)(b + (k & 1)) * 0x0011u + (uint32_t)(4 + b + (k & 1)) * 0x1100u;
-              const uint32_t x = prmt(vr[i][(k >> 1) * 2][wd], vr[i][(k >> 1) * 2 + 1][wd], sel);
-              a[k] = bf16x2_mul(e4m3_hi_to_bf16x2(x), 0x7B807B80u);
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t sel = (uint32_t)(b + (k & 1)) * 0x0011u + (uint32_t)(4 + b + (k & 1)) * 0x1100u;
+                const uint32_t x = prmt(vr[i][(k >> 1) * 2][wd], vr[i][(k >> 1) * 2 + 1][wd], sel);
+                a[k] = bf16x2_mul(e4m3_hi_to_bf16x2(x), 0x7B807B80u);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int kk = 16 * i + 2 * t + 8 * (k >> 1);
+                const uint32_t x = kk < lim ? vr[i][(k >> 1) * 2][mt] : 0u, y = kk + 1 < lim ? vr[i][(k >> 1) * 2 + 1][mt] : 0u;
+                a[k] = prmt(x, y, (k & 1) ? 0x7632u : 0x5410u);
+              }
             }
-          } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              a[k] = prmt(vr[i][(k >> 1) * 2][mt], vr[i][(k >> 1) * 2 + 1][mt], (k & 1) ? 0x7632u : 0x5410u);
-          }
+            for (int nt = 0; nt < NT; ++nt) {
+              float c[4] = {o[mt][nt][0], o[mt][nt][1], o[mt][nt][2], o[mt][nt][3]};
+              mma_bf16(c, a[0], a[1], a[2], a[3], hi[i][nt][0], hi[i][nt][1]);
+              uint32_t f[4] = {a[0], a[1], a[2], a[3]};
+              if (!FP8 && tok >= 0) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16(o[mt][nt], a[0], a[1], a[2], a[3], hi[i][nt][0], hi[i][nt][1]);
-            mma_bf16(o[mt][nt], a[0], a[1], a[2], a[3], lo[i][nt][0], lo[i][nt][1]);
+                for (int k = 0; k < 4; ++k) {
+                  if ((f[k] & 0x7F80u) == 0x7F80u) f[k] &= 0xFFFF0000u;
+                  if ((f[k] & 0x7F800000u) == 0x7F800000u) f[k] &= 0xFFFFu;
+                }
+              }
+              mma_bf16(c, f[0], f[1], f[2], f[3], lo[i][nt][0], lo[i][nt][1]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (tok < 0 || (8 * nt + 2 * t + e) / p.G == tok) {
+                  o[mt][nt][e] = c[e];
+                  o[mt][nt][2 + e] = c[2 + e];
+                }
+            }
           }
         }
+      };
+      if (FP8 || !careful) {
+        add_pv(-1);
+      } else {
+#pragma unroll 1
+        for (int tok = 0; tok < rq.q_len; ++tok) add_pv(tok);
+      }
       pg = pg_now;
       if (it + 1 < n_it) load_v(it + 1, pg);
+    }
+
+    float sum = 0.f;  // NaN where one of them is, and for infinities of both signs
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < C::kMT; ++i) sum += (o[i][nt][0] + o[i][nt][1]) + (o[i][nt][2] + o[i][nt][3]);
+    if (!FP8 && !careful && __any_sync(0xffffffffu, sum != sum)) {
+      careful = true;
+      goto again;
     }
 
     // ------------------------------------------------ join the warps

@@ -123,17 +123,32 @@ __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* pre
     p.hdr->workers = W;
     p.hdr->rows = cu[n];
   }
-  for (int w = warp; w < W; w += kPlanThreads / 32) {
+  auto start_of = [&](int w, int64_t& y) {  // the worker's request, head and blocks
     const int64_t x0 = cost * w / W, x1 = cost * (w + 1) / W;
-    const int r = find(pre, n, x0);
-    const int ql = cu[r + 1] - cu[r], kv = p.kv_len[r], nt = tiles_of(p, ql);
-    const int per_head = (int)((pre[r + 1] - pre[r]) / p.Hkv);
-    const int64_t y = x0 - pre[r];
     WorkerRec rec{};
-    rec.r = r;
-    rec.h = (int)(y / per_head);
-    int z = (int)(y - (int64_t)rec.h * per_head);
+    rec.r = find(pre, n, x0);
+    y = x0 - pre[rec.r];
     rec.n = (int)(x1 - x0);
+    return rec;
+  };
+  if (p.path != kPathChunk) {  // a tile is a head
+    for (int w = tid; w < W; w += kPlanThreads) {
+      int64_t y;
+      WorkerRec rec = start_of(w, y);
+      const int64_t per_head = (pre[rec.r + 1] - pre[rec.r]) / p.Hkv;
+      rec.h = (int)(y / per_head);
+      rec.blk = (int)(y - rec.h * per_head);
+      p.workers[w] = rec;
+    }
+    return;
+  }
+  for (int w = warp; w < W; w += kPlanThreads / 32) {
+    int64_t y;
+    WorkerRec rec = start_of(w, y);
+    const int r = rec.r, ql = cu[r + 1] - cu[r], kv = p.kv_len[r], nt = tiles_of(p, ql);
+    const int64_t per_head = (pre[r + 1] - pre[r]) / p.Hkv;
+    rec.h = (int)(y / per_head);
+    const int64_t z = y - rec.h * per_head;
     // the tile that holds block z of the head: 32 tiles at a time
     int off = 0;
     for (int t0 = 0; t0 < nt; t0 += 32) {
@@ -153,7 +168,7 @@ __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* pre
       }
       off += __shfl_sync(0xffffffffu, incl, 31);
     }
-    rec.blk = z - rec.tile_off;
+    rec.blk = (int)(z - rec.tile_off);
     if (lane == 0) p.workers[w] = rec;
   }
 }

@@ -219,3 +219,50 @@ def test_inconsistent_lengths_write_nothing(kind):
     O, lse = s.run()
     torch.cuda.synchronize()
     assert fl.flamia_get_device_status(s.ws) == fl.ERR_BAD_SEQLENS and (O == 77).all()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", ["drafts", "chunk", "split"])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_later_tokens_reach_no_earlier_row(cache, d, kind, value):
+    """A value or key of a new token that is not finite changes nothing in the rows that may not see it."""
+    q, kv = {"drafts": ([4, 3], [37, 64]), "chunk": ([200, 60], [400, 60]), "split": ([150, 3], [5000, 64])}[kind]
+    kw = dict(H=4, Hkv=2, d=d, ps=16, cache=cache, seed=21, max_q=4 if kind == "drafts" else 0)
+    clean = Step(q, kv, **kw)
+    cO, cl = clean.run()
+    for which, token in (("v", 2), ("v", q[0] - 1), ("k", 1)):
+        s = Step(q, kv, **kw)
+        j = kv[0] - q[0] + token
+        page, off = s.table_host[0][j // 16], j % 16
+        if cache == "bf16":
+            (s.k if which == "k" else s.v)[page, :, off, 7] = value
+        else:
+            (s.ks if which == "k" else s.vs)[page, :, off] = 255
+        O, lse = s.run()
+        other = [i for i in range(s.T) if not token <= i < q[0]]
+        # rows that do not see it: as without it (half a step more where an accumulator's last bit moves)
+        assert ((O[other].float() - cO[other].float()).abs() <= cO[other].float().abs() * 2.0 ** -7 + 1e-30).all()
+        assert torch.equal(lse[:, other], cl[:, other])
+        own = O[token:q[0]].float()
+        if which == "v":
+            assert torch.equal(lse, cl)
+            if cache == "bf16":
+                assert (own[..., 7] == value).all() if not math.isnan(value) else torch.isnan(own[..., 7]).all()
+                rest = [c for c in range(d) if c != 7]
+                assert torch.isfinite(own[..., rest]).all()
+            else:
+                assert torch.isnan(own).all()
+        elif cache == "e4m3" or math.isnan(value):
+            assert torch.isnan(own).all() and torch.isnan(lse[:, token:q[0]]).all()
+
+
+@pytest.mark.parametrize("kind", ["decode", "drafts", "chunk"])
+def test_infinite_values_stay_infinite(kind):
+    """An infinity in V reaches the rows that see it as an infinity, both signs as a NaN, and nothing else."""
+    q, kv, mq = {"decode": ([1, 1], [50, 300], 1), "drafts": ([4, 2], [50, 300], 4), "chunk": ([30, 1], [50, 300], 0)}[kind]
+    s = Step(q, kv, H=4, Hkv=2, seed=31, max_q=mq)
+    page = s.table_host[0][0]
+    s.v[page, :, 3, 9], s.v[page, :, 5, 17] = math.inf, -math.inf
+    s.v[page, :, 3, 33], s.v[page, :, 6, 33] = math.inf, -math.inf
+    s.check()
