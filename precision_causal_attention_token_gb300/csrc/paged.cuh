@@ -9,53 +9,67 @@ namespace flamia {
 // The split of the attention's work.  A tile is up to `rows` query rows (token
 // major, the G = H/Hkv query heads of a key/value head side by side) of one
 // request and one key/value head; its keys are visited in blocks of `blk`.
-// All blocks of all tiles in the order (request, head, tile, block) form one
-// line of `cost` blocks, and worker w (a CTA) takes the blocks
-// [floor(cost w / W), floor(cost (w + 1) / W)).  So the work is even to one
-// block whatever the lengths, a long context is split over as many SMs as
-// there are, and a worker leaves at most two unfinished tiles, whose partial
-// results (fp32) go to its two slots of the workspace: slot 2w for a tile that
-// an earlier worker began, 2w + 1 for one that it begins itself.  The last
-// worker of a tile to finish adds the partials up in worker order, so the
-// result does not depend on who is last.
+// All blocks of all tiles in the order (request, head, tile, block) form a
+// line, on which every tile also takes kTileCost places before its first
+// block for what a tile costs beside them, and worker w (a CTA) takes the
+// places [floor(cost w / W), floor(cost (w + 1) / W)).  So the work is even
+// whatever the lengths, a long context is split over as many SMs as there
+// are, and a worker leaves at most two unfinished tiles, whose partial results
+// (fp32) go to its two slots of the workspace: slot 2w for a tile that an
+// earlier worker began, 2w + 1 for one that it begins itself.  The last worker
+// of a tile to finish adds the partials up in worker order, so the result does
+// not depend on who is last.
+//
+// Requests with few rows (one new token, a few drafted ones) are served by
+// the decode kernel, the others by the chunk kernel: two lines.
 // ---------------------------------------------------------------------------
 enum { kPathDecode8 = 0, kPathDecode16 = 1, kPathChunk = 2 };
 constexpr int kDecodeBlk = 64, kChunkBlk = 128, kChunkRows = 256;
-constexpr int kMaxWorkers = 640;
+// What a tile costs beside its blocks, in blocks: its queries, first loads and
+// result (decode: 5 us of about 1 us a block)
+constexpr int kDecodeTileCost = 5, kChunkTileCost = 3;
+constexpr int kMaxWorkers = 512, kMaxChunkWorkers = 160;
 constexpr int kMaxReq = 8192;
 
 struct PagedHeader {
   WsHeader base;       // status words first, as flamia_get_device_status reads them
-  int64_t cost;        // blocks in all
-  int32_t ok;          // 1: the plan's inputs were consistent
-  int32_t rows;        // cu_q[n_req]
-  int32_t workers;     // W
+  int64_t cost[2];     // places of each line (0: decode, 1: chunk)
+  int32_t workers[2];  // W of each line
+  int32_t rows;        // cu_q[n_req], 0 after an inconsistent plan
   int32_t n_free_new;  // for a plan whose n_free and n_free_out are one word
-  int32_t pad[10];
-  unsigned int count[2 * kMaxWorkers];  // partials written, per tile (by its first worker) and half
+  int32_t pad[8];
+  unsigned int count[kMaxWorkers];              // decode: partials written, per tile (by its first worker)
+  unsigned int count_chunk[2 * kMaxChunkWorkers];  // chunk: also by half
 };
 
-struct ReqRec {
-  int32_t q0, q_len, kv_len, tiles;
-  int64_t base;      // first block of the request on the line
-  int32_t per_head;  // blocks of one head's tiles
-  int32_t pad;
+// A request of one line.
+struct __align__(16) ReqRec {
+  int32_t r, q0, q_len, kv_len;
+  int64_t base;      // its first place
+  int32_t per_head;  // places of one head's tiles
+  int32_t tiles;     // of a head
 };
-struct WorkerRec {
-  int32_t r, h, tile, blk;  // where it starts
-  int32_t n;                // its blocks
-  int32_t tile_off;         // blocks of the head's earlier tiles
+// Where a worker starts: everything that its first tile needs, in one read.
+struct __align__(16) WorkerRec {
+  ReqRec q;
+  int32_t at;        // the request's index in the line's list
+  int32_t h, tile;
+  int32_t pos;       // place within the tile
+  int32_t n;         // the worker's places (0: none)
+  int32_t tile_off;  // places of the head's earlier tiles
   int32_t pad[2];
 };
+static_assert(sizeof(ReqRec) == 32 && sizeof(WorkerRec) == 64, "read in 16-byte pieces");
 
 struct PagedLayout {
   size_t header, reqs, workers, part_ml, part_o, total;
-  int path, part_rows;
+  int path;
 };
 
 struct PagedParams {
   int n_req, T, max_q, H, Hkv, G, page_size, page_shift, n_pages, max_pages, causal, path;
-  int W_max;      // workers at most
+  int W_max[2];   // workers at most, of each line
+  int small_rows; // requests of up to so many rows go to the decode kernel (8, 16; 0: none)
   int tile_toks;  // tokens of a tile (kPathChunk)
   float c_log2;   // softmax_scale * log2(e)
   const int32_t* cu_q;
@@ -63,10 +77,10 @@ struct PagedParams {
   int32_t* block_table;
   int64_t q_stride, kv_stride;  // elements
   PagedHeader* hdr;
-  ReqRec* reqs;
-  WorkerRec* workers;
-  float2* part_ml;  // [2 W][rows] (reference, sum)
-  float* part_o;    // [2 W][rows][d] (decode), [2 W][d / 4][rows][4] (chunk)
+  ReqRec* reqs;        // [2][n_req]
+  WorkerRec* workers;  // [kMaxWorkers], [kMaxChunkWorkers]
+  float2* part_ml;     // [2 W][rows] (reference, sum)
+  float* part_o;       // [2 W][rows][d] (decode), [2 W][d / 4][rows][4] (chunk)
   // plan
   int32_t* slot_map;
   const int32_t* old_len;
@@ -93,7 +107,7 @@ cudaError_t launch_paged_decode(const PagedParams& p, int d, bool e4m3, cudaStre
 cudaError_t launch_paged_chunk(const PagedParams& p, int d, bool e4m3, const CUtensorMap& mk, const CUtensorMap& mv,
                                cudaStream_t st);
 // Workers of a launch on a GPU with `sms` SMs: what the kernel keeps resident.
-int paged_decode_workers(int sms, int path);
+int paged_decode_workers(int sms);
 
 // Keys that the rows of tokens [.., tok] of a request see (tok: its last token).
 __host__ __device__ __forceinline__ int visible_keys(int causal, int q_len, int kv_len, int tok) {

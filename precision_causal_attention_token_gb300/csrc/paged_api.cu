@@ -10,8 +10,6 @@ using namespace flamia;
 
 namespace {
 
-constexpr int kChunkMaxWorkers = 160;
-
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool dev16(const void* p) { return p && aligned(p, 16); }
 bool dev4(const void* p) { return p && aligned(p, 4); }
@@ -50,15 +48,18 @@ flamia_status_t validate(const flamia_paged_t* p) {
 PagedLayout layout(const flamia_paged_t& p) {
   PagedLayout L{};
   L.path = path_of(&p);
-  L.part_rows = L.path == kPathDecode8 ? 8 : L.path == kPathDecode16 ? 16 : kChunkRows;
-  const size_t slots = 2 * (size_t)(L.path == kPathChunk ? kChunkMaxWorkers : kMaxWorkers);
+  // the decode kernel's and the chunk kernel's partials, one after the other
+  // on the stream, lie in the same place
+  const size_t dec = 2 * (size_t)kMaxWorkers * (L.path == kPathDecode8 ? 8 : 16);
+  const size_t chunk = L.path == kPathChunk ? 2 * (size_t)kMaxChunkWorkers * kChunkRows : 0;
+  const size_t rows = dec > chunk ? dec : chunk;
   auto a256 = [](size_t x) { return (x + 255) & ~size_t(255); };
   size_t o = 0;
   L.header = o; o = a256(o + sizeof(PagedHeader));
-  L.reqs = o; o = a256(o + sizeof(ReqRec) * p.n_req);
-  L.workers = o; o = a256(o + sizeof(WorkerRec) * kMaxWorkers);
-  L.part_ml = o; o = a256(o + sizeof(float2) * slots * L.part_rows);
-  L.part_o = o; o = a256(o + sizeof(float) * slots * L.part_rows * p.d);
+  L.reqs = o; o = a256(o + sizeof(ReqRec) * 2 * p.n_req);
+  L.workers = o; o = a256(o + sizeof(WorkerRec) * (kMaxWorkers + kMaxChunkWorkers));
+  L.part_ml = o; o = a256(o + sizeof(float2) * rows);
+  L.part_o = o; o = a256(o + sizeof(float) * rows * p.d);
   L.total = o;
   return L;
 }
@@ -83,9 +84,12 @@ flamia_status_t fill(const flamia_paged_t* p, void* ws, size_t ws_bytes, PagedPa
   a->causal = p->causal != 0;
   a->path = L.path;
   const int sms = sm_count();
-  const int w = L.path == kPathChunk ? sms : paged_decode_workers(sms, L.path);
-  const int cap = L.path == kPathChunk ? kChunkMaxWorkers : kMaxWorkers;
-  a->W_max = w < cap ? w : cap;
+  const int w0 = paged_decode_workers(sms);
+  a->W_max[0] = w0 < kMaxWorkers ? w0 : kMaxWorkers;
+  a->W_max[1] = sms < kMaxChunkWorkers ? sms : kMaxChunkWorkers;
+  // which requests the decode kernel takes: all of a call with few rows each;
+  // in a call with chunks those of up to 8 rows (16 where a token alone has more than 8)
+  a->small_rows = L.path == kPathDecode8 ? 8 : L.path == kPathDecode16 ? 16 : a->G <= 8 ? 8 : a->G <= 16 ? 16 : 0;
   a->tile_toks = kChunkRows / a->G;
   const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)p->d);
   a->c_log2 = scale * 1.44269504088896341f;
@@ -191,7 +195,10 @@ flamia_status_t flamia_paged_fwd(const flamia_paged_t* p, const void* q, const f
   a.O = static_cast<__nv_bfloat16*>(O);
   a.lse = lse;
   const bool e4m3 = p->cache_dtype == FLAMIA_E4M3;
-  if (a.path != kPathChunk) return of(launch_paged_decode(a, p->d, e4m3, stream));
+  if (a.small_rows) {
+    const cudaError_t e = launch_paged_decode(a, p->d, e4m3, stream);
+    if (e != cudaSuccess || a.path != kPathChunk) return of(e);
+  }
   CUtensorMap mk{}, mv{};
   if (!e4m3 && (!make_pages_map(&mk, a.k, p, a.page_bytes) || !make_pages_map(&mv, a.v, p, a.page_bytes)))
     return FLAMIA_ERR_CUDA;

@@ -18,7 +18,6 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParam
   constexpr int kEl = BF16 ? 8 : 4;        // elements a lane holds
   constexpr int kLanes = D / kEl;          // lanes of a row (8, 16 or 32)
   constexpr int kRows = kThreads / kLanes; // rows a CTA reads at a time
-  if (!p.hdr->ok) return;
   const int sub = threadIdx.x % kLanes;
   const int64_t rows = (int64_t)p.hdr->rows * p.Hkv, all = 2 * rows;  // K's rows, then V's
   const int64_t n_slots = (int64_t)p.n_pages << p.page_shift;

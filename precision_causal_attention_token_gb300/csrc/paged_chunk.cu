@@ -151,14 +151,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   WsHeader* hdr = &p.hdr->base;
   volatile int* abort_flag = &c.abort_flag;
-  if (!p.hdr->ok || (int)blockIdx.x >= p.hdr->workers) return;
+  const WorkerRec* rec_at = p.workers + kMaxWorkers + blockIdx.x;
+  if (rec_at->n == 0) return;
 
   if (tid == 0) {
     mbar_init(&c.q_full, 128);
     mbar_init(&c.q_empty, 1);
     for (int s = 0; s < 5; ++s) {
       mbar_init(&c.kv_full[s], FP8 ? 128 : 1);
-      mbar_init(&c.kv_empty[s], 1);
+      mbar_init(&c.kv_empty[s], FP8 ? 1 : 1 + 4);  // the MMA issuer; bf16: also the loader warps
       mbar_init(&c.fix[s], 128);
     }
     for (int s = 0; s < 4; ++s) {
@@ -205,22 +206,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     setmaxnreg_dec<kRegCtl>();
     if (warp == kWarpSched && lane == 0) {
       // ------------------------------------------------------------ scheduler
-      const int64_t cost = p.hdr->cost;
-      const int W = p.hdr->workers, w = blockIdx.x;
-      const WorkerRec rec = p.workers[w];
-      int left = rec.n, r = rec.r, h = rec.h, tile = rec.tile, blk = rec.blk, off = rec.tile_off;
+      const WorkerRec rec = *rec_at;
+      ReqRec rq = rec.q;
+      int left = rec.n, at = rec.at, h = rec.h, tile = rec.tile, pos = rec.pos, off = rec.tile_off;
       bool ok = true;
-      for (uint32_t n = 0; ok; ++n) {
+      uint32_t n = 0;
+      while (true) {
         const int s = n % kFragRing;
         if (!(ok = mbar_wait(&c.f_empty[s], ((n / kFragRing) & 1) ^ 1, abort_flag, hdr, 0x801))) break;
         Frag& f = c.frag[s];
-        if (left <= 0) {
-          f.end = 1;
-          mbar_arrive(&c.f_full[s]);
-          break;
-        }
-        ReqRec rq = p.reqs[r];
-        while (rq.tiles == 0) rq = p.reqs[++r];  // no new tokens
         const int tok0 = tile * p.tile_toks, toks = min(p.tile_toks, rq.q_len - tok0), rows = toks * p.G;
         int nb[2];
 #pragma unroll
@@ -229,38 +223,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           nb[hf] = 128 * hf < rows
                        ? (visible_keys(p.causal, rq.q_len, rq.kv_len, tok0 + last) + kChunkBlk - 1) / kChunkBlk : 0;
         }
-        const int all = max(1, max(nb[0], nb[1])), take = min(left, all - blk);
-        f.r = r;
+        // the worker's part: blocks [blk, blk + nblk) behind the tile's own cost
+        const int all = max(1, max(nb[0], nb[1])), take = min(left, kChunkTileCost + all - pos);
+        const int blk = max(0, pos - kChunkTileCost), nblk = max(0, pos + take - kChunkTileCost) - blk;
+        f.r = rq.r;
         f.h = h;
         f.tile = tile;
         f.kb0 = blk;
-        f.n0 = max(0, min(nb[0], blk + take) - blk);
-        f.n1 = max(0, min(nb[1], blk + take) - blk);
+        f.n0 = max(0, min(nb[0], blk + nblk) - blk);
+        f.n1 = max(0, min(nb[1], blk + nblk) - blk);
         f.load = max(f.n0, f.n1);
         f.q0 = rq.q0;
         f.q_len = rq.q_len;
         f.kv_len = rq.kv_len;
         f.tok0 = tok0;
         f.rows = rows;
-        f.whole = take == all;
+        f.whole = nblk == all;
         f.starts = blk == 0;
         f.w0 = f.parts = 0;
         if (!f.whole) {
-          const int64_t x = rq.base + (int64_t)h * rq.per_head + off;
+          const int64_t cost = p.hdr->cost[1], x = rq.base + (int64_t)h * rq.per_head + off + kChunkTileCost;
+          const int W = p.hdr->workers[1];
           f.w0 = worker_of(x, cost, W);
           f.parts = worker_of(x + all - 1, cost, W) - f.w0 + 1;
         }
         f.end = 0;
-        mbar_arrive(&c.f_full[s]);
+        if (nblk > 0) {
+          mbar_arrive(&c.f_full[s]);
+          ++n;
+        }
         left -= take;
-        blk = 0;
-        off += all;
+        if (left == 0) break;
+        pos = 0;
+        off += kChunkTileCost + all;
         if (++tile == rq.tiles) {
           tile = off = 0;
           if (++h == p.Hkv) {
             h = 0;
-            ++r;
+            rq = p.reqs[p.n_req + ++at];
           }
+        }
+      }
+      if (ok) {  // no more
+        const int s = n % kFragRing;
+        if (mbar_wait(&c.f_empty[s], ((n / kFragRing) & 1) ^ 1, abort_flag, hdr, 0x815)) {
+          c.frag[s].end = 1;
+          mbar_arrive(&c.f_full[s]);
         }
       }
     } else if (warp == kWarpProd) {
@@ -500,11 +508,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&c.raw_empty[rs]);
         }
       } else {
+        // The loaders go through every tile, so that their waits never fall a
+        // ring's turn behind (a parity wait would then pass or stay wrongly):
+        // a stage is filled anew only when they have passed it too.
         const int all_see = seen_by_all(f);
-        for (int b = max(0, all_see / kChunkBlk - f.kb0); ok && b < f.load; ++b) {
-          const int key0 = (f.kb0 + b) * kChunkBlk, keys = f.kv_len - key0;
-          const uint32_t vi = it + 2 * b + 1, s = vi % C::kStages;
-          if (!(ok = mbar_wait_warp(&c.kv_full[s], (vi / C::kStages) & 1, abort_flag, hdr, 0x80e))) break;
+        for (int i2 = 0; i2 < 2 * f.load; ++i2, ++it) {
+          const int s = it % C::kStages, key0 = (f.kb0 + i2 / 2) * kChunkBlk, keys = f.kv_len - key0;
+          if (!(ok = mbar_wait_warp(&c.kv_full[s], (it / C::kStages) & 1, abort_flag, hdr, 0x80e))) break;
+          if (!(i2 & 1) || key0 + kChunkBlk <= all_see) {  // K, or V that every row sees
+            if (lane == 0) mbar_arrive(&c.kv_empty[s]);
+            continue;
+          }
 #pragma unroll 4
           for (int i = lt; i < 128 * (D / 8); i += 128) {
             const int row = i / (D / 8), ch = i % (D / 8);
@@ -531,8 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
           mbar_arrive(&c.fix[s]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.kv_empty[s]);
         }
-        it += 2 * f.load;
       }
     }
   } else {
@@ -690,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&c.wg[hf]);
         if (!(ok = mbar_wait_warp(&c.wg[hf], wgc & 1, abort_flag, hdr, 0x813))) break;
         ++wgc;
-        unsigned int* ctr = &p.hdr->count[2 * f.w0 + hf];
+        unsigned int* ctr = &p.hdr->count_chunk[2 * f.w0 + hf];
         if (row == 0) {
           const bool last = atomicAdd(ctr, 1u) == (unsigned)(f.parts - 1);
           if (last) *ctr = 0;
@@ -758,7 +773,7 @@ cudaError_t launch(const PagedParams& p, const CUtensorMap& mk, const CUtensorMa
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  paged_chunk_kernel<D, FP8><<<p.W_max, kThreads, smem, st>>>(p, mk, mv);
+  paged_chunk_kernel<D, FP8><<<p.W_max[1], kThreads, smem, st>>>(p, mk, mv);
   return cudaGetLastError();
 }
 

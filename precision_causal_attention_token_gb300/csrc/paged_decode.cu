@@ -4,27 +4,31 @@
 // Every cached byte is used by all rows of its head at once and needed once,
 // so the kernel is bound by HBM and its work is to keep loads in flight.  A
 // warp takes its own chunks of 4 KB of K and of V and runs them with no
-// barrier: fragments go from global memory straight to registers, 16 bytes a
-// lane, in whole 64- and 128-byte segments.  The products are m16n8k16 MMAs
-// in which the keys (S^T = K Q^T) and then the channels (O^T = V^T P^T) fill
-// the 16 rows and the query rows the 8 columns, so few rows waste little; a
-// dot product may take its channels in any order, so lane (g, t) simply holds
-// 16 contiguous bytes of key g, and V^T's channels are dealt the same way.
-// P^T leaves the first product with keys in rows and is turned for the second
-// by movmatrix.  The weights enter as two bf16 terms (hi + lo: 16 bits), which
-// is free here and leaves the output's own rounding as the only one that
-// counts.  The next chunk's K is requested as soon as this one's scores are
-// formed, its V as soon as P V is: about 6 KB in flight per warp.
+// barrier: each lane copies its fragments, 16 bytes at a time in whole 64- and
+// 128-byte segments, to its own places of a shared-memory ring two chunks
+// deep (asynchronous copies: 12 to 16 KB in flight per warp and no registers
+// held), and reads them back without a bank conflict.  The products are
+// m16n8k16 MMAs in which the keys (S^T = K Q^T) and then the channels
+// (O^T = V^T P^T) fill the 16 rows and the query rows the 8 columns, so few
+// rows waste little; a dot product may take its channels in any order, so lane
+// (g, t) simply holds 16 contiguous bytes of key g, and V^T's channels are
+// dealt the same way.  P^T leaves the first product with keys in rows and is
+// turned for the second by movmatrix.
 //
-// E4M3: K's codes become f16 (exact) and the queries f16 with a power-of-two
-// row scale (bf16's 8 significant bits fit; the scale puts the row's largest
-// element at 2^13, so what f16 cannot hold lies 2^-37 below it); the key's
-// scale multiplies its scores.  V's codes become bf16 (exact), the key's
-// scale multiplies its weights, whose range bf16 keeps.
+// bf16: the weights enter as two bf16 terms (hi + lo: 16 bits), which leaves
+// the output's own rounding as the only one that counts.
+// E4M3: codes become f16 (exact, one instruction for two).  The queries are
+// f16 with a power-of-two row scale (bf16's 8 significant bits fit; the scale
+// puts the row's largest element at 2^13, so what f16 cannot hold lies 2^-37
+// below it); the key's scale multiplies its scores.  The weights are f16
+// (2^-11 relative), times 2^(e - E + 7) with e the key's V exponent and E the
+// largest seen so far: at most 2^15, and f16's normal range leaves 29 binades
+// below the largest; E's rise rescales the accumulators.
 //
 // The softmax reference of a column moves only when a score passes it by 2^8,
 // so most chunks need no shuffles; sums and accumulators are fp32.
 #include <climits>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -34,9 +38,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-// CTAs of an SM: 4 x 128 threads x 128 registers fill its register file
-// (16 rows: 168 registers, 3 CTAs).
-constexpr int ctas_of(int nt) { return nt == 1 ? 4 : 3; }
+constexpr int kUnit = 4096;  // bytes of a chunk's K (or V)
+constexpr int kRingB = kWarps * 4 * kUnit;  // two chunks a warp
+// 3 CTAs of an SM: their rings take 192 of its 228 KB
+constexpr int kCtas = 3;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -56,16 +61,37 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
-// Cache bytes are read once: past L1.
-__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+// Asynchronous copies of a lane's own bytes; of them `n` (all or 0) are read, the rest is zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src, uint32_t n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ld8(const uint8_t* p) {
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
+}
+// Four E4M3 codes -> two f16 pairs, exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 template <int D, bool FP8, int NT>
@@ -79,34 +105,39 @@ struct Decode {
   static constexpr int kQ = 8 * NT;                 // query rows
 };
 
-template <int D, bool FP8, int NT>
-struct DecodeSmem {
+// Dynamic shared memory: the warps' rings and, after a tile's last key, the
+// join's buffers in the same place; then the E4M3 scale bytes.
+template <int D, int NT>
+struct Join {
   float o[kWarps][8 * NT][D + 4];
   float m[kWarps][8 * NT], l[kWarps][8 * NT];
-  int last;
+};
+struct Scales {
+  uint8_t b[kWarps][2][2][64];  // [warp][chunk mod 2][K, V][key]
 };
 
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const PagedParams p) {
   using C = Decode<D, FP8, NT>;
-  __shared__ DecodeSmem<D, FP8, NT> sm;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int sm_last;
+  Join<D, NT>& sm = *reinterpret_cast<Join<D, NT>*>(smem);
+  Scales& scl = *reinterpret_cast<Scales*>(smem + kRingB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   PagedHeader* hdr = p.hdr;
-  if (!hdr->ok) return;
-  const int W = hdr->workers, w = blockIdx.x;
-  if (w >= W) return;
-  const int64_t cost = hdr->cost;
+  const int w = blockIdx.x;
   const WorkerRec rec = p.workers[w];
-  int left = rec.n, r = rec.r, h = rec.h, blk = rec.blk;
+  int left = rec.n, at = rec.at, h = rec.h, pos = rec.pos;
+  if (left == 0) return;
+  ReqRec rq = rec.q;
 
-  while (left > 0) {
-    const ReqRec rq = p.reqs[r];
-    if (rq.per_head == 0) {  // no new tokens
-      ++r;
-      continue;
-    }
-    const int nb = min(left, rq.per_head - blk);
+  while (true) {
+    // the worker's part of this tile: blocks [blk, blk + nb) behind the tile's own cost
+    const int take = min(left, rq.per_head - pos), blk = max(0, pos - kDecodeTileCost);
+    const int blocks = rq.per_head - kDecodeTileCost, nb = max(0, pos + take - kDecodeTileCost) - blk;
+    const int r = rq.r;
     const int kbeg = blk * kDecodeBlk, kend = min(rq.kv_len, (blk + nb) * kDecodeBlk);
+   if (nb > 0) {
     const int rows = rq.q_len * p.G;
     // ------------------------------------------------ queries (B operand) and column limits
     uint32_t qf[NT][D / 16][2];
@@ -176,69 +207,51 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
       }
       return id;
     };
-    uint32_t kr[C::kSub][2][C::kKJ][4];
-    uint32_t vr[C::kSub][4][C::kVW];
-    uint32_t sc_k = 0, sc_v = 0;  // scale bytes: lane i (< 16) K's of key i, lane 16 + i V's, a byte per key tile
-    auto load_k = [&](int it, int pg) {
+    const uint32_t ring = smem_u32(smem) + warp * 4 * kUnit;  // K, V of even chunks, K, V of odd ones
+    const uint32_t scales = smem_u32(scl.b[warp]);
+    // request a chunk's K (or V) and its scale bytes: one group of copies each
+    auto request = [&](int it, int pg, auto is_v) {
+      constexpr bool kV = decltype(is_v)::value;
       const int key0 = key_of(it);
+      const uint32_t dst = ring + (2 * (it & 1) + kV) * kUnit + lane * (kV && C::kVW == 2 ? 8 : 16);
 #pragma unroll
       for (int s = 0; s < C::kSub; ++s) {
         const int id = __shfl_sync(0xffffffffu, pg, (it % kGroup) * C::kSub + s);
         const int key = key0 + 16 * s;
         const int64_t in_page = (int64_t)h * p.page_size + (key & (p.page_size - 1));
-        const uint8_t* base = p.k + id * p.page_bytes + in_page * C::kRowB + t * 16;
+        const uint8_t* base = (kV ? p.v : p.k) + id * p.page_bytes + in_page * C::kRowB;
+        if constexpr (!kV) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const bool in = key + 8 * half + g < kend;
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t n = key + 8 * half + g < kend ? 16 : 0;
 #pragma unroll
-          for (int j = 0; j < C::kKJ; ++j) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (in) x = ld16(base + (8 * half + g) * C::kRowB + 64 * j);
-            kr[s][half][j][0] = x.x;
-            kr[s][half][j][1] = x.y;
-            kr[s][half][j][2] = x.z;
-            kr[s][half][j][3] = x.w;
+            for (int j = 0; j < C::kKJ; ++j)
+              copy16(dst + ((s * 2 + half) * C::kKJ + j) * 512, base + (8 * half + g) * C::kRowB + t * 16 + 64 * j, n);
           }
-        }
-        if constexpr (FP8) {
-          const int64_t at = (int64_t)id * p.Hkv * p.page_size + in_page + (lane & 15);
-          uint32_t b = 127;
-          if (key + (lane & 15) < kend) b = __ldg((lane < 16 ? p.k_scales : p.v_scales) + at);
-          sc_k = s ? sc_k | (b << (8 * s)) : b;
-        }
-      }
-    };
-    auto load_v = [&](int it, int pg) {
-      const int key0 = key_of(it);
+        } else {
 #pragma unroll
-      for (int s = 0; s < C::kSub; ++s) {
-        const int id = __shfl_sync(0xffffffffu, pg, (it % kGroup) * C::kSub + s);
-        const int key = key0 + 16 * s;
-        const int64_t in_page = (int64_t)h * p.page_size + (key & (p.page_size - 1));
-        const uint8_t* base = p.v + id * p.page_bytes + in_page * C::kRowB;
+          for (int i = 0; i < 4; ++i) {
+            const int kk = 2 * t + (i & 1) + 8 * (i >> 1);
+            const bool in = key + kk < kend;
+            if constexpr (C::kVW == 2) {
+              copy8(dst + (s * 4 + i) * 256, base + kk * C::kRowB + g * 8, in ? 8 : 0);
+            } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int kk = 2 * t + (i & 1) + 8 * (i >> 1);
-          const bool in = key + kk < kend;
-          if constexpr (C::kVW == 2) {
-            uint2 x = make_uint2(0, 0);
-            if (in) x = ld8(base + kk * C::kRowB + g * 8);
-            vr[s][i][0] = x.x;
-            vr[s][i][1] = x.y;
-          } else {
-#pragma unroll
-            for (int j = 0; j < C::kVW / 4; ++j) {
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (in) x = ld16(base + kk * C::kRowB + 128 * j + g * 16);
-              vr[s][i][4 * j] = x.x;
-              vr[s][i][4 * j + 1] = x.y;
-              vr[s][i][4 * j + 2] = x.z;
-              vr[s][i][4 * j + 3] = x.w;
+              for (int j = 0; j < C::kVW / 4; ++j)
+                copy16(dst + ((s * 4 + i) * (C::kVW / 4) + j) * 512, base + kk * C::kRowB + 128 * j + g * 16, in ? 16 : 0);
             }
           }
         }
+        if constexpr (FP8) {  // 16 bytes of one page
+          if (lane == s)
+            copy16(scales + ((it & 1) * 2 + kV) * 64 + 16 * s, (kV ? p.v_scales : p.k_scales) + (int64_t)id * p.Hkv * p.page_size + in_page,
+                   key < kend ? 16 : 0);
+        }
       }
+      copy_commit();
     };
+    using K_ = std::integral_constant<bool, false>;
+    using V_ = std::integral_constant<bool, true>;
 
     float o[C::kMT][NT][4];
     float m[NT][2], l[NT][2];
@@ -254,16 +267,33 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
 #pragma unroll
       for (int i = 0; i < C::kMT; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
     }
+    [[maybe_unused]] int e_ref = 0;  // E + 127: the largest V scale byte so far
     int pg = 0, pg_next = 0;
     if (n_it > 0) {
       pg = page_group(0);
-      load_k(0, pg);
-      load_v(0, pg);
+      request(0, pg, K_{});
+      request(0, pg, V_{});
+      if (n_it > 1) {
+        request(1, pg, K_{});
+        request(1, pg, V_{});
+      } else {
+        copy_commit();
+        copy_commit();
+      }
       if (n_it > kGroup) pg_next = page_group(kGroup);
     }
     for (int it = 0; it < n_it; ++it) {
       const int key0 = key_of(it);
+      const uint32_t kb = ring + 2 * (it & 1) * kUnit + lane * 16;
+      const uint32_t vb = ring + (2 * (it & 1) + 1) * kUnit + lane * (C::kVW == 2 ? 8 : 16);
+      // the page ids of chunk it + 2
+      if ((it + 2) % kGroup == 0) {
+        pg = pg_next;
+        if (it + 2 + kGroup < n_it) pg_next = page_group(it + 2 + kGroup);
+      }
       // ---------------------------------------------- S^T = K Q^T
+      copy_wait<3>();
+      if (FP8) __syncwarp();  // the scale bytes are other lanes' copies
       float s[C::kSub][NT][4];
 #pragma unroll
       for (int i = 0; i < C::kSub; ++i) {
@@ -271,12 +301,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
         for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.f;
 #pragma unroll
         for (int j = 0; j < C::kKJ; ++j) {
+          const uint4 u0 = lds16(kb + ((i * 2 + 0) * C::kKJ + j) * 512), u1 = lds16(kb + ((i * 2 + 1) * C::kKJ + j) * 512);
+          const uint32_t x[4] = {u0.x, u0.y, u0.z, u0.w}, y[4] = {u1.x, u1.y, u1.z, u1.w};
           if constexpr (FP8) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const uint32_t x = kr[i][0][j][u], y = kr[i][1][j][u];
-              const uint32_t a0 = e4m3x2_to_f16x2(x & 0xFFFFu), a2 = e4m3x2_to_f16x2(x >> 16);
-              const uint32_t a1 = e4m3x2_to_f16x2(y & 0xFFFFu), a3 = e4m3x2_to_f16x2(y >> 16);
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(x[u], a0, a2);
+              e4m3x4_to_f16(y[u], a1, a3);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma_f16(s[i][nt], a0, a1, a2, a3, qf[nt][4 * j + u][0], qf[nt][4 * j + u][1]);
             }
@@ -285,40 +317,38 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_bf16(s[i][nt], kr[i][0][j][2 * u], kr[i][1][j][2 * u], kr[i][0][j][2 * u + 1], kr[i][1][j][2 * u + 1],
-                         qf[nt][2 * j + u][0], qf[nt][2 * j + u][1]);
+                mma_bf16(s[i][nt], x[2 * u], y[2 * u], x[2 * u + 1], y[2 * u + 1], qf[nt][2 * j + u][0], qf[nt][2 * j + u][1]);
           }
         }
       }
-      sc_v = sc_k;  // this chunk's scale bytes; load_k takes the next one's
-      int pg_now = pg;
-      if (it + 1 < n_it) {
-        if ((it + 1) % kGroup == 0) {
-          pg_now = pg_next;
-          if (it + 1 + kGroup < n_it) pg_next = page_group(it + 1 + kGroup);
+      if constexpr (FP8) {
+        const uint8_t* sk = scl.b[warp][it & 1][0];
+#pragma unroll
+        for (int i = 0; i < C::kSub; ++i) {
+          const float f0 = ue8m0(sk[16 * i + g]), f1 = ue8m0(sk[16 * i + 8 + g]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              s[i][nt][e] *= cq[nt][e] * f0;
+              s[i][nt][2 + e] *= cq[nt][e] * f1;
+            }
         }
-        load_k(it + 1, pg_now);
+        __syncwarp();
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::kSub; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[i][nt][e] *= cq[nt][e & 1];
       }
+      if (it + 2 < n_it) request(it + 2, pg, K_{});
+      else copy_commit();
       // ---------------------------------------------- scores, reference, weights
       float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < C::kSub; ++i) {
-        float f0 = 1.f, f1 = 1.f;
-        if constexpr (FP8) {
-          f0 = ue8m0((__shfl_sync(0xffffffffu, sc_v, g) >> (8 * i)) & 0xFFu);
-          f1 = ue8m0((__shfl_sync(0xffffffffu, sc_v, 8 + g) >> (8 * i)) & 0xFFu);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            s[i][nt][e] *= FP8 ? cq[nt][e] * f0 : cq[nt][e];
-            s[i][nt][2 + e] *= FP8 ? cq[nt][e] * f1 : cq[nt][e];
-          }
-        }
-      }
       if (key0 + C::kChunk > vis_min) {
 #pragma unroll
         for (int i = 0; i < C::kSub; ++i)
@@ -360,13 +390,40 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
             }
           }
       }
-      uint32_t hi[C::kSub][NT][2], lo[C::kSub][NT][2];  // P^T as B operand
+      // ---------------------------------------------- weights: P^T as B operand
+      uint32_t hi[C::kSub][NT][2];
+      [[maybe_unused]] uint32_t lo[FP8 ? 1 : C::kSub][NT][2];
+      copy_wait<3>();  // this chunk's V
+      if constexpr (FP8) {
+        __syncwarp();
+        const uint8_t* sv = scl.b[warp][it & 1][1];
+        int e_top = 0;
+#pragma unroll
+        for (int i = 0; i < C::kSub; ++i) {
+          const int b = sv[16 * i + (lane & 15)];
+          e_top = max(e_top, b == 255 ? 0 : b);
+        }
+        if (__any_sync(0xffffffffu, e_top > e_ref)) {
+          e_top = __reduce_max_sync(0xffffffffu, e_top);
+          const float a = e_top - e_ref < 127 ? exp2i(e_ref - e_top) : 0.f;
+          e_ref = e_top;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < C::kMT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[i][nt][e] *= a;
+        }
+      }
 #pragma unroll
       for (int i = 0; i < C::kSub; ++i) {
         float f[2] = {1.f, 1.f};
         if constexpr (FP8) {
-          f[0] = ue8m0((__shfl_sync(0xffffffffu, sc_v, 16 + g) >> (8 * i)) & 0xFFu);
-          f[1] = ue8m0((__shfl_sync(0xffffffffu, sc_v, 24 + g) >> (8 * i)) & 0xFFu);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int b = scl.b[warp][it & 1][1][16 * i + 8 * k + g];
+            f[k] = b == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(max(b - e_ref + 134, 0) << 23);
+          }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -380,11 +437,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
               // a NaN scale stays with the rows that see the key
               if constexpr (FP8) y[e] = s[i][nt][2 * k + e] == -INFINITY ? 0.f : y[e] * f[k];
             }
-            const uint32_t a = pack_bf16x2(y[0], y[1]);
-            hi[i][nt][k] = transpose8(a);
-            lo[i][nt][k] = transpose8(pack_bf16x2(y[0] - bf16_lo(a), y[1] - bf16_hi(a)));
+            if constexpr (FP8) {
+              hi[i][nt][k] = transpose8(pack_f16x2(y[0], y[1]));
+            } else {
+              const uint32_t a = pack_bf16x2(y[0], y[1]);
+              hi[i][nt][k] = transpose8(a);
+              lo[i][nt][k] = transpose8(pack_bf16x2(y[0] - bf16_lo(a), y[1] - bf16_hi(a)));
+            }
           }
       }
+      if (FP8) __syncwarp();
       // ---------------------------------------------- O^T += V^T P^T
       // tok >= 0 (careful): only the columns of token tok, over the keys that
       // it sees, and the lower terms over finite values
@@ -392,45 +454,73 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
         const int lim = tok < 0 ? INT_MAX : visible_keys(p.causal, rq.q_len, rq.kv_len, tok) - key0;
 #pragma unroll
         for (int i = 0; i < C::kSub; ++i) {
+          // four channel tiles (E4M3: 16 bytes of a row are eight) at a time
+          constexpr int kW = C::kVW == 2 ? 2 : 4;  // words a load gives
 #pragma unroll
-          for (int mt = 0; mt < C::kMT; ++mt) {
-            uint32_t a[4];
+          for (int j = 0; j < C::kVW / kW; ++j) {
+            uint32_t w[4][kW];  // [key][word]
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (kW == 2) {
+                const uint2 x = lds8(vb + (i * 4 + k) * 256);
+                w[k][0] = x.x;
+                w[k][1] = x.y;
+              } else {
+                const uint4 x = lds16(vb + ((i * 4 + k) * (C::kVW / 4) + j) * 512);
+                w[k][0] = x.x;
+                w[k][1] = x.y;
+                w[k][kW - 2] = x.z;
+                w[k][kW - 1] = x.w;
+              }
+              if (!FP8 && 16 * i + 2 * t + (k & 1) + 8 * (k >> 1) >= lim)
+#pragma unroll
+                for (int x = 0; x < kW; ++x) w[k][x] = 0u;
+            }
             if constexpr (FP8) {
-              // channels 2 mt, 2 mt + 1 of the lane's run: bytes of one word
-              const int wd = mt >> 1, b = 2 * (mt & 1);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t sel = (uint32_t)(b + (k & 1)) * 0x0011u + (uint32_t)(4 + b + (k & 1)) * 0x1100u;
-                const uint32_t x = prmt(vr[i][(k >> 1) * 2][wd], vr[i][(k >> 1) * 2 + 1][wd], sel);
-                a[k] = bf16x2_mul(e4m3_hi_to_bf16x2(x), 0x7B807B80u);
+              for (int x = 0; x < kW; ++x) {
+                uint32_t c[4][2];  // channel pairs 4x, 4x + 1 and 4x + 2, 4x + 3 of each key
+#pragma unroll
+                for (int k = 0; k < 4; ++k) e4m3x4_to_f16(w[k][x], c[k][0], c[k][1]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  const uint32_t a0 = prmt(c[0][half], c[1][half], 0x5410u), a1 = prmt(c[0][half], c[1][half], 0x7632u);
+                  const uint32_t a2 = prmt(c[2][half], c[3][half], 0x5410u), a3 = prmt(c[2][half], c[3][half], 0x7632u);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * x + half][nt], a0, a1, a2, a3, hi[i][nt][0], hi[i][nt][1]);
+                }
               }
             } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int kk = 16 * i + 2 * t + 8 * (k >> 1);
-                const uint32_t x = kk < lim ? vr[i][(k >> 1) * 2][mt] : 0u, y = kk + 1 < lim ? vr[i][(k >> 1) * 2 + 1][mt] : 0u;
-                a[k] = prmt(x, y, (k & 1) ? 0x7632u : 0x5410u);
-              }
-            }
+              for (int x = 0; x < kW; ++x) {
+                const int mt = 4 * j + x;
+                uint32_t a[4] = {prmt(w[0][x], w[1][x], 0x5410u), prmt(w[0][x], w[1][x], 0x7632u),
+                                 prmt(w[2][x], w[3][x], 0x5410u), prmt(w[2][x], w[3][x], 0x7632u)};
+                float c[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float c[4] = {o[mt][nt][0], o[mt][nt][1], o[mt][nt][2], o[mt][nt][3]};
-              mma_bf16(c, a[0], a[1], a[2], a[3], hi[i][nt][0], hi[i][nt][1]);
-              uint32_t f[4] = {a[0], a[1], a[2], a[3]};
-              if (!FP8 && tok >= 0) {
+                for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if ((f[k] & 0x7F80u) == 0x7F80u) f[k] &= 0xFFFF0000u;
-                  if ((f[k] & 0x7F800000u) == 0x7F800000u) f[k] &= 0xFFFFu;
+                  for (int e = 0; e < 4; ++e) c[nt][e] = o[mt][nt][e];
+                  mma_bf16(c[nt], a[0], a[1], a[2], a[3], hi[i][nt][0], hi[i][nt][1]);
+                }
+                if (tok >= 0) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    if ((a[k] & 0x7F80u) == 0x7F80u) a[k] &= 0xFFFF0000u;
+                    if ((a[k] & 0x7F800000u) == 0x7F800000u) a[k] &= 0xFFFFu;
+                  }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma_bf16(c[nt], a[0], a[1], a[2], a[3], lo[i][nt][0], lo[i][nt][1]);
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (tok < 0 || (8 * nt + 2 * t + e) / p.G == tok) {
+                      o[mt][nt][e] = c[nt][e];
+                      o[mt][nt][2 + e] = c[nt][2 + e];
+                    }
                 }
               }
-              mma_bf16(c, f[0], f[1], f[2], f[3], lo[i][nt][0], lo[i][nt][1]);
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (tok < 0 || (8 * nt + 2 * t + e) / p.G == tok) {
-                  o[mt][nt][e] = c[e];
-                  o[mt][nt][2 + e] = c[2 + e];
-                }
             }
           }
         }
@@ -441,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
 #pragma unroll 1
         for (int tok = 0; tok < rq.q_len; ++tok) add_pv(tok);
       }
-      pg = pg_now;
-      if (it + 1 < n_it) load_v(it + 1, pg);
+      if (it + 2 < n_it) request(it + 2, pg, V_{});
+      else copy_commit();
     }
 
     float sum = 0.f;  // NaN where one of them is, and for infinities of both signs
@@ -456,6 +546,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
     }
 
     // ------------------------------------------------ join the warps
+    if constexpr (FP8) {  // the accumulators hold 2^(134 - e_ref) times the sum; in two normal factors
+      const float f0 = exp2i((e_ref - 134) / 2), f1 = exp2i(e_ref - 134 - (e_ref - 134) / 2);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < C::kMT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][nt][e] = o[i][nt][e] * f0 * f1;
+    }
+    __syncthreads();  // every warp is done with its ring
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -478,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
         }
       }
     __syncthreads();
-    const bool whole = nb == rq.per_head;
+    const bool whole = nb == blocks;
     constexpr int kSpan = kThreads / C::kQ;      // threads of a query row (16 or 8)
     constexpr int kPer = D / kSpan;              // channels of a thread
     const int row = tid / kSpan, d0 = (tid % kSpan) * kPer;
@@ -503,36 +603,53 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
     }
     bool write = whole;
     if (!whole) {
-      const int64_t tile0 = rq.base + (int64_t)h * rq.per_head;
-      const int w0 = worker_of(tile0, cost, W), n = worker_of(tile0 + rq.per_head - 1, cost, W) - w0 + 1;
+      const int64_t cost = hdr->cost[0], tile0 = rq.base + (int64_t)h * rq.per_head;
+      const int W = hdr->workers[0];
+      const int w0 = worker_of(tile0 + kDecodeTileCost, cost, W), n = worker_of(tile0 + rq.per_head - 1, cost, W) - w0 + 1;
       const int slot = blk == 0 ? 2 * w + 1 : 2 * w;
       float* po = p.part_o + ((int64_t)slot * C::kQ + row) * D + d0;
 #pragma unroll
       for (int k = 0; k < kPer; k += 4)
         __stcg(reinterpret_cast<float4*>(po + k), make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]));
       if (d0 == 0) __stcg(p.part_ml + (int64_t)slot * C::kQ + row, make_float2(M, L));
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
+        __threadfence();  // after the barrier: for the whole CTA
         const bool last = atomicAdd(&hdr->count[w0], 1u) == (unsigned)(n - 1);
         if (last) hdr->count[w0] = 0;
-        sm.last = last;
+        sm_last = last;
       }
       __syncthreads();
-      write = sm.last;
+      write = sm_last;
       if (write) {
+        // The partials' references and sums come in one round, then each
+        // row's threads form the weights together and add up their channels,
+        // eight partials in flight (one after the other, 57 of them took 20 us).
         __threadfence();
         auto slot_of = [&](int i) { return (int64_t)(i == 0 ? 2 * w0 + 1 : 2 * (w0 + i)); };
+        float2* ml = reinterpret_cast<float2*>(smem);  // [n][kQ]; the join's buffers are free
+        for (int x = tid; x < n * C::kQ; x += kThreads) ml[x] = __ldcg(p.part_ml + slot_of(x / C::kQ) * C::kQ + x % C::kQ);
+        __syncthreads();
+        const int me = tid % kSpan;
         M = -INFINITY;
-        for (int i = 0; i < n; ++i) M = fmaxf(M, __ldcg(p.part_ml + slot_of(i) * C::kQ + row).x);
+        for (int i = me; i < n; i += kSpan) M = fmaxf(M, ml[i * C::kQ + row].x);
+#pragma unroll
+        for (int k = kSpan / 2; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
         L = 0.f;
+        for (int i = me; i < n; i += kSpan) {
+          const float2 x = ml[i * C::kQ + row];
+          const float a = x.x == M ? 1.f : ex2_approx(x.x - M);
+          L += a * x.y;
+          ml[i * C::kQ + row].x = a;
+        }
+#pragma unroll
+        for (int k = kSpan / 2; k; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
+        __syncwarp();
 #pragma unroll
         for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < n; ++i) {
-          const float2 ml = __ldcg(p.part_ml + slot_of(i) * C::kQ + row);
-          const float a = ml.x == M ? 1.f : ex2_approx(ml.x - M);
-          L += a * ml.y;
+          const float a = ml[i * C::kQ + row].x;
           const float* src = p.part_o + (slot_of(i) * C::kQ + row) * D + d0;
 #pragma unroll
           for (int k = 0; k < kPer; k += 4) {
@@ -562,28 +679,41 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) paged_decode_kernel(con
       if (d0 == 0 && p.lse) p.lse[(int64_t)hq * p.T + rq.q0 + tok] = (M + lg2_f(L)) * 0.69314718055994531f;
     }
     __syncthreads();  // the join buffers are free
-    left -= nb;
-    blk = 0;
+   }
+    left -= take;
+    if (left == 0) break;
+    pos = 0;
     if (++h == p.Hkv) {
       h = 0;
-      ++r;
+      rq = p.reqs[++at];
     }
   }
 }
 
 template <int D, bool FP8, int NT>
 cudaError_t launch(const PagedParams& p, cudaStream_t st) {
-  paged_decode_kernel<D, FP8, NT><<<p.W_max, kThreads, 0, st>>>(p);
+  constexpr size_t smem = kRingB + (FP8 ? sizeof(Scales) : 0);
+  static_assert(sizeof(Join<D, NT>) <= kRingB && sizeof(float2) * kMaxWorkers * 8 * NT <= kRingB, "these lie in the rings' place");
+  static bool attr_set[64] = {};  // per device: raised once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(paged_decode_kernel<D, FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  paged_decode_kernel<D, FP8, NT><<<p.W_max[0], kThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 template <int D, bool FP8>
 cudaError_t launch_n(const PagedParams& p, cudaStream_t st) {
-  return p.path == kPathDecode8 ? launch<D, FP8, 1>(p, st) : launch<D, FP8, 2>(p, st);
+  return p.small_rows == 8 ? launch<D, FP8, 1>(p, st) : launch<D, FP8, 2>(p, st);
 }
 
 }  // namespace
 
-int paged_decode_workers(int sms, int path) { return sms * ctas_of(path == kPathDecode8 ? 1 : 2); }
+int paged_decode_workers(int sms) { return sms * kCtas; }
 
 cudaError_t launch_paged_decode(const PagedParams& p, int d, bool e4m3, cudaStream_t st) {
   if (d == 128) return e4m3 ? launch_n<128, true>(p, st) : launch_n<128, false>(p, st);

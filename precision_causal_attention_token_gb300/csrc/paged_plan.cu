@@ -58,27 +58,31 @@ __device__ __forceinline__ int find(const I* pre, int n, int64_t i) {
   return lo;
 }
 
-// Blocks of one tile.
-__device__ __forceinline__ int tile_blocks(const PagedParams& p, int q_len, int kv_len, int tile) {
-  if (p.path != kPathChunk) return max(1, (kv_len + kDecodeBlk - 1) / kDecodeBlk);
-  const int last = min(q_len, (tile + 1) * p.tile_toks) - 1;
-  return max(1, (visible_keys(p.causal, q_len, kv_len, last) + kChunkBlk - 1) / kChunkBlk);
-}
+// The line of a request with new tokens.
+__device__ __forceinline__ int line_of(const PagedParams& p, int q_len) { return (int64_t)q_len * p.G > p.small_rows; }
 __device__ __forceinline__ int tiles_of(const PagedParams& p, int q_len) {
-  if (p.path != kPathChunk) return q_len > 0;
-  return (q_len + p.tile_toks - 1) / p.tile_toks;
+  return line_of(p, q_len) ? (q_len + p.tile_toks - 1) / p.tile_toks : q_len > 0;
+}
+// Places of one tile.
+__device__ __forceinline__ int tile_places(const PagedParams& p, int line, int q_len, int kv_len, int tile) {
+  if (!line) return kDecodeTileCost + max(1, (kv_len + kDecodeBlk - 1) / kDecodeBlk);
+  const int last = min(q_len, (tile + 1) * p.tile_toks) - 1;
+  return kChunkTileCost + max(1, (visible_keys(p.causal, q_len, kv_len, last) + kChunkBlk - 1) / kChunkBlk);
 }
 
-// The work split (one CTA).  pre: [n_req + 1] blocks before each request.
-__device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* pre, int64_t* sm) {
+// The work split (one CTA): the requests of each line with their places, and
+// where each worker starts.  smem: per [n] places of a head, pre [n + 2] first
+// places, rid [n + 2] the requests; line 0 from entry 0, line 1 behind it,
+// each with an end entry.
+__device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* per, int64_t* pre, int32_t* rid, int64_t* sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.n_req;
   constexpr int kSerial = 4;  // tiles that a thread adds up alone; longer chunks take a warp
   for (int r = tid; r < n; r += kPlanThreads) {
-    const int ql = cu[r + 1] - cu[r], kv = p.kv_len[r], nt = tiles_of(p, ql);
+    const int ql = cu[r + 1] - cu[r], kv = p.kv_len[r], nt = tiles_of(p, ql), line = line_of(p, ql);
     int64_t sum = 0;
     if (nt <= kSerial)
-      for (int i = 0; i < nt; ++i) sum += tile_blocks(p, ql, kv, i);
-    pre[r] = sum;
+      for (int i = 0; i < nt; ++i) sum += tile_places(p, line, ql, kv, i);
+    per[r] = sum;
   }
   __syncthreads();
   if (p.path == kPathChunk) {
@@ -87,101 +91,140 @@ __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* pre
       if (nt <= kSerial) continue;
       const int kv = p.kv_len[r];
       int64_t sum = 0;
-      for (int i = lane; i < nt; i += 32) sum += tile_blocks(p, ql, kv, i);
+      for (int i = lane; i < nt; i += 32) sum += tile_places(p, 1, ql, kv, i);
 #pragma unroll
       for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      if (lane == 0) pre[r] = sum;
+      if (lane == 0) per[r] = sum;
     }
     __syncthreads();
   }
   const int seg = (n + kPlanThreads - 1) / kPlanThreads, r0 = min(n, tid * seg), r1 = min(n, r0 + seg);
-  int64_t mine = 0, cost;
-  for (int r = r0; r < r1; ++r) mine += pre[r] * p.Hkv;
-  int64_t at = block_scan(mine, sm, &cost);
+  int64_t cnt = 0, mine[2] = {0, 0}, cost[2], all;
   for (int r = r0; r < r1; ++r) {
-    const int64_t per_head = pre[r];
+    const int ql = cu[r + 1] - cu[r];
+    if (ql == 0) continue;
+    const int line = line_of(p, ql);
+    cnt += line ? (int64_t)1 << 32 : 1;
+    mine[line] += per[r] * p.Hkv;
+  }
+  const int64_t at = block_scan(cnt, sm, &all);
+  const int n0 = (int)(all & 0xFFFFFFFF), n1 = (int)(all >> 32);
+  int64_t place[2] = {block_scan(mine[0], sm, &cost[0]), block_scan(mine[1], sm, &cost[1])};
+  int idx[2] = {(int)(at & 0xFFFFFFFF), (int)(at >> 32)};
+  for (int r = r0; r < r1; ++r) {
+    const int ql = cu[r + 1] - cu[r];
+    if (ql == 0) continue;
+    const int line = line_of(p, ql);
     ReqRec q;
+    q.r = r;
     q.q0 = cu[r];
-    q.q_len = cu[r + 1] - cu[r];
+    q.q_len = ql;
     q.kv_len = p.kv_len[r];
-    q.tiles = tiles_of(p, q.q_len);
-    q.base = at;
-    q.per_head = (int)per_head;
-    q.pad = 0;
-    p.reqs[r] = q;
-    pre[r] = at;
-    at += per_head * p.Hkv;
+    q.base = place[line];
+    q.per_head = (int)per[r];
+    q.tiles = tiles_of(p, ql);
+    p.reqs[(int64_t)line * n + idx[line]] = q;
+    const int e = line * (n0 + 1) + idx[line];
+    pre[e] = place[line];
+    rid[e] = r;
+    place[line] += per[r] * p.Hkv;
+    ++idx[line];
   }
-  if (tid == 0) pre[n] = cost;
-  __syncthreads();
-  // Fewer workers than fit the GPU where a share would be too small to pay
-  // for joining its partial results.
-  const int64_t share = p.path == kPathChunk ? 2 : 4;
-  const int W = (int)max((int64_t)(cost > 0), min((int64_t)p.W_max, cost / share));
   if (tid == 0) {
-    p.hdr->cost = cost;
-    p.hdr->workers = W;
-    p.hdr->rows = cu[n];
+    pre[n0] = cost[0];
+    pre[n0 + 1 + n1] = cost[1];
   }
-  auto start_of = [&](int w, int64_t& y) {  // the worker's request, head and blocks
-    const int64_t x0 = cost * w / W, x1 = cost * (w + 1) / W;
-    WorkerRec rec{};
-    rec.r = find(pre, n, x0);
-    y = x0 - pre[rec.r];
-    rec.n = (int)(x1 - x0);
-    return rec;
-  };
-  if (p.path != kPathChunk) {  // a tile is a head
-    for (int w = tid; w < W; w += kPlanThreads) {
-      int64_t y;
-      WorkerRec rec = start_of(w, y);
-      const int64_t per_head = (pre[rec.r + 1] - pre[rec.r]) / p.Hkv;
-      rec.h = (int)(y / per_head);
-      rec.blk = (int)(y - rec.h * per_head);
-      p.workers[w] = rec;
+  __syncthreads();
+  for (int line = 0; line < 2; ++line) {
+    const int64_t* lp = pre + line * (n0 + 1);
+    const int32_t* lr = rid + line * (n0 + 1);
+    const int nl = line ? n1 : n0;
+    const int64_t c = cost[line];
+    // Fewer workers than fit the GPU where a share would be too small to pay
+    // for joining its partial results.
+    const int64_t share = line ? kChunkTileCost + 2 : kDecodeTileCost + 3;
+    const int W = (int)max((int64_t)(c > 0), min((int64_t)p.W_max[line], c / share));
+    if (tid == 0) {
+      p.hdr->cost[line] = c;
+      p.hdr->workers[line] = W;
     }
-    return;
-  }
-  for (int w = warp; w < W; w += kPlanThreads / 32) {
-    int64_t y;
-    WorkerRec rec = start_of(w, y);
-    const int r = rec.r, ql = cu[r + 1] - cu[r], kv = p.kv_len[r], nt = tiles_of(p, ql);
-    const int64_t per_head = (pre[r + 1] - pre[r]) / p.Hkv;
-    rec.h = (int)(y / per_head);
-    const int64_t z = y - rec.h * per_head;
-    // the tile that holds block z of the head: 32 tiles at a time
-    int off = 0;
-    for (int t0 = 0; t0 < nt; t0 += 32) {
-      const int nb = t0 + lane < nt ? tile_blocks(p, ql, kv, t0 + lane) : 0;
-      int incl = nb;
+    WorkerRec* out = p.workers + (line ? kMaxWorkers : 0);
+    auto start_of = [&](int w, int64_t& y) {  // the worker's request and its place there
+      WorkerRec rec{};
+      const int64_t x0 = c * w / W, x1 = c * (w + 1) / W;
+      const int i = find(lp, nl, x0), r = lr[i];
+      rec.q.r = r;
+      rec.q.q0 = cu[r];
+      rec.q.q_len = cu[r + 1] - cu[r];
+      rec.q.kv_len = p.kv_len[r];
+      rec.q.base = lp[i];
+      rec.q.per_head = (int)per[r];
+      rec.q.tiles = tiles_of(p, rec.q.q_len);
+      rec.at = i;
+      rec.n = (int)(x1 - x0);
+      y = x0 - lp[i];
+      rec.h = (int)(y / rec.q.per_head);
+      y -= (int64_t)rec.h * rec.q.per_head;
+      return rec;
+    };
+    if (!line) {  // a tile is a head
+      for (int w = tid; w < p.W_max[0]; w += kPlanThreads) {
+        WorkerRec rec{};
+        if (w < W) {
+          int64_t y;
+          rec = start_of(w, y);
+          rec.pos = (int)y;
+        }
+        out[w] = rec;
+      }
+      continue;
+    }
+    for (int w = warp; w < p.W_max[1]; w += kPlanThreads / 32) {
+      WorkerRec rec{};
+      if (w < W) {
+        int64_t z;
+        rec = start_of(w, z);
+        const int ql = rec.q.q_len, kv = rec.q.kv_len, nt = rec.q.tiles;
+        // the tile that holds place z of the head: 32 tiles at a time
+        int off = 0;
+        for (int t0 = 0; t0 < nt; t0 += 32) {
+          const int nb = t0 + lane < nt ? tile_places(p, 1, ql, kv, t0 + lane) : 0;
+          int incl = nb;
 #pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, s);
-        if (lane >= s) incl += o;
+          for (int s = 1; s < 32; s <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, s);
+            if (lane >= s) incl += o;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, off + incl > z);
+          if (hit) {
+            const int k = __ffs(hit) - 1;
+            rec.tile = t0 + k;
+            rec.tile_off = off + __shfl_sync(0xffffffffu, incl - nb, k);
+            break;
+          }
+          off += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        rec.pos = (int)(z - rec.tile_off);
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, off + incl > z);
-      if (hit) {
-        const int k = __ffs(hit) - 1;
-        rec.tile = t0 + k;
-        rec.tile_off = off + __shfl_sync(0xffffffffu, incl - nb, k);
-        break;
-      }
-      off += __shfl_sync(0xffffffffu, incl, 31);
+      if (lane == 0) out[w] = rec;
     }
-    rec.blk = (int)(z - rec.tile_off);
-    if (lane == 0) p.workers[w] = rec;
   }
 }
 
-// smem: cu [n + 1], taken [n + 1], given [n + 1] (int32), pre [n + 1] (int64)
+// smem: cu [n + 1], then CTA 0: per [n], pre [n + 2], rid [n + 2]; the others:
+// taken [n + 1], given [n + 1]
+constexpr size_t plan_smem(int n) { return (size_t)(n + 2) * 24; }
+
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ int64_t sm[32];
   const int n = p.n_req, tid = threadIdx.x, sh = p.page_shift;
-  int64_t* pre = reinterpret_cast<int64_t*>(raw);
-  int32_t* cu = reinterpret_cast<int32_t*>(pre + (n + 1));
-  int32_t* taken = cu + (n + 1);
-  int32_t* given = taken + (n + 1);
+  int64_t* per = reinterpret_cast<int64_t*>(raw);
+  int64_t* pre = per + n;
+  int32_t* rid = reinterpret_cast<int32_t*>(pre + n + 2);
+  int32_t* cu = rid + n + 2;
+  int32_t* taken = reinterpret_cast<int32_t*>(raw);
+  int32_t* given = taken + n + 1;
   const bool manage = p.old_len != nullptr;
   const bool first = blockIdx.x == 0;
 
@@ -189,9 +232,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     if (tid == 0) {
       p.hdr->base.status = 0;
       p.hdr->base.status_where = 0;
-      p.hdr->ok = 0;
     }
-    for (int i = tid; i < 2 * kMaxWorkers; i += kPlanThreads) p.hdr->count[i] = 0;
+    for (int i = tid; i < kMaxWorkers; i += kPlanThreads) p.hdr->count[i] = 0;
+    for (int i = tid; i < 2 * kMaxChunkWorkers; i += kPlanThreads) p.hdr->count_chunk[i] = 0;
   }
   // lengths in, checked
   int bad = 0;
@@ -219,13 +262,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     int64_t at = block_scan(mine, sm, &sum);
     n_taken = (int)(sum >> 32);
     n_given = (int)(sum & 0xFFFFFFFF);
-    for (int r = r0; r < r1; ++r) {
+    for (int r = r0; !first && r < r1; ++r) {
       taken[r] = (int)(at >> 32);
       given[r] = (int)(at & 0xFFFFFFFF);
       const int d = pages_of(p.kv_len[r], sh) - pages_of(p.old_len[r], sh);
       at += d > 0 ? (int64_t)d << 32 : (int64_t)-d;
     }
-    if (tid == 0) {
+    if (!first && tid == 0) {
       taken[n] = n_taken;
       given[n] = n_given;
     }
@@ -238,15 +281,16 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     if (tid == 0) {
       if (manage) *p.n_free_out = why ? *p.n_free : top - n_taken;
       if (why) report(&p.hdr->base, why, 0x700);
+      p.hdr->rows = why ? 0 : cu[n];
     }
     if (!why) {
-      split_work(p, cu, pre, sm);
-      if (tid == 0) p.hdr->ok = 1;
+      split_work(p, cu, per, pre, rid, sm);
+    } else {  // no worker has work
+      for (int w = tid; w < kMaxWorkers + kMaxChunkWorkers; w += kPlanThreads) p.workers[w] = WorkerRec{};
     }
-    if (gridDim.x > 1) return;
+    return;
   }
-  const int part = gridDim.x > 1 ? (int)blockIdx.x - 1 : 0, parts = max(1, (int)gridDim.x - 1);
-  const int i0 = part * kPlanThreads + tid, step = parts * kPlanThreads;
+  const int i0 = ((int)blockIdx.x - 1) * kPlanThreads + tid, step = ((int)gridDim.x - 1) * kPlanThreads;
   if (why) {
     if (p.slot_map)
       for (int t = i0; t < p.T; t += step) p.slot_map[t] = -1;
@@ -287,13 +331,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedParams& p, cudaStream_t st) {
-  const size_t smem = (size_t)(p.n_req + 1) * (8 + 3 * 4);
+  const size_t smem = plan_smem(p.n_req);
   static bool attr_set[64] = {};  // per device: raised once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kMaxReq + 1) * 20);
+    e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(kMaxReq));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }

@@ -129,14 +129,18 @@ class Step:
             return k.double(), v.double()
         return row_values(k, self.ks[page, h, off]), row_values(v, self.vs[page, h, off])
 
-    def reference(self, weight_rounding):
+    def reference(self, weight_rounding, weight_floor=0.0):
         """O, lse in 64 bits and how far a result may be from them.
 
         O: half a bf16 step of the value, plus what errs in the weights: their own rounding (`weight_rounding`
         relative, 0 where a second term holds what the first lost) and that of the scores in fp32.  A score is a sum
         of d products, each step of which rounds by at most 2^-23 of what is summed in magnitude (2^-23, not 2^-24:
         the matrix units may truncate); scaling, the subtraction of the reference and the exponential add 2^-22 of
-        the score's size and of the result."""
+        the score's size and of the result.
+
+        weight_floor: E4M3 weights kept in f16 as p 2^(e - E + 7) (p: relative to a reference that the sum is at least
+        1 of; e: the key's exponent, E: the largest) round by at most 2^-25 below f16's normal range, that is by 2^-32
+        of 2^E times the code, at most 448: weight_floor = 2^-32 for each of the keys."""
         T, H, d, G = self.T, self.H, self.d, self.H // self.Hkv
         O = torch.full((T, H, d), 77.0, dtype=torch.float64, device=self.dev)
         lse = torch.full((H, T), 77.0, dtype=torch.float64, device=self.dev)
@@ -165,9 +169,23 @@ class Step:
                     err = size * (d + 4) * 2.0 ** -23 + 2.0 ** -21  # of a score, and so relative of a weight
                     rel = (w * err).sum(1, keepdim=True)  # of the sum
                     A = (w * (err + weight_rounding)) @ V.abs() + rel * (w @ V.abs())
-                    tO[at, hq] = HALF_BF16 * O[at, hq].abs() + 1.02 * A + 2.0 ** -126
+                    low = weight_floor * kv * 448.0 * float(self.largest_scale(r, h)) if weight_floor and kv else 0.0
+                    tO[at, hq] = HALF_BF16 * O[at, hq].abs() + 1.02 * A + low + 2.0 ** -126
                     tl[hq, at] = rel[:, 0] * 1.02 + 2.0 ** -22 * lse[hq, at].abs().nan_to_num(0, 0, 0) + 2.0 ** -20
         return O, lse, tO, tl
+
+    def largest_scale(self, r, h):
+        j = torch.arange(self.kv_len[r])
+        page = torch.tensor(self.table_host[r])[j // self.ps].to(self.dev)
+        b = self.vs[page, h, (j % self.ps).to(self.dev)].int()
+        return 2.0 ** (int(b[b != 255].max()) - 127)
+
+    def rounding(self):
+        """(weight_rounding, weight_floor): the tile kernel rounds the weights to bf16, the decode kernel to two bf16
+        terms over a bf16 cache and to f16 over an E4M3 one."""
+        if self.chunk_path():
+            return HALF_BF16, 0.0
+        return (HALF_BF16 ** 2, 0.0) if self.cache == "bf16" else (torch.finfo(torch.float16).eps / 2, 2.0 ** -32)
 
     def chunk_path(self):
         return (max(1, self.prob.max_q or self.T)) * (self.H // self.Hkv) > 16
@@ -177,8 +195,7 @@ class Step:
         torch.cuda.synchronize()
         st = fl.flamia_get_device_status(self.ws)
         assert st == fl.OK, fl.status_string(st)
-        # the tile kernel rounds the weights to bf16 once, the decode kernel to two bf16 terms
-        wO, wl, tO, tl = self.reference(HALF_BF16 if self.chunk_path() else HALF_BF16 ** 2)
+        wO, wl, tO, tl = self.reference(*self.rounding())
         compare(O, wO, tO, "O")
         compare(lse, wl, tl, "lse")
 
