@@ -264,24 +264,36 @@ def flamia_paged_workspace_size(prob: Paged) -> int:
     return int(load_library().flamia_paged_workspace_size(ctypes.byref(prob)))
 
 
+def _paged_call(name, ws, stream, *args):
+    """One launch on the device of `ws`, on `stream` or that device's current stream.  These calls are short: their
+    host time is what a small serving step costs."""
+    import torch
+    dev = ws.get_device()
+    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            st = getattr(_lib or load_library(), name)(*args, ws.data_ptr(), ws.nbytes, s)
+    else:
+        st = getattr(_lib or load_library(), name)(*args, ws.data_ptr(), ws.nbytes, s)
+    if st:
+        raise FlamiaError(st, name)
+
+
 def flamia_paged_plan(prob: Paged, ws, slot_map=None, old_len=None, free_pages=None, n_free=None, n_free_out=None,
                       stream=None):
     """Once per step: block table, free stack, slot map and the attention's work split."""
-    _check(load_library().flamia_paged_plan(ctypes.byref(prob), _ptr(slot_map), _ptr(old_len), _ptr(free_pages),
-                                            _ptr(n_free), _ptr(n_free_out), _ptr(ws), ws.numel() * ws.element_size(),
-                                            _stream(stream)), "flamia_paged_plan")
+    _paged_call("flamia_paged_plan", ws, stream, prob, _ptr(slot_map), _ptr(old_len), _ptr(free_pages), _ptr(n_free),
+                _ptr(n_free_out))
 
 
 def flamia_paged_append(prob: Paged, k, v, slot_map, cache: Cache, ws, stream=None):
-    _check(load_library().flamia_paged_append(ctypes.byref(prob), _ptr(k), _ptr(v), _ptr(slot_map),
-                                              ctypes.byref(cache), _ptr(ws), ws.numel() * ws.element_size(),
-                                              _stream(stream)), "flamia_paged_append")
+    """The step's K and V rows into their slots of one layer's cache."""
+    _paged_call("flamia_paged_append", ws, stream, prob, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), cache)
 
 
 def flamia_paged_fwd(prob: Paged, q, cache: Cache, O, lse, ws, stream=None):
-    _check(load_library().flamia_paged_fwd(ctypes.byref(prob), _ptr(q), ctypes.byref(cache), _ptr(O), _ptr(lse),
-                                           _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "flamia_paged_fwd")
+    """Attention of the step's queries over one layer's cache (lse may be None)."""
+    _paged_call("flamia_paged_fwd", ws, stream, prob, q.data_ptr(), cache, O.data_ptr(), _ptr(lse))
 
 
 @dataclass

@@ -4,61 +4,58 @@
 // and written as one contiguous run of its page: rounded to bf16, or as E4M3
 // codes with the row's own no-clamp exponent, whose maximum the group forms by
 // shuffles.  Every byte is read and written once; HBM bound at large sizes, a
-// launch's latency at small ones.  A thread keeps kUnroll rows in flight.
+// launch's latency at small ones.  A CTA takes a few consecutive tokens and
+// heads at a time, so that what it reads is contiguous (tokens of all heads)
+// and so is what it writes (a head's tokens); a thread keeps kHeads rows in
+// flight.
 #include "paged.cuh"
 
 namespace flamia {
 
 namespace {
 
-constexpr int kThreads = 256, kUnroll = 4;
+constexpr int kThreads = 256, kHeads = 4;
 
 template <int D, bool E4M3, bool BF16>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParams p) {
-  constexpr int kEl = BF16 ? 8 : 4;        // elements a lane holds
-  constexpr int kLanes = D / kEl;          // lanes of a row (8, 16 or 32)
-  constexpr int kRows = kThreads / kLanes; // rows a CTA reads at a time
-  const int sub = threadIdx.x % kLanes;
-  const int64_t rows = (int64_t)p.hdr->rows * p.Hkv, all = 2 * rows;  // K's rows, then V's
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParams p, int tiles, int head_groups) {
+  constexpr int kEl = BF16 ? 8 : 4;         // elements a lane holds
+  constexpr int kLanes = D / kEl;           // lanes of a row (8, 16 or 32)
+  constexpr int kToks = kThreads / kLanes;  // tokens of a tile
+  const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int rows = p.hdr->rows;
   const int64_t n_slots = (int64_t)p.n_pages << p.page_shift;
-  const int64_t step = (int64_t)gridDim.x * kRows * kUnroll;
-  // whole groups of lanes stay together: a row past the end is not loaded or stored
-  for (int64_t base = (int64_t)blockIdx.x * kRows * kUnroll; base < all; base += step) {
-    uint4 x[kUnroll];
-    int slot[kUnroll], head[kUnroll];
-    bool is_v[kUnroll];
+  // units: (token tile, K or V, head group)
+  for (int unit = blockIdx.x; unit < tiles * 2 * head_groups; unit += gridDim.x) {
+    const int rest = unit / head_groups, h0 = (unit - rest * head_groups) * kHeads;
+    const bool is_v = rest & 1;
+    const int t = (rest >> 1) * kToks + group;
+    const bool in = t < p.T;  // whole groups of lanes
+    int64_t slot = in ? __ldg(p.slots + t) : -1;
+    uint4 x[kHeads];
+    const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v_new : p.k_new) +
+                         ((int64_t)t * p.kv_stride + (int64_t)h0 * D + sub * kEl) * (BF16 ? 2 : 4);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = base + u * kRows + threadIdx.x / kLanes;
-      slot[u] = -1;
-      head[u] = 0;
-      is_v[u] = i >= rows;
+    for (int u = 0; u < kHeads; ++u) {
       x[u] = make_uint4(0, 0, 0, 0);
-      if (i < all) {
-        const int64_t j = is_v[u] ? i - rows : i;
-        const int t = (int)(j / p.Hkv);
-        head[u] = (int)(j - (int64_t)t * p.Hkv);
-        slot[u] = __ldg(p.slots + t);
-        const uint8_t* src = static_cast<const uint8_t*>(is_v[u] ? p.v_new : p.k_new);
-        const int64_t off = (int64_t)t * p.kv_stride + head[u] * D + sub * kEl;
-        x[u] = __ldg(reinterpret_cast<const uint4*>(src + off * (BF16 ? 2 : 4)));
-      }
+      if (in && h0 + u < p.Hkv) x[u] = __ldg(reinterpret_cast<const uint4*>(src + u * D * (BF16 ? 2 : 4)));
     }
+    if (t >= rows) slot = -1;  // behind the last request
+    if (slot >= n_slots || slot < -1) {
+      report(&p.hdr->base, FLAMIA_ERR_BAD_PAGE, 0x711);
+      slot = -1;
+    }
+    const int64_t page = slot >> p.page_shift;
+    const int at = (int)(slot & (p.page_size - 1));
+    uint8_t* pool = (is_v ? p.v : p.k) + page * p.page_bytes;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kHeads; ++u) {
+      const bool write = slot >= 0 && h0 + u < p.Hkv;
+      const int64_t in_page = (int64_t)(h0 + u) * p.page_size + at;
       const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
       float f[kEl];
 #pragma unroll
       for (int e = 0; e < kEl; ++e)
         f[e] = BF16 ? __uint_as_float((e & 1) ? (w[e / 2] & 0xFFFF0000u) : (w[e / 2] << 16)) : __uint_as_float(w[e & 3]);
-      int64_t row = slot[u];
-      if (row >= n_slots || row < -1) {
-        report(&p.hdr->base, FLAMIA_ERR_BAD_PAGE, 0x711);
-        row = -1;
-      }
-      const int64_t page = row >> p.page_shift;
-      const int64_t in_page = (int64_t)head[u] * p.page_size + (row & (p.page_size - 1));
-      uint8_t* pool = is_v[u] ? p.v : p.k;
       if constexpr (E4M3) {
         uint32_t top = 0;  // the magnitudes order like their bits, infinities and NaN last
 #pragma unroll
@@ -73,15 +70,15 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParam
         for (int k = 0; k < kEl / 4; ++k)
           c[k] = finite ? pack_e4m3x4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv)
                         : 0x7F7F7F7Fu;
-        if (row >= 0) {
-          uint8_t* dst = pool + page * p.page_bytes + in_page * D + sub * kEl;
+        if (write) {
+          uint8_t* dst = pool + in_page * D + sub * kEl;
           if constexpr (kEl == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[kEl / 4 - 1]);
           else *reinterpret_cast<uint32_t*>(dst) = c[0];
           if (sub == 0)
-            (is_v[u] ? p.v_scales : p.k_scales)[page * p.Hkv * p.page_size + in_page] = (uint8_t)(finite ? e + 127 : 255);
+            (is_v ? p.v_scales : p.k_scales)[page * p.Hkv * p.page_size + in_page] = (uint8_t)(finite ? e + 127 : 255);
         }
-      } else if (row >= 0) {
-        uint8_t* dst = pool + page * p.page_bytes + (in_page * D + sub * kEl) * 2;
+      } else if (write) {
+        uint8_t* dst = pool + (in_page * D + sub * kEl) * 2;
         if constexpr (BF16) *reinterpret_cast<uint4*>(dst) = x[u];
         else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
       }
@@ -91,9 +88,11 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParam
 
 template <int D, bool E4M3, bool BF16>
 cudaError_t launch(const PagedParams& p, int sms, cudaStream_t st) {
-  constexpr int kPer = kThreads / (D / (BF16 ? 8 : 4)) * kUnroll;
-  const int64_t need = (2 * (int64_t)p.T * p.Hkv + kPer - 1) / kPer, most = (int64_t)sms * 8;
-  paged_append_kernel<D, E4M3, BF16><<<(int)(need < most ? need : most), kThreads, 0, st>>>(p);
+  constexpr int kToks = kThreads / (D / (BF16 ? 8 : 4));
+  const int tiles = (p.T + kToks - 1) / kToks, groups = (p.Hkv + kHeads - 1) / kHeads;
+  const int64_t units = (int64_t)tiles * 2 * groups, most = (int64_t)sms * 8;
+  if (units > INT32_MAX) return cudaErrorInvalidValue;
+  paged_append_kernel<D, E4M3, BF16><<<(int)(units < most ? units : most), kThreads, 0, st>>>(p, tiles, groups);
   return cudaGetLastError();
 }
 template <int D>

@@ -40,8 +40,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 4096;  // bytes of a chunk's K (or V)
 constexpr int kRingB = kWarps * 4 * kUnit;  // two chunks a warp
-// 3 CTAs of an SM: their rings take 192 of its 228 KB
-constexpr int kCtas = 3;
+// 2 CTAs of an SM (3: 59 against 57 us on 65,522 tokens; more partials to join)
+constexpr int kCtas = 2;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {

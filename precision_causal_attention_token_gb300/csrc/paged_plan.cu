@@ -58,6 +58,12 @@ __device__ __forceinline__ int find(const I* pre, int n, int64_t i) {
   return lo;
 }
 
+// Quotient of non-negative numbers: in 32 bits where they fit (a 64-bit
+// division is a hundred instructions).
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The line of a request with new tokens.
 __device__ __forceinline__ int line_of(const PagedParams& p, int q_len) { return (int64_t)q_len * p.G > p.small_rows; }
 __device__ __forceinline__ int tiles_of(const PagedParams& p, int q_len) {
@@ -77,27 +83,29 @@ __device__ __forceinline__ int tile_places(const PagedParams& p, int line, int q
 __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* per, int64_t* pre, int32_t* rid, int64_t* sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.n_req;
   constexpr int kSerial = 4;  // tiles that a thread adds up alone; longer chunks take a warp
+  __shared__ int n_long;
+  if (tid == 0) n_long = 0;
+  __syncthreads();
   for (int r = tid; r < n; r += kPlanThreads) {
     const int ql = cu[r + 1] - cu[r], kv = p.kv_len[r], nt = tiles_of(p, ql), line = line_of(p, ql);
     int64_t sum = 0;
-    if (nt <= kSerial)
+    if (nt <= kSerial) {
       for (int i = 0; i < nt; ++i) sum += tile_places(p, line, ql, kv, i);
-    per[r] = sum;
+      per[r] = sum;
+    } else {
+      rid[atomicAdd(&n_long, 1)] = r;
+    }
   }
   __syncthreads();
-  if (p.path == kPathChunk) {
-    for (int r = warp; r < n; r += kPlanThreads / 32) {
-      const int ql = cu[r + 1] - cu[r], nt = tiles_of(p, ql);
-      if (nt <= kSerial) continue;
-      const int kv = p.kv_len[r];
-      int64_t sum = 0;
-      for (int i = lane; i < nt; i += 32) sum += tile_places(p, 1, ql, kv, i);
+  for (int k = warp; k < n_long; k += kPlanThreads / 32) {
+    const int r = rid[k], ql = cu[r + 1] - cu[r], kv = p.kv_len[r], nt = tiles_of(p, ql);
+    int64_t sum = 0;
+    for (int i = lane; i < nt; i += 32) sum += tile_places(p, 1, ql, kv, i);
 #pragma unroll
-      for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      if (lane == 0) per[r] = sum;
-    }
-    __syncthreads();
+    for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    if (lane == 0) per[r] = sum;
   }
+  __syncthreads();
   const int seg = (n + kPlanThreads - 1) / kPlanThreads, r0 = min(n, tid * seg), r1 = min(n, r0 + seg);
   int64_t cnt = 0, mine[2] = {0, 0}, cost[2], all;
   for (int r = r0; r < r1; ++r) {
@@ -143,7 +151,7 @@ __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* per
     // Fewer workers than fit the GPU where a share would be too small to pay
     // for joining its partial results.
     const int64_t share = line ? kChunkTileCost + 2 : kDecodeTileCost + 3;
-    const int W = (int)max((int64_t)(c > 0), min((int64_t)p.W_max[line], c / share));
+    const int W = (int)max((int64_t)(c > 0), min((int64_t)p.W_max[line], quot(c, share)));
     if (tid == 0) {
       p.hdr->cost[line] = c;
       p.hdr->workers[line] = W;
@@ -151,7 +159,7 @@ __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* per
     WorkerRec* out = p.workers + (line ? kMaxWorkers : 0);
     auto start_of = [&](int w, int64_t& y) {  // the worker's request and its place there
       WorkerRec rec{};
-      const int64_t x0 = c * w / W, x1 = c * (w + 1) / W;
+      const int64_t x0 = quot(c * w, W), x1 = quot(c * (w + 1), W);
       const int i = find(lp, nl, x0), r = lr[i];
       rec.q.r = r;
       rec.q.q0 = cu[r];
@@ -163,50 +171,45 @@ __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* per
       rec.at = i;
       rec.n = (int)(x1 - x0);
       y = x0 - lp[i];
-      rec.h = (int)(y / rec.q.per_head);
+      rec.h = (int)quot(y, rec.q.per_head);
       y -= (int64_t)rec.h * rec.q.per_head;
       return rec;
     };
-    if (!line) {  // a tile is a head
-      for (int w = tid; w < p.W_max[0]; w += kPlanThreads) {
-        WorkerRec rec{};
-        if (w < W) {
-          int64_t y;
-          rec = start_of(w, y);
-          rec.pos = (int)y;
-        }
-        out[w] = rec;
-      }
-      continue;
-    }
-    for (int w = warp; w < p.W_max[1]; w += kPlanThreads / 32) {
+    for (int w = tid; w < p.W_max[line]; w += kPlanThreads) {
       WorkerRec rec{};
       if (w < W) {
-        int64_t z;
-        rec = start_of(w, z);
-        const int ql = rec.q.q_len, kv = rec.q.kv_len, nt = rec.q.tiles;
-        // the tile that holds place z of the head: 32 tiles at a time
-        int off = 0;
-        for (int t0 = 0; t0 < nt; t0 += 32) {
-          const int nb = t0 + lane < nt ? tile_places(p, 1, ql, kv, t0 + lane) : 0;
-          int incl = nb;
-#pragma unroll
-          for (int s = 1; s < 32; s <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, s);
-            if (lane >= s) incl += o;
-          }
-          const unsigned hit = __ballot_sync(0xffffffffu, off + incl > z);
-          if (hit) {
-            const int k = __ffs(hit) - 1;
-            rec.tile = t0 + k;
-            rec.tile_off = off + __shfl_sync(0xffffffffu, incl - nb, k);
-            break;
-          }
-          off += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        rec.pos = (int)(z - rec.tile_off);
+        int64_t y;
+        rec = start_of(w, y);
+        rec.pos = (int)y;  // of the head, which is a tile in line 0
       }
-      if (lane == 0) out[w] = rec;
+      out[w] = rec;
+    }
+    if (!line) continue;
+    // line 1: the tile that holds the place, 32 tiles at a time
+    __syncthreads();
+    for (int w = warp; w < W; w += kPlanThreads / 32) {
+      const int ql = out[w].q.q_len, kv = out[w].q.kv_len, nt = out[w].q.tiles, z = out[w].pos;
+      if (nt == 1) continue;
+      int off = 0;
+      for (int t0 = 0; t0 < nt; t0 += 32) {
+        const int nb = t0 + lane < nt ? tile_places(p, 1, ql, kv, t0 + lane) : 0;
+        int incl = nb;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, incl, s);
+          if (lane >= s) incl += o;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, off + incl > z);
+        if (hit) {
+          if (lane == __ffs(hit) - 1) {
+            out[w].tile = t0 + lane;
+            out[w].tile_off = off + incl - nb;
+            out[w].pos = z - (off + incl - nb);
+          }
+          break;
+        }
+        off += __shfl_sync(0xffffffffu, incl, 31);
+      }
     }
   }
 }
