@@ -370,7 +370,7 @@ flamia_status_t flamia_plan_noalloc(const flamia_problem_t* p, int2* fwd_items, 
  *                map; rows behind cu_q[n_req] <= T belong to no request and
  *                are neither read nor written (their slots are set to -1).
  *   max_q        upper bound of a request's new tokens, 1..T (0 selects T).  The
- *                kernel is chosen by it: up to max_q * H / Hkv = 16 rows a
+ *                kernel is chosen by it: up to max_q * H / Hkv = 32 rows a
  *                (request, key/value head) take the decode kernel.
  *   H, Hkv, d    query heads, key/value heads (H % Hkv == 0), head dimension
  *                64 or 128

@@ -23,7 +23,7 @@ namespace flamia {
 // Requests with few rows (one new token, a few drafted ones) are served by
 // the decode kernel, the others by the chunk kernel: two lines.
 // ---------------------------------------------------------------------------
-enum { kPathDecode8 = 0, kPathDecode16 = 1, kPathChunk = 2 };
+enum { kPathDecode8 = 0, kPathDecode16 = 1, kPathDecode32 = 2, kPathChunk = 3 };
 constexpr int kDecodeBlk = 64, kChunkBlk = 128, kChunkRows = 256;
 // What a tile costs beside its blocks, in blocks: its queries, first loads and
 // result (decode: 5 us of about 1 us a block)
@@ -69,7 +69,7 @@ struct PagedLayout {
 struct PagedParams {
   int n_req, T, max_q, H, Hkv, G, page_size, page_shift, n_pages, max_pages, causal, path;
   int W_max[2];   // workers at most, of each line
-  int small_rows; // requests of up to so many rows go to the decode kernel (8, 16; 0: none)
+  int small_rows; // requests of up to so many rows go to the decode kernel (8, 16, 32; 0: none)
   int tile_toks;  // tokens of a tile (kPathChunk)
   float c_log2;   // softmax_scale * log2(e)
   const int32_t* cu_q;

@@ -16,12 +16,12 @@ bool dev4(const void* p) { return p && aligned(p, 4); }
 
 int max_q_of(const flamia_paged_t* p) { return p->max_q ? p->max_q : p->T; }
 
-// Up to 16 query rows of a key/value head: the decode kernel, whose MMAs have
-// 8 or 16 columns for them and which is bound by the cache's bytes alone.
-// More rows: 256-row tiles on the tensor cores.
+// Up to 32 query rows of a key/value head: the decode kernel, whose MMAs have
+// 8, 16 or 32 columns for them and which is bound by the cache's bytes.  More
+// rows: 256-row tiles on the tensor cores.
 int path_of(const flamia_paged_t* p) {
   const int64_t rows = (int64_t)max_q_of(p) * (p->H / p->Hkv);
-  return rows <= 8 ? kPathDecode8 : rows <= 16 ? kPathDecode16 : kPathChunk;
+  return rows <= 8 ? kPathDecode8 : rows <= 16 ? kPathDecode16 : rows <= 32 ? kPathDecode32 : kPathChunk;
 }
 
 flamia_status_t validate(const flamia_paged_t* p) {
@@ -50,7 +50,7 @@ PagedLayout layout(const flamia_paged_t& p) {
   L.path = path_of(&p);
   // the decode kernel's and the chunk kernel's partials, one after the other
   // on the stream, lie in the same place
-  const size_t dec = 2 * (size_t)kMaxWorkers * (L.path == kPathDecode8 ? 8 : 16);
+  const size_t dec = 2 * (size_t)kMaxWorkers * (L.path == kPathDecode8 ? 8 : L.path == kPathDecode32 ? 32 : 16);
   const size_t chunk = L.path == kPathChunk ? 2 * (size_t)kMaxChunkWorkers * kChunkRows : 0;
   const size_t rows = dec > chunk ? dec : chunk;
   auto a256 = [](size_t x) { return (x + 255) & ~size_t(255); };
@@ -89,7 +89,8 @@ flamia_status_t fill(const flamia_paged_t* p, void* ws, size_t ws_bytes, PagedPa
   a->W_max[1] = sms < kMaxChunkWorkers ? sms : kMaxChunkWorkers;
   // which requests the decode kernel takes: all of a call with few rows each;
   // in a call with chunks those of up to 8 rows (16 where a token alone has more than 8)
-  a->small_rows = L.path == kPathDecode8 ? 8 : L.path == kPathDecode16 ? 16 : a->G <= 8 ? 8 : a->G <= 16 ? 16 : 0;
+  a->small_rows = L.path == kPathDecode8 ? 8 : L.path == kPathDecode16 ? 16 : L.path == kPathDecode32 ? 32
+                  : a->G <= 8 ? 8 : a->G <= 16 ? 16 : 0;
   a->tile_toks = kChunkRows / a->G;
   const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)p->d);
   a->c_log2 = scale * 1.44269504088896341f;

@@ -1,5 +1,5 @@
 // paged_decode.cu — attention of few query rows over a paged cache: one token
-// per request, or a few drafted ones (up to 16 rows of a key/value head).
+// per request, or a few drafted ones (up to 32 rows of a key/value head).
 //
 // Every cached byte is used by all rows of its head at once and needed once,
 // so the kernel is bound by HBM and its work is to keep loads in flight.  A
@@ -100,6 +100,9 @@ struct Decode {
   static constexpr int kVW = kRowB / 32;            // 32-bit words of a V row per lane, 8 lanes side by side
   static constexpr int kMT = D / 16;                // m16 channel tiles
   static constexpr int kQ = 8 * NT;                 // query rows
+  // 32 rows: the queries' fragments stay in shared memory, the registers hold
+  // the 128 accumulators
+  static constexpr bool kQShared = NT == 4;
   // Which 16-byte pieces of a row trade places (xor), so that the eight lanes
   // of a shared-memory phase read eight different 16-byte columns of the
   // banks' 128 bytes.  K: rows g, g + 1, four pieces side by side; V: rows 2t
@@ -112,7 +115,8 @@ struct Decode {
 };
 
 // Dynamic shared memory: the warps' rings and, after a tile's last key, the
-// join's buffers in the same place; then the E4M3 scale bytes.
+// join's buffers in the same place; then the E4M3 scale bytes and, for 32
+// rows, the queries.
 template <int D, int NT>
 struct Join {
   float o[kWarps][8 * NT][D + 4];
@@ -121,6 +125,15 @@ struct Join {
 struct Scales {
   uint8_t b[kWarps][2][2][64];  // [warp][chunk mod 2][K, V][key]
 };
+template <int D>
+struct Queries {
+  uint2 q[4][D / 16][32];  // [8 rows][K step][lane]
+  float scale[32];
+};
+template <int D, int NT>
+constexpr size_t ring_bytes() {
+  return sizeof(Join<D, NT>) > kRingB ? (sizeof(Join<D, NT>) + 15) / 16 * 16 : kRingB;
+}
 
 template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const PagedParams p) {
@@ -128,7 +141,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int sm_last;
   Join<D, NT>& sm = *reinterpret_cast<Join<D, NT>*>(smem);
-  Scales& scl = *reinterpret_cast<Scales*>(smem + kRingB);
+  Scales& scl = *reinterpret_cast<Scales*>(smem + ring_bytes<D, NT>());
+  [[maybe_unused]] Queries<D>& qsm = *reinterpret_cast<Queries<D>*>(smem + ring_bytes<D, NT>() + sizeof(Scales));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   PagedHeader* hdr = p.hdr;
   const int w = blockIdx.x;
@@ -146,12 +160,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
    if (nb > 0) {
     const int rows = rq.q_len * p.G;
     // ------------------------------------------------ queries (B operand) and column limits
-    uint32_t qf[NT][D / 16][2];
-    float cq[NT][2];  // score factor of columns 2t, 2t + 1
-    int vis[NT][2];   // keys that they see
-    int vis_min = kend;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    // fragments of rows 8 nt .. 8 nt + 7, and the score factor of row g of them
+    auto load_q = [&](int nt, uint32_t (&f)[D / 16][2]) {
       const int row = 8 * nt + g;
       const int tok = row / p.G, hq = h * p.G + (row - tok * p.G);
       const __nv_bfloat16* src = p.q + (int64_t)(rq.q0 + tok) * p.q_stride + (int64_t)hq * D;
@@ -161,17 +171,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         const int d = FP8 ? (ks >> 2) * 64 + t * 16 + (ks & 3) * 4 : (ks >> 1) * 32 + t * 8 + (ks & 1) * 4;
         uint2 x = make_uint2(0, 0);
         if (row < rows) x = __ldg(reinterpret_cast<const uint2*>(src + d));
-        qf[nt][ks][0] = x.x;
-        qf[nt][ks][1] = x.y;
+        f[ks][0] = x.x;
+        f[ks][1] = x.y;
       }
-      float scale = p.c_log2;  // of row g
+      float scale = p.c_log2;
       if constexpr (FP8) {
         uint32_t top = 0;  // largest magnitude's bits
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            top = max(top, max(qf[nt][ks][i] & 0x7FFFu, (qf[nt][ks][i] >> 16) & 0x7FFFu));
+          for (int i = 0; i < 2; ++i) top = max(top, max(f[ks][i] & 0x7FFFu, (f[ks][i] >> 16) & 0x7FFFu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // exponent field E: the row's largest element is below 2^(E - 126);
@@ -182,14 +191,30 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const __half2 v = __floats2half2_rn(bf16_lo(qf[nt][ks][i]) * up, bf16_hi(qf[nt][ks][i]) * up);
-            qf[nt][ks][i] = *reinterpret_cast<const uint32_t*>(&v);
-          }
+          for (int i = 0; i < 2; ++i) f[ks][i] = pack_f16x2(bf16_lo(f[ks][i]) * up, bf16_hi(f[ks][i]) * up);
       }
+      return scale;
+    };
+    [[maybe_unused]] uint32_t qf[C::kQShared ? 1 : NT][D / 16][2];
+    float cq[NT][2];  // score factor of columns 2t, 2t + 1
+    int vis[NT][2];   // keys that they see
+    int vis_min = kend;
+    if constexpr (C::kQShared) {  // a warp each
+      static_assert(kWarps == NT || !C::kQShared, "a warp for every eight rows");
+      uint32_t f[D / 16][2];
+      const float scale = load_q(warp, f);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) qsm.q[warp][ks][lane] = make_uint2(f[ks][0], f[ks][1]);
+      if (t == 0) qsm.scale[8 * warp + g] = scale;
+      __syncthreads();
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float scale = 0.f;
+      if constexpr (!C::kQShared) scale = load_q(nt, qf[nt]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        cq[nt][e] = __shfl_sync(0xffffffffu, scale, 4 * (2 * t + e));
+        cq[nt][e] = C::kQShared ? qsm.scale[8 * nt + 2 * t + e] : __shfl_sync(0xffffffffu, scale, 4 * (2 * t + e));
         const int c = 8 * nt + 2 * t + e;
         const int n = visible_keys(p.causal, rq.q_len, rq.kv_len, c / p.G);
         vis[nt][e] = c < rows ? n : kend;  // columns past the rows hold zeros
@@ -291,29 +316,48 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
       __syncwarp();  // the bytes are other lanes' copies
       float s[C::kSub][NT][4];
 #pragma unroll
-      for (int i = 0; i < C::kSub; ++i) {
+      for (int i = 0; i < C::kSub; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.f;
+      // the queries' fragments of a K step serve all key tiles
+      constexpr int kU = FP8 ? 4 : 2;  // K steps of a 64-byte piece
 #pragma unroll
-        for (int j = 0; j < C::kKJ; ++j) {
+      for (int j = 0; j < C::kKJ; ++j) {
+        uint32_t x[C::kSub][4], y[C::kSub][4];
+#pragma unroll
+        for (int i = 0; i < C::kSub; ++i) {
           const uint32_t a = kb + (16 * i + g) * C::kRowB + (((4 * j + t) ^ C::swap(false, g)) << 4);  // g and g + 8 alike
           const uint4 u0 = lds16(a), u1 = lds16(a + 8 * C::kRowB);
-          const uint32_t x[4] = {u0.x, u0.y, u0.z, u0.w}, y[4] = {u1.x, u1.y, u1.z, u1.w};
-          if constexpr (FP8) {
+          x[i][0] = u0.x, x[i][1] = u0.y, x[i][2] = u0.z, x[i][3] = u0.w;
+          y[i][0] = u1.x, y[i][1] = u1.y, y[i][2] = u1.z, y[i][3] = u1.w;
+        }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint32_t a0, a1, a2, a3;
-              e4m3x4_to_f16(x[u], a0, a2);
-              e4m3x4_to_f16(y[u], a1, a3);
+        for (int u = 0; u < kU; ++u) {
+          uint32_t b[NT][2];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(s[i][nt], a0, a1, a2, a3, qf[nt][4 * j + u][0], qf[nt][4 * j + u][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (C::kQShared) {
+              const uint2 q = qsm.q[nt][kU * j + u][lane];
+              b[nt][0] = q.x;
+              b[nt][1] = q.y;
+            } else {
+              b[nt][0] = qf[nt][kU * j + u][0];
+              b[nt][1] = qf[nt][kU * j + u][1];
             }
-          } else {
+          }
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+          for (int i = 0; i < C::kSub; ++i) {
+            if constexpr (FP8) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(x[i][u], a0, a2);
+              e4m3x4_to_f16(y[i][u], a1, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(s[i][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+            } else {
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_bf16(s[i][nt], x[2 * u], y[2 * u], x[2 * u + 1], y[2 * u + 1], qf[nt][2 * j + u][0], qf[nt][2 * j + u][1]);
+                mma_bf16(s[i][nt], x[i][2 * u], y[i][2 * u], x[i][2 * u + 1], y[i][2 * u + 1], b[nt][0], b[nt][1]);
+            }
           }
         }
       }
@@ -620,34 +664,32 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
       __syncthreads();
       write = sm_last;
       if (write) {
-        // The partials' references and sums come in one round, then each
-        // row's threads form the weights together and add up their channels,
-        // eight partials in flight (one after the other, 57 of them took 20 us).
+        // A row's threads form the partials' weights together, then add up
+        // their channels, eight partials in flight (one after the other, 57 of
+        // them took 20 us).
         __threadfence();
         auto slot_of = [&](int i) { return (int64_t)(i == 0 ? 2 * w0 + 1 : 2 * (w0 + i)); };
-        float2* ml = reinterpret_cast<float2*>(smem);  // [n][kQ]; the join's buffers are free
-        for (int x = tid; x < n * C::kQ; x += kThreads) ml[x] = __ldcg(p.part_ml + slot_of(x / C::kQ) * C::kQ + x % C::kQ);
-        __syncthreads();
+        float* wt = reinterpret_cast<float*>(smem);  // [n][kQ]; the join's buffers are free
         const int me = tid % kSpan;
         M = -INFINITY;
-        for (int i = me; i < n; i += kSpan) M = fmaxf(M, ml[i * C::kQ + row].x);
+        for (int i = me; i < n; i += kSpan) M = fmaxf(M, __ldcg(p.part_ml + slot_of(i) * C::kQ + row).x);
 #pragma unroll
         for (int k = kSpan / 2; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
         L = 0.f;
         for (int i = me; i < n; i += kSpan) {
-          const float2 x = ml[i * C::kQ + row];
+          const float2 x = __ldcg(p.part_ml + slot_of(i) * C::kQ + row);
           const float a = x.x == M ? 1.f : ex2_approx(x.x - M);
           L += a * x.y;
-          ml[i * C::kQ + row].x = a;
+          wt[i * C::kQ + row] = a;
         }
 #pragma unroll
         for (int k = kSpan / 2; k; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-#pragma unroll 8
+#pragma unroll (kPer <= 16 ? 8 : 2)
         for (int i = 0; i < n; ++i) {
-          const float a = ml[i * C::kQ + row].x;
+          const float a = wt[i * C::kQ + row];
           const float* src = p.part_o + (slot_of(i) * C::kQ + row) * D + d0;
 #pragma unroll
           for (int k = 0; k < kPer; k += 4) {
@@ -690,8 +732,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
 
 template <int D, bool FP8, int NT>
 cudaError_t launch(const PagedParams& p, cudaStream_t st) {
-  constexpr size_t smem = kRingB + (FP8 ? sizeof(Scales) : 0);
-  static_assert(sizeof(Join<D, NT>) <= kRingB && sizeof(float2) * kMaxWorkers * 8 * NT <= kRingB, "these lie in the rings' place");
+  constexpr size_t smem = ring_bytes<D, NT>() + sizeof(Scales) + (NT == 4 ? sizeof(Queries<D>) : 0);
+  static_assert(sizeof(float) * kMaxWorkers * 8 * NT <= ring_bytes<D, NT>(), "the weights lie in the rings' place");
   static bool attr_set[64] = {};  // per device: raised once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -706,7 +748,7 @@ cudaError_t launch(const PagedParams& p, cudaStream_t st) {
 }
 template <int D, bool FP8>
 cudaError_t launch_n(const PagedParams& p, cudaStream_t st) {
-  return p.small_rows == 8 ? launch<D, FP8, 1>(p, st) : launch<D, FP8, 2>(p, st);
+  return p.small_rows == 8 ? launch<D, FP8, 1>(p, st) : p.small_rows == 16 ? launch<D, FP8, 2>(p, st) : launch<D, FP8, 4>(p, st);
 }
 
 }  // namespace

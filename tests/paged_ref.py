@@ -188,7 +188,7 @@ class Step:
         return (HALF_BF16 ** 2, 0.0) if self.cache == "bf16" else (torch.finfo(torch.float16).eps / 2, 2.0 ** -32)
 
     def chunk_path(self):
-        return (max(1, self.prob.max_q or self.T)) * (self.H // self.Hkv) > 16
+        return (max(1, self.prob.max_q or self.T)) * (self.H // self.Hkv) > 32
 
     def check(self):
         O, lse = self.run()

@@ -45,6 +45,17 @@ def test_drafted_tokens(cache, causal):
 @pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [True, False])
+def test_drafted_tokens_of_32_rows(cache, d, causal):
+    """Up to 32 rows of a key/value head; a long context, split; few rows beside many."""
+    Step([8, 5, 1, 8, 3], [2000, 33, 9000, 8, 2], H=8, Hkv=2, d=d, cache=cache, causal=causal, seed=15, max_q=8).check()
+    Step([2, 1], [700, 65], H=16, Hkv=1, d=d, ps=64, cache=cache, causal=causal, seed=16, max_q=2).check()
+    Step([1, 1], [100, 300], H=32, Hkv=1, d=d, ps=32, cache=cache, causal=causal, seed=17, max_q=1).check()
+    Step([10, 7], [100, 300], H=3, Hkv=1, d=d, ps=32, cache=cache, causal=causal, seed=18, max_q=10).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
 def test_chunk_lengths(cache, d, causal):
     """Chunks of many sizes over contexts of many sizes, some rows without a key, one request without tokens."""
     q = [1, 17, 64, 65, 130, 300, 0, 33, 20]
