@@ -370,17 +370,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              s[i][nt][e] *= cq[nt][e] * f0;
-              s[i][nt][2 + e] *= cq[nt][e] * f1;
+              s[i][nt][e] *= f0;
+              s[i][nt][2 + e] *= f1;
             }
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < C::kSub; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[i][nt][e] *= cq[nt][e & 1];
       }
       __syncwarp();  // every lane has read K: its place is free
       if (it + 2 < n_it) request(it + 2, pg, K_{});
@@ -408,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int i = 0; i < C::kSub; ++i) top[nt][e] = fmax3(top[nt][e], s[i][nt][e], s[i][nt][2 + e]);
+          top[nt][e] *= cq[nt][e];  // the factor is positive
           up |= top[nt][e] > m[nt][e] + 8.f;
         }
       if (__any_sync(0xffffffffu, up)) {
@@ -435,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
       [[maybe_unused]] uint32_t lo[FP8 ? 1 : C::kSub][NT][2];
       copy_wait<3>();  // this chunk's V
       __syncwarp();
+      bool nan_key = false;
       if constexpr (FP8) {
         const uint8_t* sv = scl.b[warp][it & 1][1];
         int e_top = 0;
@@ -442,7 +437,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         for (int i = 0; i < C::kSub; ++i) {
           const int b = sv[16 * i + (lane & 15)];
           e_top = max(e_top, b == 255 ? 0 : b);
+          nan_key |= b == 255;
         }
+        nan_key = __any_sync(0xffffffffu, nan_key);
         if (__any_sync(0xffffffffu, e_top > e_ref)) {
           e_top = __reduce_max_sync(0xffffffffu, e_top);
           const float a = e_top - e_ref < 127 ? exp2i(e_ref - e_top) : 0.f;
@@ -455,37 +452,47 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
               for (int e = 0; e < 4; ++e) o[i][nt][e] *= a;
         }
       }
+      float neg[NT][2];  // minus the references
 #pragma unroll
-      for (int i = 0; i < C::kSub; ++i) {
-        float f[2] = {1.f, 1.f};
-        if constexpr (FP8) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int b = scl.b[warp][it & 1][1][16 * i + 8 * k + g];
-            f[k] = b == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(max(b - e_ref + 134, 0) << 23);
+        for (int e = 0; e < 2; ++e) neg[nt][e] = m[nt][e] == -INFINITY ? 0.f : -m[nt][e];
+      // keep: a NaN scale's key stays with the rows that see it (0 x NaN)
+      auto weights = [&](auto keep) {
+#pragma unroll
+        for (int i = 0; i < C::kSub; ++i) {
+          [[maybe_unused]] float f[2];
+          if constexpr (FP8) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int b = scl.b[warp][it & 1][1][16 * i + 8 * k + g];
+              f[k] = __uint_as_float(max(b - e_ref + 134, 0) << 23);
+              if (decltype(keep)::value && b == 255) f[k] = __uint_as_float(0x7FC00000u);
+            }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float y[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                y[e] = ex2_approx(__fmaf_rn(s[i][nt][2 * k + e], cq[nt][e], neg[nt][e]));
+                l[nt][e] += y[e];
+                if constexpr (FP8) y[e] = decltype(keep)::value && s[i][nt][2 * k + e] == -INFINITY ? 0.f : y[e] * f[k];
+              }
+              if constexpr (FP8) {
+                hi[i][nt][k] = transpose8(pack_f16x2(y[0], y[1]));
+              } else {
+                const uint32_t a = pack_bf16x2(y[0], y[1]);
+                hi[i][nt][k] = transpose8(a);
+                lo[i][nt][k] = transpose8(pack_bf16x2(y[0] - bf16_lo(a), y[1] - bf16_hi(a)));
+              }
+            }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float y[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              y[e] = ex2_approx(s[i][nt][2 * k + e] - (m[nt][e] == -INFINITY ? 0.f : m[nt][e]));
-              l[nt][e] += y[e];
-              // a NaN scale stays with the rows that see the key
-              if constexpr (FP8) y[e] = s[i][nt][2 * k + e] == -INFINITY ? 0.f : y[e] * f[k];
-            }
-            if constexpr (FP8) {
-              hi[i][nt][k] = transpose8(pack_f16x2(y[0], y[1]));
-            } else {
-              const uint32_t a = pack_bf16x2(y[0], y[1]);
-              hi[i][nt][k] = transpose8(a);
-              lo[i][nt][k] = transpose8(pack_bf16x2(y[0] - bf16_lo(a), y[1] - bf16_hi(a)));
-            }
-          }
-      }
+      };
+      if (FP8 && nan_key) weights(std::true_type{});
+      else weights(std::false_type{});
       // ---------------------------------------------- O^T += V^T P^T
       // tok >= 0 (careful): only the columns of token tok, over the keys that
       // it sees, and the lower terms over finite values
