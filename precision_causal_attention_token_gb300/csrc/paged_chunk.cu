@@ -59,8 +59,8 @@ struct Frag {
 template <int D, bool FP8>
 struct Cfg {
   static constexpr int kTileB = 128 * D * 2;        // bytes of a bf16 tile of 128 rows
-  static constexpr int kStages = FP8 ? 3 : 5;       // K/V tiles
-  static constexpr int kRaw = FP8 ? 4 : 0;          // raw E4M3 tiles
+  static constexpr int kStages = FP8 ? 3 : 4;       // K/V tiles
+  static constexpr int kRaw = FP8 ? 3 : 0;          // raw E4M3 tiles
   static constexpr int kRawB = 128 * D;
 };
 
@@ -68,7 +68,8 @@ template <int D, bool FP8>
 struct __align__(1024) Tiles {
   uint8_t q[2 * Cfg<D, FP8>::kTileB];
   uint8_t kv[Cfg<D, FP8>::kStages][Cfg<D, FP8>::kTileB];
-  uint8_t raw[FP8 ? Cfg<D, FP8>::kRaw : 1][FP8 ? Cfg<D, FP8>::kRawB : 16];
+  uint8_t raw[FP8 ? Cfg<D, FP8>::kRaw : 1][FP8 ? Cfg<D, FP8>::kRawB : 1024];
+  uint8_t out[8][2048];  // softmax warps: 32 rows x 32 channels of O on their way out
 };
 
 struct Ctl {
@@ -648,107 +649,151 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += (u0 + u1) + (u2 + u3);
       }
       if (!ok) break;
-      // ------------------------------------------------------------ the row's result
-      float acc[D];
+      // ------------------------------------------------------------ the rows' results
+      // 32 channels at a time: out of tensor memory, then to the workspace or
+      // through a small shared-memory square to O in 64-byte pieces (a row's
+      // 16 bytes a store, 128 rows side by side, took 3 us a tile)
       if (n_blk) {
         if (!(ok = mbar_wait_warp(&c.o_full[hf], oc & 1, abort_flag, hdr, 0x812))) break;
         ++oc;
         tc_fence_after();
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
+      }
+      // infinities and NaN that the loaders took out of V: a weight is above 0
+      const int odd = f.load ? *reinterpret_cast<volatile int*>(&c.odd_key[n % 4]) : INT_MAX;
+      const int odd_end = min(vis, (f.kb0 + n_blk) * kChunkBlk);
+      auto piece = [&](int j, float (&v)[32]) {
+        if (n_blk) {
           uint32_t o[32];
           tmem_ld32(to + 32 * j, o);
           tmem_ld_wait_regs(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) acc[32 * j + k] = __uint_as_float(o[k]);
-        }
-        tc_fence_before();
-      } else {
-#pragma unroll
-        for (int k = 0; k < D; ++k) acc[k] = 0.f;
-      }
-      // infinities and NaN that the loaders took out of V: a weight is above 0
-      const int odd = f.load ? *reinterpret_cast<volatile int*>(&c.odd_key[n % 4]) : INT_MAX;
-      if (odd < vis) {
-        if constexpr (FP8) {  // a whole row
-#pragma unroll
-          for (int k = 0; k < D; ++k) acc[k] = __uint_as_float(0x7FC00000u);
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(o[k]);
         } else {
-          const int end = min(vis, (f.kb0 + n_blk) * kChunkBlk);
-          for (int j = odd; j < end; ++j) {
-            const int id = __ldg(p.block_table + (int64_t)f.r * p.max_pages + (j >> p.page_shift));
-            if ((unsigned)id >= (unsigned)p.n_pages) continue;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                p.v + id * p.page_bytes + ((int64_t)f.h * p.page_size + (j & (p.page_size - 1))) * D * 2);
 #pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-              const uint4 x = __ldg(src + k);
-              const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+          for (int k = 0; k < 32; ++k) v[k] = 0.f;
+        }
+        if (odd < odd_end) {
+          if constexpr (FP8) {  // a whole row
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((wd[e] & 0x7F80u) == 0x7F80u) acc[8 * k + 2 * e] += bf16_lo(wd[e]);
-                if ((wd[e] & 0x7F800000u) == 0x7F800000u) acc[8 * k + 2 * e + 1] += bf16_hi(wd[e]);
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(0x7FC00000u);
+          } else {
+#pragma unroll 1
+            for (int key = odd; key < odd_end; ++key) {
+              const int id = __ldg(p.block_table + (int64_t)f.r * p.max_pages + (key >> p.page_shift));
+              if ((unsigned)id >= (unsigned)p.n_pages) continue;
+              const uint4* src = reinterpret_cast<const uint4*>(p.v + id * p.page_bytes +
+                                                                (((int64_t)f.h * p.page_size + (key & (p.page_size - 1))) * D + 32 * j) * 2);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint4 x = __ldg(src + k);
+                const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((wd[e] & 0x7F80u) == 0x7F80u) v[8 * k + 2 * e] += bf16_lo(wd[e]);
+                  if ((wd[e] & 0x7F800000u) == 0x7F800000u) v[8 * k + 2 * e + 1] += bf16_hi(wd[e]);
+                }
               }
             }
           }
         }
-      }
-      bool write = f.whole;
-      if (!f.whole) {
-        const int64_t slot = f.starts ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x;
-        float4* po = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * kChunkRows + R;
+      };
+      const int64_t t_row = f.q0 + f.tok0 + tok, my_out = row_ok ? (t_row * p.H + hq) * D : -1;
+      uint8_t* sq = tl.out[warp];
+      // row r of the square: 16-byte piece k at (k ^ (r / 2) % 4)
+      auto emit = [&](int j, const float (&v)[32], float inv) {
 #pragma unroll
-        for (int k = 0; k < D / 4; ++k)
-          __stcg(po + k * kChunkRows, make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]));
-        __stcg(p.part_ml + slot * kChunkRows + R, make_float2(m, l));
-        __threadfence();
-        mbar_arrive(&c.wg[hf]);
-        if (!(ok = mbar_wait_warp(&c.wg[hf], wgc & 1, abort_flag, hdr, 0x813))) break;
-        ++wgc;
-        unsigned int* ctr = &p.hdr->count_chunk[2 * f.w0 + hf];
-        if (row == 0) {
-          const bool last = atomicAdd(ctr, 1u) == (unsigned)(f.parts - 1);
-          if (last) *ctr = 0;
-          c.last[hf] = last;
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(sq + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(pack_bf16x2(v[8 * k] * inv, v[8 * k + 1] * inv), pack_bf16x2(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
+                         pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv), pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + (lane >> 2), k = lane & 3;
+          const int64_t at = __shfl_sync(0xffffffffu, my_out, r);
+          const uint4 x = *reinterpret_cast<const uint4*>(sq + r * 64 + ((k ^ ((r >> 1) & 3)) << 4));
+          if (at >= 0) *reinterpret_cast<uint4*>(p.O + at + 32 * j + 8 * k) = x;
         }
-        mbar_arrive(&c.wg[hf]);
-        if (!(ok = mbar_wait_warp(&c.wg[hf], wgc & 1, abort_flag, hdr, 0x814))) break;
-        ++wgc;
-        write = *reinterpret_cast<volatile int*>(&c.last[hf]) != 0;
-        if (write) {
-          __threadfence();
-          auto slot_of = [&](int i) { return (int64_t)(i == 0 ? 2 * f.w0 + 1 : 2 * (f.w0 + i)); };
-          m = -INFINITY;
-          for (int i = 0; i < f.parts; ++i) m = fmaxf(m, __ldcg(p.part_ml + slot_of(i) * kChunkRows + R).x);
-          l = 0.f;
+        __syncwarp();
+      };
+      auto inverse = [](float x) { return x > 0.f ? 1.f / x : (x == 0.f ? 0.f : x); };  // a NaN sum stays
+      if (f.whole) {
+        const float inv = inverse(l);
+#pragma unroll 1
+        for (int j = 0; j < D / 32; ++j) {
+          float v[32];
+          piece(j, v);
+          emit(j, v, inv);
+        }
+        if (row_ok && p.lse) p.lse[(int64_t)hq * p.T + t_row] = (m + lg2_f(l)) * 0.69314718055994531f;
+        tc_fence_before();
+        continue;
+      }
+      const int64_t slot = f.starts ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x;
+#pragma unroll 1
+      for (int j = 0; j < D / 32; ++j) {
+        float v[32];
+        piece(j, v);
+        float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (D / 4) + 8 * j) * kChunkRows + R;
+        if (row_ok)
 #pragma unroll
-          for (int k = 0; k < D; ++k) acc[k] = 0.f;
+          for (int k = 0; k < 8; ++k) __stcg(po + k * kChunkRows, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+      }
+      tc_fence_before();
+      if (row_ok) __stcg(p.part_ml + slot * kChunkRows + R, make_float2(m, l));
+      mbar_arrive(&c.wg[hf]);
+      if (!(ok = mbar_wait_warp(&c.wg[hf], wgc & 1, abort_flag, hdr, 0x813))) break;
+      ++wgc;
+      unsigned int* ctr = &p.hdr->count_chunk[2 * f.w0 + hf];
+      if (row == 0) {
+        __threadfence();  // after the barrier: for the whole half
+        const bool last = atomicAdd(ctr, 1u) == (unsigned)(f.parts - 1);
+        if (last) *ctr = 0;
+        __threadfence();
+        c.last[hf] = last;
+      }
+      mbar_arrive(&c.wg[hf]);
+      if (!(ok = mbar_wait_warp(&c.wg[hf], wgc & 1, abort_flag, hdr, 0x814))) break;
+      ++wgc;
+      if (*reinterpret_cast<volatile int*>(&c.last[hf]) == 0) continue;
+      // the last of the tile's workers adds the partials up, in worker order
+      auto slot_of = [&](int i) { return (int64_t)(i == 0 ? 2 * f.w0 + 1 : 2 * (f.w0 + i)); };
+      const float2* ml = p.part_ml + R;
+      m = -INFINITY;
+      l = 0.f;
+      if (row_ok) {
+#pragma unroll 8
+        for (int i = 0; i < f.parts; ++i) m = fmaxf(m, __ldcg(ml + slot_of(i) * kChunkRows).x);
+#pragma unroll 8
+        for (int i = 0; i < f.parts; ++i) {
+          const float2 x = __ldcg(ml + slot_of(i) * kChunkRows);
+          l += (x.x == m ? 1.f : ex2_approx(x.x - m)) * x.y;
+        }
+      }
+      const float inv = inverse(l);
+#pragma unroll 1
+      for (int j = 0; j < D / 32; ++j) {
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+        if (row_ok) {
+#pragma unroll 2
           for (int i = 0; i < f.parts; ++i) {
-            const float2 ml = __ldcg(p.part_ml + slot_of(i) * kChunkRows + R);
-            const float a = ml.x == m ? 1.f : ex2_approx(ml.x - m);
-            l += a * ml.y;
-            const float4* src = reinterpret_cast<const float4*>(p.part_o) + slot_of(i) * (D / 4) * kChunkRows + R;
+            const float x = __ldcg(ml + slot_of(i) * kChunkRows).x, a = x == m ? 1.f : ex2_approx(x - m);
+            const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot_of(i) * (D / 4) + 8 * j) * kChunkRows + R;
 #pragma unroll
-            for (int k = 0; k < D / 4; ++k) {
-              const float4 x = __ldcg(src + k * kChunkRows);
-              acc[4 * k] += a * x.x;
-              acc[4 * k + 1] += a * x.y;
-              acc[4 * k + 2] += a * x.z;
-              acc[4 * k + 3] += a * x.w;
+            for (int k = 0; k < 8; ++k) {
+              const float4 y = __ldcg(src + k * kChunkRows);
+              v[4 * k] += a * y.x;
+              v[4 * k + 1] += a * y.y;
+              v[4 * k + 2] += a * y.z;
+              v[4 * k + 3] += a * y.w;
             }
           }
         }
+        emit(j, v, inv);
       }
-      if (write && row_ok) {
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays
-        const int64_t t = f.q0 + f.tok0 + tok;
-        uint4* dst = reinterpret_cast<uint4*>(p.O + (t * p.H + hq) * D);
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k)
-          dst[k] = make_uint4(pack_bf16x2(acc[8 * k] * inv, acc[8 * k + 1] * inv), pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
-                              pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv), pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
-        if (p.lse) p.lse[(int64_t)hq * p.T + t] = (m + lg2_f(l)) * 0.69314718055994531f;
-      }
+      if (row_ok && p.lse) p.lse[(int64_t)hq * p.T + t_row] = (m + lg2_f(l)) * 0.69314718055994531f;
     }
   }
   __syncwarp();  // single-thread roles rejoin their warp
@@ -763,7 +808,7 @@ cudaError_t launch(const PagedParams& p, const CUtensorMap& mk, const CUtensorMa
   constexpr size_t smem = smem_bytes<D, FP8>();
   static_assert(smem <= 232448, "shared memory");
   using T = Tiles<D, FP8>;
-  static_assert(offsetof(T, kv) % 1024 == 0 && offsetof(T, raw) % 1024 == 0, "tile alignment");
+  static_assert(offsetof(T, kv) % 1024 == 0 && offsetof(T, raw) % 1024 == 0 && offsetof(T, out) % 1024 == 0, "tile alignment");
   static bool attr_set[64] = {};  // per device: raised once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
