@@ -104,8 +104,8 @@ struct PagedParams {
 cudaError_t launch_paged_plan(const PagedParams& p, cudaStream_t st);
 cudaError_t launch_paged_append(const PagedParams& p, int d, bool e4m3, bool in_bf16, int sms, cudaStream_t st);
 cudaError_t launch_paged_decode(const PagedParams& p, int d, bool e4m3, cudaStream_t st);
-cudaError_t launch_paged_chunk(const PagedParams& p, int d, bool e4m3, const CUtensorMap& mk, const CUtensorMap& mv,
-                               cudaStream_t st);
+cudaError_t launch_paged_chunk(const PagedParams& p, int d, bool e4m3, const CUtensorMap& mq, const CUtensorMap& mk,
+                               const CUtensorMap& mv, cudaStream_t st);
 // Workers of a launch on a GPU with `sms` SMs: what the kernel keeps resident.
 int paged_decode_workers(int sms);
 
@@ -124,20 +124,15 @@ __device__ __forceinline__ float ue8m0(uint32_t b) {
   return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23);
 }
 
-// Two E4M3FN codes (low byte first) -> f16x2, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
-  return r;
-}
-// Two E4M3 codes in bits 8-15 and 24-31 of `t` -> bf16x2 values times 2^-120
-// (other bits of t are ignored).  The code's exponent and mantissa moved to
-// the top of bf16's exponent field's low end keep their meaning, subnormal
-// codes included, with the bias 127 in place of 7; the caller multiplies by
-// 2^120 times the row's scale, which is exact for every code.
-__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t t) {
-  return ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
-}
+// Two E4M3 codes in bits 0-7 and 16-23 of `t` (the other bits zero) -> bf16x2
+// values times 2^-120: exponent and mantissa move to bits 4-10 of their half,
+// the low end of bf16's exponent field, where they keep their meaning,
+// subnormal codes included, with the bias 127 in place of 7; the sign moves
+// from bit 7 to bit 15 (16 * 128 + 240 * 128 = 2^15).  The caller multiplies by
+// 2^120 times the row's scale, which is exact for every code.  Multiply-adds,
+// because logic runs at half their rate (shift and mask: 876 us against 854 for
+// 2,048 tokens over 32,768).
+__device__ __forceinline__ uint32_t e4m3_to_bf16x2(uint32_t t) { return t * 16u + (t & 0x00800080u) * 240u; }
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -122,24 +122,40 @@ flamia_status_t fill_cache(const flamia_paged_t* p, const flamia_cache_t* c, Pag
   return FLAMIA_OK;
 }
 
-// 4-D map over bf16 pages [n_pages][Hkv][page_size][d]: box = one page and
-// head, 64 channels (128 bytes, 128B swizzle).
-bool make_pages_map(CUtensorMap* m, void* ptr, const flamia_paged_t* p, int64_t page_bytes) {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
   }
-  cuuint64_t dims[4] = {(cuuint64_t)p->d, (cuuint64_t)p->page_size, (cuuint64_t)p->Hkv, (cuuint64_t)p->n_pages};
-  cuuint64_t strides[3] = {(cuuint64_t)p->d * 2, (cuuint64_t)p->page_size * p->d * 2, (cuuint64_t)page_bytes};
-  cuuint32_t box[4] = {64, (cuuint32_t)p->page_size, 1, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn;
+}
+
+// bf16 map, 128B swizzle, out-of-range elements read as zero.
+template <int N>
+bool bf16_map(CUtensorMap* m, const void* ptr, const cuuint64_t (&dims)[N], const cuuint64_t (&strides)[N - 1],
+              const cuuint32_t (&box)[N]) {
+  auto fn = encode_fn();
+  cuuint32_t estr[N];
+  for (auto& e : estr) e = 1;
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Over the queries [T][H][d]: box = a tile's tokens x the heads of one
+// key/value head x 64 channels (128 bytes).
+bool make_q_map(CUtensorMap* m, const PagedParams& a, int d) {
+  return bf16_map<3>(m, a.q, {(cuuint64_t)d, (cuuint64_t)a.H, (cuuint64_t)a.T}, {(cuuint64_t)d * 2, (cuuint64_t)a.q_stride * 2},
+                     {64, (cuuint32_t)a.G, (cuuint32_t)a.tile_toks});
+}
+// Over bf16 pages [n_pages][Hkv][page_size][d]: box = one page and head, 64 channels.
+bool make_pages_map(CUtensorMap* m, const void* ptr, const PagedParams& a, int d) {
+  return bf16_map<4>(m, ptr, {(cuuint64_t)d, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.n_pages},
+                     {(cuuint64_t)d * 2, (cuuint64_t)a.page_size * d * 2, (cuuint64_t)a.page_bytes},
+                     {64, (cuuint32_t)a.page_size, 1, 1});
 }
 
 flamia_status_t of(cudaError_t e) { return e == cudaSuccess ? FLAMIA_OK : FLAMIA_ERR_CUDA; }
@@ -200,10 +216,10 @@ flamia_status_t flamia_paged_fwd(const flamia_paged_t* p, const void* q, const f
     const cudaError_t e = launch_paged_decode(a, p->d, e4m3, stream);
     if (e != cudaSuccess || a.path != kPathChunk) return of(e);
   }
-  CUtensorMap mk{}, mv{};
-  if (!e4m3 && (!make_pages_map(&mk, a.k, p, a.page_bytes) || !make_pages_map(&mv, a.v, p, a.page_bytes)))
+  CUtensorMap mq{}, mk{}, mv{};
+  if (!make_q_map(&mq, a, p->d) || (!e4m3 && (!make_pages_map(&mk, a.k, a, p->d) || !make_pages_map(&mv, a.v, a, p->d))))
     return FLAMIA_ERR_CUDA;
-  return of(launch_paged_chunk(a, p->d, e4m3, mk, mv, stream));
+  return of(launch_paged_chunk(a, p->d, e4m3, mq, mk, mv, stream));
 }
 
 }  // extern "C"

@@ -15,19 +15,20 @@
 //              row's accumulator), and writes the weights back as bf16 over
 //              the scores, from where the P V product reads them as its A
 //              operand: P never touches shared memory.
-//   warps 8-11 loaders: the tile's queries (any row stride and G) into
-//              swizzled shared memory.  E4M3: also each block's codes from
-//              the raw ring into bf16 tiles, times the row's scale (exact).
-//              They put zeros in rows past the request's last key, where
-//              pages hold what an earlier owner left: 0 x NaN is NaN.  For
-//              the same reason they take infinities and NaN out of V in the
-//              blocks that some row sees in part, and leave word of the first
-//              such key, so that the rows that do see it get them back.
+//   warps 8-11 loaders.  E4M3: each block's codes from the raw ring into bf16
+//              tiles, times the row's scale (exact).  Both: zeros in rows past
+//              the request's last key, where pages hold what an earlier owner
+//              left: 0 x NaN is NaN.  For the same reason they take infinities
+//              and NaN out of V in the blocks that some row sees in part, and
+//              leave word of the first such key, so that the rows that do see
+//              it get them back.
 //   warp 12    producer: the block's pages, one copy per page and 64 channels
 //              (bf16, TMA into the swizzled tile) or one per page (E4M3 codes
 //              and scale bytes, into the raw ring).
 //   warp 13    MMA issuer.
 //   warp 14    scheduler: the worker's tiles (the plan's split).
+//   warp 15    the tile's queries: one box of G heads x tokens for 64 channels,
+//              whose rows come in the tile's order whatever G is.
 // The row's weights are rounded to bf16 once (2^-9 relative); sums use the
 // unrounded ones.
 #include <climits>
@@ -41,9 +42,9 @@ namespace {
 constexpr int kThreads = 512;
 constexpr uint32_t kRegSoftmax = 192, kRegLoad = 80, kRegCtl = 48;
 static_assert(256 * kRegSoftmax + 128 * kRegLoad + 128 * kRegCtl <= kThreads * 128, "register split");
-constexpr int kWarpProd = 12, kWarpMma = 13, kWarpSched = 14;
-constexpr int kFragRing = 2;  // odd_key's four slots go by it
-constexpr int kFragConsumers = 8 + 4 + 1 + 1;  // warps that read a fragment
+constexpr int kWarpProd = 12, kWarpMma = 13, kWarpSched = 14, kWarpQ = 15;
+constexpr int kFragRing = 2;  // odd_key's eight slots go by it
+constexpr int kFragConsumers = 8 + 4 + 3;  // warps that read a fragment
 constexpr uint32_t kColS = 0, kColO = 256;     // half h: + 128 h
 
 // One worker's share of one tile.
@@ -66,7 +67,7 @@ struct Cfg {
 
 template <int D, bool FP8>
 struct __align__(1024) Tiles {
-  uint8_t q[2 * Cfg<D, FP8>::kTileB];
+  uint8_t q[2 * Cfg<D, FP8>::kTileB];  // [d / 64][256 rows][128 bytes]
   uint8_t kv[Cfg<D, FP8>::kStages][Cfg<D, FP8>::kTileB];
   uint8_t raw[FP8 ? Cfg<D, FP8>::kRaw : 1][FP8 ? Cfg<D, FP8>::kRawB : 1024];
   uint8_t out[8][2048];  // softmax warps: 32 rows x 32 channels of O on their way out
@@ -79,7 +80,7 @@ struct Ctl {
   uint64_t f_full[kFragRing], f_empty[kFragRing];
   Frag frag[kFragRing];
   int last[2];
-  int odd_key[4];  // per fragment (mod 4): the first key whose V was taken out for not being finite
+  int odd_key[8];  // per fragment (mod 8): the first key whose V was taken out for not being finite
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -114,20 +115,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// 16 bytes to shared memory; of them `bytes` (16 or 0) are read, the rest is zero.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // S[half] = Q[half] K^T: both K-major, 128-byte swizzled rows of 64 channels.
 template <int D>
 __device__ __forceinline__ void issue_s(uint32_t d, const uint8_t* q, const uint8_t* k) {
   const uint32_t qa = smem_u32(q), ka = smem_u32(k);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = (kk / 4) * 128 * 128 + (kk % 4) * 32;
-    mma_ss(d, smem_desc(qa + off, 16, 1024, kSwz128), smem_desc(ka + off, 16, 1024, kSwz128), bf16_idesc(128, 128, 0, 0), kk > 0);
+    const uint32_t q_off = (kk / 4) * 256 * 128 + (kk % 4) * 32, k_off = (kk / 4) * 128 * 128 + (kk % 4) * 32;
+    mma_ss(d, smem_desc(qa + q_off, 16, 1024, kSwz128), smem_desc(ka + k_off, 16, 1024, kSwz128), bf16_idesc(128, 128, 0, 0), kk > 0);
   }
 }
 // O[half] += P[half] V: P in tensor memory, V's rows are keys (MN-major B):
@@ -143,7 +138,8 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, const uint8_
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_chunk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+    paged_chunk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap map_q,
+                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   using C = Cfg<D, FP8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_base_1k(smem_raw);
@@ -156,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (rec_at->n == 0) return;
 
   if (tid == 0) {
-    mbar_init(&c.q_full, 128);
+    mbar_init(&c.q_full, 1);
     mbar_init(&c.q_empty, 1);
     for (int s = 0; s < 5; ++s) {
       mbar_init(&c.kv_full[s], FP8 ? 128 : 1);
@@ -173,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.o_full[s], 1);
       mbar_init(&c.wg[s], 128);
     }
-    for (int s = 0; s < 4; ++s) c.odd_key[s] = INT_MAX;
+    for (int s = 0; s < 8; ++s) c.odd_key[s] = INT_MAX;
     for (int s = 0; s < kFragRing; ++s) {
       mbar_init(&c.f_full[s], 1);
       mbar_init(&c.f_empty[s], kFragConsumers);
@@ -182,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == kWarpMma) tmem_alloc(&c.tmem_base, 512);
+  if (warp == kWarpQ && lane == 0) prefetch_tensormap(&map_q);
   if (!FP8 && warp == kWarpProd && lane == 0) {
     prefetch_tensormap(&map_k);
     prefetch_tensormap(&map_v);
@@ -324,6 +321,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           id = id_next;
         }
       }
+    } else if (warp == kWarpQ) {
+      // ------------------------------------------------------------ queries
+      bool ok = true;
+      Frag f;
+      for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x816); ++n) {
+        if (!(ok = mbar_wait_warp(&c.q_empty, (n & 1) ^ 1, abort_flag, hdr, 0x80b))) break;
+        if (lane == 0) {  // a tile's whole box: rows past its last are not its own and not written
+          mbar_arrive_expect_tx(&c.q_full, p.tile_toks * p.G * D * 2);
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) tma_load_3d(tl.q + j * 256 * 128, &map_q, &c.q_full, 64 * j, f.h * p.G, f.q0 + f.tok0);
+        }
+        __syncwarp();
+      }
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------ MMA issuer
       uint32_t it = 0, pc[2] = {0, 0}, fixed = 0;  // fixed: phase bits of fix[]
@@ -346,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf)
                 if (nh[hf]) {
-                  issue_s<D>(tb + kColS + 128 * hf, tl.q + hf * C::kTileB, tl.kv[it % C::kStages]);
+                  issue_s<D>(tb + kColS + 128 * hf, tl.q + hf * 128 * 128, tl.kv[it % C::kStages]);
                   tc_commit(&c.s_full[hf]);
                 }
               tc_commit(&c.kv_empty[it % C::kStages]);
@@ -383,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     k_in = true;
                     tc_fence_after();
                   }
-                  issue_s<D>(tb + kColS + 128 * hf, tl.q + hf * C::kTileB, kt);
+                  issue_s<D>(tb + kColS + 128 * hf, tl.q + hf * 128 * 128, kt);
                   tc_commit(&c.s_full[hf]);
                 }
               }
@@ -407,28 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Frag f;
     for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x80a); ++n) {
-      if (!(ok = mbar_wait_warp(&c.q_empty, (n & 1) ^ 1, abort_flag, hdr, 0x80b))) break;
-      // straight to shared memory, all of a thread's 16-byte pieces in flight
-      // (through registers, four at a time, a tile waited 8 us for its queries)
-      constexpr int kCh = D / 8;  // pieces of a row
-      const int ch = lt % kCh;
-      const uint32_t q_dst = smem_u32(tl.q) + (ch / 8) * 128 * 128;
-#pragma unroll 8
-      for (int row = lt / kCh; row < 256; row += 128 / kCh) {
-        const int tok = row / p.G;
-        const bool in = row < f.rows;
-        const __nv_bfloat16* src =
-            in ? p.q + (int64_t)(f.q0 + f.tok0 + tok) * p.q_stride + (int64_t)(f.h * p.G + row - tok * p.G) * D + ch * 8 : p.q;
-        cp_async16(q_dst + (row >> 7) * C::kTileB + sw128_off(row & 127, ch % 8), src, in ? 16 : 0);
-      }
-      cp_async_wait_all();
-      // the slot of the fragment after this one.  Its last user, three back,
-      // is done: this fragment is published once every softmax warp has taken
-      // the one two back (the fragment ring), having finished the one before.
-      if (lt == 0) c.odd_key[(n + 1) % 4] = INT_MAX;
-      int* odd_key = &c.odd_key[n % 4];
-      fence_proxy_async_smem();
-      mbar_arrive(&c.q_full);
+      // Clear the slot of the fragment four on.  Its last user, four back, is
+      // done: this fragment is published once every softmax warp has taken the
+      // one two back (the fragment ring), having finished the one before.  And
+      // no loader warp is at the one four on before this one has gone on.
+      if (lt == 0) c.odd_key[(n + 4) % 8] = INT_MAX;
+      int* odd_key = &c.odd_key[n % 8];
       if constexpr (FP8) {
         for (int b = 0; ok && b < 2 * f.load; ++b, ++it) {
           const int rs = it % C::kRaw, s = it % C::kStages;
@@ -439,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // in the swizzle (row mod 8) stays.  The upper 64 channels' lanes
           // write their two 16-byte chunks in the other order: the two
           // 64-channel columns share their banks.
-          constexpr int kRawCh = D / 16, kStep = 128 / kRawCh, kBatch = 4;
+          constexpr int kRawCh = D / 16, kStep = 128 / kRawCh, kBatch = kRawCh;
           const int ch = lt % kRawCh, row0 = lt / kRawCh;
           const int flip = (ch >> 2) & 1;
           const uint8_t* src = tl.raw[rs] + row0 * D + ch * 16;
@@ -449,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              y[2 * k] = bf16x2_mul(e4m3_hi_to_bf16x2(prmt(wd[k], 0u, 0x1404u)), f);
-              y[2 * k + 1] = bf16x2_mul(e4m3_hi_to_bf16x2(prmt(wd[k], 0u, 0x3424u)), f);
+              y[2 * k] = bf16x2_mul(e4m3_to_bf16x2(prmt(wd[k], 0u, 0x4140u)), f);
+              y[2 * k + 1] = bf16x2_mul(e4m3_to_bf16x2(prmt(wd[k], 0u, 0x4342u)), f);
             }
           };
           auto put = [&](int i, const uint32_t (&y)[8]) {
@@ -659,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       // infinities and NaN that the loaders took out of V: a weight is above 0
-      const int odd = f.load ? *reinterpret_cast<volatile int*>(&c.odd_key[n % 4]) : INT_MAX;
+      const int odd = f.load ? *reinterpret_cast<volatile int*>(&c.odd_key[n % 8]) : INT_MAX;
       const int odd_end = min(vis, (f.kb0 + n_blk) * kChunkBlk);
       auto piece = [&](int j, float (&v)[32]) {
         if (n_blk) {
@@ -804,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool FP8>
-cudaError_t launch(const PagedParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+cudaError_t launch(const PagedParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
   constexpr size_t smem = smem_bytes<D, FP8>();
   static_assert(smem <= 232448, "shared memory");
   using T = Tiles<D, FP8>;
@@ -818,16 +812,16 @@ cudaError_t launch(const PagedParams& p, const CUtensorMap& mk, const CUtensorMa
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  paged_chunk_kernel<D, FP8><<<p.W_max[1], kThreads, smem, st>>>(p, mk, mv);
+  paged_chunk_kernel<D, FP8><<<p.W_max[1], kThreads, smem, st>>>(p, mq, mk, mv);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_paged_chunk(const PagedParams& p, int d, bool e4m3, const CUtensorMap& mk, const CUtensorMap& mv,
-                               cudaStream_t st) {
-  if (d == 128) return e4m3 ? launch<128, true>(p, mk, mv, st) : launch<128, false>(p, mk, mv, st);
-  return e4m3 ? launch<64, true>(p, mk, mv, st) : launch<64, false>(p, mk, mv, st);
+cudaError_t launch_paged_chunk(const PagedParams& p, int d, bool e4m3, const CUtensorMap& mq, const CUtensorMap& mk,
+                               const CUtensorMap& mv, cudaStream_t st) {
+  if (d == 128) return e4m3 ? launch<128, true>(p, mq, mk, mv, st) : launch<128, false>(p, mq, mk, mv, st);
+  return e4m3 ? launch<64, true>(p, mq, mk, mv, st) : launch<64, false>(p, mq, mk, mv, st);
 }
 
 }  // namespace flamia
