@@ -372,8 +372,8 @@ flamia_status_t flamia_plan_noalloc(const flamia_problem_t* p, int2* fwd_items, 
  *   max_q        upper bound of a request's new tokens, 1..T (0 selects T).  The
  *                kernel is chosen by it: up to max_q * H / Hkv = 32 rows a
  *                (request, key/value head) take the decode kernel.
- *   H, Hkv, d    query heads, key/value heads (H % Hkv == 0), head dimension
- *                64 or 128
+ *   H, Hkv, d    query heads, key/value heads (H % Hkv == 0, H / Hkv <= 128),
+ *                head dimension 64 or 128
  *   page_size    16, 32, 64 or 128
  *   n_pages      pages of the pool; n_pages * page_size < 2^31
  *   max_pages    columns of the block table

@@ -70,7 +70,7 @@ struct PagedParams {
   int n_req, T, max_q, H, Hkv, G, page_size, page_shift, n_pages, max_pages, causal, path;
   int W_max[2];   // workers at most, of each line
   int small_rows; // requests of up to so many rows go to the decode kernel (8, 16, 32; 0: none)
-  int tile_toks;  // tokens of a tile (kPathChunk)
+  int half_toks;  // tokens of a tile's half (chunk kernel): 128 / G
   float c_log2;   // softmax_scale * log2(e)
   const int32_t* cu_q;
   const int32_t* kv_len;

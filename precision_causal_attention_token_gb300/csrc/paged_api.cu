@@ -33,7 +33,7 @@ flamia_status_t validate(const flamia_paged_t* p) {
   if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) return FLAMIA_ERR_UNSUPPORTED;
   if (p->cache_dtype != FLAMIA_BF16 && p->cache_dtype != FLAMIA_E4M3) return FLAMIA_ERR_UNSUPPORTED;
   if (p->in_dtype != FLAMIA_BF16 && p->in_dtype != FLAMIA_F32) return FLAMIA_ERR_UNSUPPORTED;
-  if (p->n_req > kMaxReq || p->T > (1 << 30) || p->H / p->Hkv > kChunkRows) return FLAMIA_ERR_UNSUPPORTED;
+  if (p->n_req > kMaxReq || p->T > (1 << 30) || p->H / p->Hkv > kChunkRows / 2) return FLAMIA_ERR_UNSUPPORTED;
   if ((int64_t)p->T * p->H * p->d >= (int64_t)1 << 40) return FLAMIA_ERR_UNSUPPORTED;
   if ((int64_t)p->n_pages * p->page_size > INT32_MAX || (int64_t)p->max_pages * p->page_size > INT32_MAX ||
       (int64_t)p->n_req * p->max_pages > INT32_MAX)
@@ -91,7 +91,7 @@ flamia_status_t fill(const flamia_paged_t* p, void* ws, size_t ws_bytes, PagedPa
   // in a call with chunks those of up to 8 rows (16 where a token alone has more than 8)
   a->small_rows = L.path == kPathDecode8 ? 8 : L.path == kPathDecode16 ? 16 : L.path == kPathDecode32 ? 32
                   : a->G <= 8 ? 8 : a->G <= 16 ? 16 : 0;
-  a->tile_toks = kChunkRows / a->G;
+  a->half_toks = kChunkRows / 2 / a->G;
   const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)p->d);
   a->c_log2 = scale * 1.44269504088896341f;
   a->cu_q = p->cu_q;
@@ -145,11 +145,11 @@ bool bf16_map(CUtensorMap* m, const void* ptr, const cuuint64_t (&dims)[N], cons
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// Over the queries [T][H][d]: box = a tile's tokens x the heads of one
+// Over the queries [T][H][d]: box = half a tile's tokens x the heads of one
 // key/value head x 64 channels (128 bytes).
 bool make_q_map(CUtensorMap* m, const PagedParams& a, int d) {
   return bf16_map<3>(m, a.q, {(cuuint64_t)d, (cuuint64_t)a.H, (cuuint64_t)a.T}, {(cuuint64_t)d * 2, (cuuint64_t)a.q_stride * 2},
-                     {64, (cuuint32_t)a.G, (cuuint32_t)a.tile_toks});
+                     {64, (cuuint32_t)a.G, (cuuint32_t)a.half_toks});
 }
 // Over bf16 pages [n_pages][Hkv][page_size][d]: box = one page and head, 64 channels.
 bool make_pages_map(CUtensorMap* m, const void* ptr, const PagedParams& a, int d) {

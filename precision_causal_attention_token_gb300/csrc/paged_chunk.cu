@@ -2,8 +2,8 @@
 // the tensor cores: S = Q K^T and O += P V as tcgen05 kind::f16 MMAs in bf16
 // with fp32 accumulators in tensor memory.
 //
-// A CTA works on tiles of up to 256 query rows (two halves of 128, one per
-// TMEM lane) against 128-key blocks of one key/value head: the rows are the
+// A CTA works on tiles of up to 256 query rows (two halves of up to 128, a
+// TMEM lane a row, each of whole tokens) against 128-key blocks of one key/value head: the rows are the
 // tokens of the chunk times the G = H / Hkv heads that share that head, so a
 // K/V block is fetched once for all of them.  Per block and half the tensor
 // cores need 2 x 128 x 128 x d multiply-adds, the softmax 128 x 128
@@ -27,8 +27,9 @@
 //              and scale bytes, into the raw ring).
 //   warp 13    MMA issuer.
 //   warp 14    scheduler: the worker's tiles (the plan's split).
-//   warp 15    the tile's queries: one box of G heads x tokens for 64 channels,
-//              whose rows come in the tile's order whatever G is.
+//   warp 15    the queries of each half, as soon as its last scores of the
+//              tile before are formed: one box of G heads x tokens for 64
+//              channels, whose rows come in the tile's order whatever G is.
 // The row's weights are rounded to bf16 once (2^-9 relative); sums use the
 // unrounded ones.
 #include <climits>
@@ -52,7 +53,7 @@ struct Frag {
   int r, h, tile, kb0;       // first key block
   int n0, n1;                // blocks of each half
   int load;                  // blocks fetched: the larger
-  int q0, q_len, kv_len, tok0, rows;
+  int q0, q_len, kv_len, tok0, toks;
   int whole, starts, w0, parts;  // parts: workers that share the tile
   int end;
 };
@@ -67,7 +68,7 @@ struct Cfg {
 
 template <int D, bool FP8>
 struct __align__(1024) Tiles {
-  uint8_t q[2 * Cfg<D, FP8>::kTileB];  // [d / 64][256 rows][128 bytes]
+  uint8_t q[2][Cfg<D, FP8>::kTileB];  // [half][d / 64][128 rows][128 bytes]
   uint8_t kv[Cfg<D, FP8>::kStages][Cfg<D, FP8>::kTileB];
   uint8_t raw[FP8 ? Cfg<D, FP8>::kRaw : 1][FP8 ? Cfg<D, FP8>::kRawB : 1024];
   uint8_t out[8][2048];  // softmax warps: 32 rows x 32 channels of O on their way out
@@ -75,7 +76,7 @@ struct __align__(1024) Tiles {
 
 struct Ctl {
   uint8_t scales[4][128];  // raw ring: scale bytes
-  uint64_t q_full, q_empty, kv_full[5], kv_empty[5], raw_full[4], raw_empty[4];
+  uint64_t q_full[2], q_empty[2], kv_full[5], kv_empty[5], raw_full[4], raw_empty[4];
   uint64_t s_full[2], p_full[2], o_full[2], fix[5], wg[2];
   uint64_t f_full[kFragRing], f_empty[kFragRing];
   Frag frag[kFragRing];
@@ -121,8 +122,8 @@ __device__ __forceinline__ void issue_s(uint32_t d, const uint8_t* q, const uint
   const uint32_t qa = smem_u32(q), ka = smem_u32(k);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t q_off = (kk / 4) * 256 * 128 + (kk % 4) * 32, k_off = (kk / 4) * 128 * 128 + (kk % 4) * 32;
-    mma_ss(d, smem_desc(qa + q_off, 16, 1024, kSwz128), smem_desc(ka + k_off, 16, 1024, kSwz128), bf16_idesc(128, 128, 0, 0), kk > 0);
+    const uint32_t off = (kk / 4) * 128 * 128 + (kk % 4) * 32;
+    mma_ss(d, smem_desc(qa + off, 16, 1024, kSwz128), smem_desc(ka + off, 16, 1024, kSwz128), bf16_idesc(128, 128, 0, 0), kk > 0);
   }
 }
 // O[half] += P[half] V: P in tensor memory, V's rows are keys (MN-major B):
@@ -152,8 +153,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (rec_at->n == 0) return;
 
   if (tid == 0) {
-    mbar_init(&c.q_full, 1);
-    mbar_init(&c.q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&c.q_full[s], 1);
+      mbar_init(&c.q_empty[s], 1);
+    }
     for (int s = 0; s < 5; ++s) {
       mbar_init(&c.kv_full[s], FP8 ? 128 : 1);
       mbar_init(&c.kv_empty[s], FP8 ? 1 : 1 + 4);  // the MMA issuer; bf16: also the loader warps
@@ -213,12 +216,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = n % kFragRing;
         if (!(ok = mbar_wait(&c.f_empty[s], ((n / kFragRing) & 1) ^ 1, abort_flag, hdr, 0x801))) break;
         Frag& f = c.frag[s];
-        const int tok0 = tile * p.tile_toks, toks = min(p.tile_toks, rq.q_len - tok0), rows = toks * p.G;
+        const int tok0 = tile * 2 * p.half_toks, toks = min(2 * p.half_toks, rq.q_len - tok0);
         int nb[2];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const int last = min(toks - 1, (128 * hf + 127) / p.G);  // last token of the half
-          nb[hf] = 128 * hf < rows
+          const int last = min(toks, (hf + 1) * p.half_toks) - 1;  // last token of the half
+          nb[hf] = hf * p.half_toks < toks
                        ? (visible_keys(p.causal, rq.q_len, rq.kv_len, tok0 + last) + kChunkBlk - 1) / kChunkBlk : 0;
         }
         // the worker's part: blocks [blk, blk + nblk) behind the tile's own cost
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         f.q_len = rq.q_len;
         f.kv_len = rq.kv_len;
         f.tok0 = tok0;
-        f.rows = rows;
+        f.toks = toks;
         f.whole = nblk == all;
         f.starts = blk == 0;
         f.w0 = f.parts = 0;
@@ -323,20 +326,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kWarpQ) {
       // ------------------------------------------------------------ queries
+      uint32_t uses[2] = {0, 0};
       bool ok = true;
       Frag f;
       for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x816); ++n) {
-        if (!(ok = mbar_wait_warp(&c.q_empty, (n & 1) ^ 1, abort_flag, hdr, 0x80b))) break;
-        if (lane == 0) {  // a tile's whole box: rows past its last are not its own and not written
-          mbar_arrive_expect_tx(&c.q_full, p.tile_toks * p.G * D * 2);
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) tma_load_3d(tl.q + j * 256 * 128, &map_q, &c.q_full, 64 * j, f.h * p.G, f.q0 + f.tok0);
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!ok || (hf ? f.n1 : f.n0) == 0) continue;
+          ok = mbar_wait_warp(&c.q_empty[hf], (uses[hf] & 1) ^ 1, abort_flag, hdr, 0x80b);
+          if (!ok) continue;
+          ++uses[hf];
+          if (lane == 0) {  // a half's whole box: rows past the tile's last are not its own and not written
+            mbar_arrive_expect_tx(&c.q_full[hf], p.half_toks * p.G * D * 2);
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+              tma_load_3d(tl.q[hf] + j * 128 * 128, &map_q, &c.q_full[hf], 64 * j, f.h * p.G, f.q0 + f.tok0 + hf * p.half_toks);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------ MMA issuer
-      uint32_t it = 0, pc[2] = {0, 0}, fixed = 0;  // fixed: phase bits of fix[]
+      uint32_t it = 0, pc[2] = {0, 0}, qc[2] = {0, 0}, fixed = 0;  // fixed: phase bits of fix[]
       bool ok = true;
       const uint32_t elected = elect_one();
       Frag f;
@@ -346,24 +357,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         // one thread waits and issues; the warp stays together at the fragment's end
         if (elected) {
           do {
-            if (!(ok = mbar_wait(&c.q_full, n & 1, abort_flag, hdr, 0x806))) break;
             auto full = [&](uint32_t i) {
               return mbar_wait(&c.kv_full[i % C::kStages], (i / C::kStages) & 1, abort_flag, hdr, 0x807);
             };
             if (f.load) {
               if (!(ok = full(it))) break;
-              tc_fence_after();
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf)
-                if (nh[hf]) {
-                  issue_s<D>(tb + kColS + 128 * hf, tl.q + hf * 128 * 128, tl.kv[it % C::kStages]);
+                if (ok && nh[hf]) {
+                  ok = mbar_wait(&c.q_full[hf], qc[hf] & 1, abort_flag, hdr, 0x806);
+                  if (!ok) continue;
+                  ++qc[hf];
+                  tc_fence_after();
+                  issue_s<D>(tb + kColS + 128 * hf, tl.q[hf], tl.kv[it % C::kStages]);
                   tc_commit(&c.s_full[hf]);
+                  if (nh[hf] == 1) tc_commit(&c.q_empty[hf]);
                 }
+              if (!ok) break;
               tc_commit(&c.kv_empty[it % C::kStages]);
             }
-            // the queries are free once the last block's scores are formed: the
-            // next tile's come in under this one's last weights and products
-            if (f.load <= 1) tc_commit(&c.q_empty);
             for (int b = 0; ok && b < f.load; ++b) {
               const uint32_t vi = it + 2 * b + 1, ki = vi + 1;
               const uint8_t* vt = tl.kv[vi % C::kStages];
@@ -393,14 +405,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     k_in = true;
                     tc_fence_after();
                   }
-                  issue_s<D>(tb + kColS + 128 * hf, tl.q + hf * 128 * 128, kt);
+                  issue_s<D>(tb + kColS + 128 * hf, tl.q[hf], kt);
                   tc_commit(&c.s_full[hf]);
+                  // the queries are free once the last block's scores are formed
+                  if (b + 2 == nh[hf]) tc_commit(&c.q_empty[hf]);
                 }
               }
               if (!ok) break;
               tc_commit(&c.kv_empty[vi % C::kStages]);
               if (more) tc_commit(&c.kv_empty[ki % C::kStages]);
-              if (b + 2 == f.load) tc_commit(&c.q_empty);
             }
             if (!ok) break;
             it += 2 * f.load;
@@ -555,16 +568,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     Frag f;
     for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x810); ++n) {
       const int R = 128 * hf + row;
-      if (128 * hf >= f.rows) continue;  // the half is empty
+      if (hf * p.half_toks >= f.toks) continue;  // the half is empty
       const int n_blk = hf ? f.n1 : f.n0;
-      const bool row_ok = R < f.rows;
-      const int tok = R / p.G, hq = f.h * p.G + (R - tok * p.G);
+      const int tok = hf * p.half_toks + row / p.G, hq = f.h * p.G + row % p.G;
+      const bool row_ok = row < p.half_toks * p.G && tok < f.toks;
       const int vis = row_ok ? min(f.kv_len, visible_keys(p.causal, f.q_len, f.kv_len, f.tok0 + tok)) : f.kv_len;
       const int vis_min = __reduce_min_sync(0xffffffffu, vis);
       float m = -INFINITY, l = 0.f;
       for (int b = 0; ok && b < n_blk; ++b, ++sc) {
         if (!(ok = mbar_wait_warp(&c.s_full[hf], sc & 1, abort_flag, hdr, 0x811))) break;
         tc_fence_after();
+        const int key0 = (f.kb0 + b) * kChunkBlk, nv = vis - key0;
+        const bool masked = key0 + kChunkBlk > vis_min;
+        if (FP8 && masked) {
+          // through tensor memory, a quarter at a time: a fourth of the code.
+          // The E4M3 kernel's roles fill the instruction cache (4 x 4,096: 312
+          // against 298 us); bf16 is better off in registers.
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t x[32];
+            tmem_ld32(ts + 32 * q, x);
+            tmem_ld_wait_regs(x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (32 * q + j >= nv) x[j] = 0xFF800000u;
+            tmem_st32(ts + 32 * q, x);
+          }
+          tmem_st_wait();
+        }
         uint32_t s0[32], s1[32], s2[32], s3[32];
         tmem_ld32(ts, s0);
         tmem_ld32(ts + 32, s1);
@@ -572,9 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(ts + 96, s3);
         tmem_ld_wait_regs(s0, s1);
         tmem_ld_wait_regs(s2, s3);
-        const int key0 = (f.kb0 + b) * kChunkBlk;
-        if (key0 + kChunkBlk > vis_min) {
-          const int nv = vis - key0;
+        if (!FP8 && masked) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             if (j >= nv) s0[j] = 0xFF800000u;
@@ -693,6 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const int64_t t_row = f.q0 + f.tok0 + tok, my_out = row_ok ? (t_row * p.H + hq) * D : -1;
       uint8_t* sq = tl.out[warp];
+      int64_t out_at[4];  // of the rows that this lane stores a piece of
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out_at[i] = __shfl_sync(0xffffffffu, my_out, 8 * i + (lane >> 2));
       // row r of the square: 16-byte piece k at (k ^ (r / 2) % 4)
       auto emit = [&](int j, const float (&v)[32], float inv) {
 #pragma unroll
@@ -704,36 +736,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * i + (lane >> 2), k = lane & 3;
-          const int64_t at = __shfl_sync(0xffffffffu, my_out, r);
           const uint4 x = *reinterpret_cast<const uint4*>(sq + r * 64 + ((k ^ ((r >> 1) & 3)) << 4));
-          if (at >= 0) *reinterpret_cast<uint4*>(p.O + at + 32 * j + 8 * k) = x;
+          if (out_at[i] >= 0) *reinterpret_cast<uint4*>(p.O + out_at[i] + 32 * j + 8 * k) = x;
         }
         __syncwarp();
       };
       auto inverse = [](float x) { return x > 0.f ? 1.f / x : (x == 0.f ? 0.f : x); };  // a NaN sum stays
-      if (f.whole) {
-        const float inv = inverse(l);
-#pragma unroll 1
-        for (int j = 0; j < D / 32; ++j) {
-          float v[32];
-          piece(j, v);
-          emit(j, v, inv);
-        }
-        if (row_ok && p.lse) p.lse[(int64_t)hq * p.T + t_row] = (m + lg2_f(l)) * 0.69314718055994531f;
-        tc_fence_before();
-        continue;
-      }
       const int64_t slot = f.starts ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x;
-#pragma unroll 1
+      const float inv_l = inverse(l);
+#pragma unroll 1  // unrolled, the code outgrows the instruction cache (E4M3 4 x 4,096: 310 -> 367 us)
       for (int j = 0; j < D / 32; ++j) {
         float v[32];
         piece(j, v);
-        float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (D / 4) + 8 * j) * kChunkRows + R;
-        if (row_ok)
+        if (f.whole) {
+          emit(j, v, inv_l);
+        } else if (row_ok) {
+          float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (D / 4) + 8 * j) * kChunkRows + R;
 #pragma unroll
           for (int k = 0; k < 8; ++k) __stcg(po + k * kChunkRows, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+        }
       }
       tc_fence_before();
+      if (f.whole) {
+        if (row_ok && p.lse) p.lse[(int64_t)hq * p.T + t_row] = (m + lg2_f(l)) * 0.69314718055994531f;
+        continue;
+      }
       if (row_ok) __stcg(p.part_ml + slot * kChunkRows + R, make_float2(m, l));
       mbar_arrive(&c.wg[hf]);
       if (!(ok = mbar_wait_warp(&c.wg[hf], wgc & 1, abort_flag, hdr, 0x813))) break;

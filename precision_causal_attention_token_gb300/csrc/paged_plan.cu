@@ -67,12 +67,12 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
 // The line of a request with new tokens.
 __device__ __forceinline__ int line_of(const PagedParams& p, int q_len) { return (int64_t)q_len * p.G > p.small_rows; }
 __device__ __forceinline__ int tiles_of(const PagedParams& p, int q_len) {
-  return line_of(p, q_len) ? (q_len + p.tile_toks - 1) / p.tile_toks : q_len > 0;
+  return line_of(p, q_len) ? (q_len + 2 * p.half_toks - 1) / (2 * p.half_toks) : q_len > 0;
 }
 // Places of one tile.
 __device__ __forceinline__ int tile_places(const PagedParams& p, int line, int q_len, int kv_len, int tile) {
   if (!line) return kDecodeTileCost + max(1, (kv_len + kDecodeBlk - 1) / kDecodeBlk);
-  const int last = min(q_len, (tile + 1) * p.tile_toks) - 1;
+  const int last = min(q_len, (tile + 1) * 2 * p.half_toks) - 1;
   return kChunkTileCost + max(1, (visible_keys(p.causal, q_len, kv_len, last) + kChunkBlk - 1) / kChunkBlk);
 }
 

@@ -71,8 +71,10 @@ def test_chunk_head_groups(cache, H, Hkv):
 
 
 @pytest.mark.parametrize("cache", CACHES)
-def test_chunk_head_group_of_256(cache):
-    Step([3, 1], [60, 200], H=256, Hkv=1, d=64, ps=32, cache=cache, seed=1).check()
+@pytest.mark.parametrize("H", [65, 127, 128])
+def test_chunk_large_head_groups(cache, H):
+    """One token a half tile."""
+    Step([3, 1], [60, 200], H=H, Hkv=1, d=64, ps=32, cache=cache, seed=1).check()
 
 
 @pytest.mark.parametrize("cache", CACHES)
