@@ -62,7 +62,7 @@ struct __align__(16) WorkerRec {
 static_assert(sizeof(ReqRec) == 32 && sizeof(WorkerRec) == 64, "read in 16-byte pieces");
 
 struct PagedLayout {
-  size_t header, reqs, workers, part_ml, part_o, total;
+  size_t header, reqs, workers, part_ml, part_o, chunk_ml, chunk_o, total;
   int path;
 };
 
@@ -79,8 +79,10 @@ struct PagedParams {
   PagedHeader* hdr;
   ReqRec* reqs;        // [2][n_req]
   WorkerRec* workers;  // [kMaxWorkers], [kMaxChunkWorkers]
-  float2* part_ml;     // [2 W][rows] (reference, sum)
-  float* part_o;       // [2 W][rows][d] (decode), [2 W][d / 4][rows][4] (chunk)
+  float2* part_ml;     // decode: [2 W][rows] (reference, sum)
+  float* part_o;       // [2 W][rows][d]
+  float2* chunk_ml;    // chunk: [2 W][256]
+  float* chunk_o;      // [2 W][d / 4][256][4]
   // plan
   int32_t* slot_map;
   const int32_t* old_len;

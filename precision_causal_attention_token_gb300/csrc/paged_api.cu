@@ -48,18 +48,17 @@ flamia_status_t validate(const flamia_paged_t* p) {
 PagedLayout layout(const flamia_paged_t& p) {
   PagedLayout L{};
   L.path = path_of(&p);
-  // the decode kernel's and the chunk kernel's partials, one after the other
-  // on the stream, lie in the same place
   const size_t dec = 2 * (size_t)kMaxWorkers * (L.path == kPathDecode8 ? 8 : L.path == kPathDecode32 ? 32 : 16);
   const size_t chunk = L.path == kPathChunk ? 2 * (size_t)kMaxChunkWorkers * kChunkRows : 0;
-  const size_t rows = dec > chunk ? dec : chunk;
   auto a256 = [](size_t x) { return (x + 255) & ~size_t(255); };
   size_t o = 0;
   L.header = o; o = a256(o + sizeof(PagedHeader));
   L.reqs = o; o = a256(o + sizeof(ReqRec) * 2 * p.n_req);
   L.workers = o; o = a256(o + sizeof(WorkerRec) * (kMaxWorkers + kMaxChunkWorkers));
-  L.part_ml = o; o = a256(o + sizeof(float2) * rows);
-  L.part_o = o; o = a256(o + sizeof(float) * rows * p.d);
+  L.part_ml = o; o = a256(o + sizeof(float2) * dec);
+  L.part_o = o; o = a256(o + sizeof(float) * dec * p.d);
+  L.chunk_ml = o; o = a256(o + sizeof(float2) * chunk);
+  L.chunk_o = o; o = a256(o + sizeof(float) * chunk * p.d);
   L.total = o;
   return L;
 }
@@ -105,6 +104,8 @@ flamia_status_t fill(const flamia_paged_t* p, void* ws, size_t ws_bytes, PagedPa
   a->workers = reinterpret_cast<WorkerRec*>(b + L.workers);
   a->part_ml = reinterpret_cast<float2*>(b + L.part_ml);
   a->part_o = reinterpret_cast<float*>(b + L.part_o);
+  a->chunk_ml = reinterpret_cast<float2*>(b + L.chunk_ml);
+  a->chunk_o = reinterpret_cast<float*>(b + L.chunk_o);
   return FLAMIA_OK;
 }
 

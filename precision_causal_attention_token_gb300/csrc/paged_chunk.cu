@@ -149,8 +149,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   WsHeader* hdr = &p.hdr->base;
   volatile int* abort_flag = &c.abort_flag;
+  // Launched while the decode kernel of the same call may still run (other
+  // rows, other partials): what follows on the stream waits for this grid, so
+  // this grid ends after that one.
+  auto wait_for_decode = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   const WorkerRec* rec_at = p.workers + kMaxWorkers + blockIdx.x;
-  if (rec_at->n == 0) return;
+  if (rec_at->n == 0) {
+    wait_for_decode();
+    return;
+  }
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -751,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (f.whole) {
           emit(j, v, inv_l);
         } else if (row_ok) {
-          float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (D / 4) + 8 * j) * kChunkRows + R;
+          float4* po = reinterpret_cast<float4*>(p.chunk_o) + (slot * (D / 4) + 8 * j) * kChunkRows + R;
 #pragma unroll
           for (int k = 0; k < 8; ++k) __stcg(po + k * kChunkRows, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
         }
@@ -761,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row_ok && p.lse) p.lse[(int64_t)hq * p.T + t_row] = (m + lg2_f(l)) * 0.69314718055994531f;
         continue;
       }
-      if (row_ok) __stcg(p.part_ml + slot * kChunkRows + R, make_float2(m, l));
+      if (row_ok) __stcg(p.chunk_ml + slot * kChunkRows + R, make_float2(m, l));
       mbar_arrive(&c.wg[hf]);
       if (!(ok = mbar_wait_warp(&c.wg[hf], wgc & 1, abort_flag, hdr, 0x813))) break;
       ++wgc;
@@ -779,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*reinterpret_cast<volatile int*>(&c.last[hf]) == 0) continue;
       // the last of the tile's workers adds the partials up, in worker order
       auto slot_of = [&](int i) { return (int64_t)(i == 0 ? 2 * f.w0 + 1 : 2 * (f.w0 + i)); };
-      const float2* ml = p.part_ml + R;
+      const float2* ml = p.chunk_ml + R;
       m = -INFINITY;
       l = 0.f;
       if (row_ok) {
@@ -801,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 2
           for (int i = 0; i < f.parts; ++i) {
             const float x = __ldcg(ml + slot_of(i) * kChunkRows).x, a = x == m ? 1.f : ex2_approx(x - m);
-            const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot_of(i) * (D / 4) + 8 * j) * kChunkRows + R;
+            const float4* src = reinterpret_cast<const float4*>(p.chunk_o) + (slot_of(i) * (D / 4) + 8 * j) * kChunkRows + R;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const float4 y = __ldcg(src + k * kChunkRows);
@@ -822,6 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   drain_after_abort(abort_flag);
   if (warp == kWarpMma) tmem_dealloc(tb, 512);
+  wait_for_decode();
 }
 
 template <int D, bool FP8>
@@ -839,8 +847,17 @@ cudaError_t launch(const PagedParams& p, const CUtensorMap& mq, const CUtensorMa
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  paged_chunk_kernel<D, FP8><<<p.W_max[1], kThreads, smem, st>>>(p, mq, mk, mv);
-  return cudaGetLastError();
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.W_max[1]);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = p.small_rows ? 1 : 0;  // a decode kernel came before
+  return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<D, FP8>, p, mq, mk, mv);
 }
 
 }  // namespace

@@ -145,6 +145,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
   [[maybe_unused]] Queries<D>& qsm = *reinterpret_cast<Queries<D>*>(smem + ring_bytes<D, NT>() + sizeof(Scales));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   PagedHeader* hdr = p.hdr;
+  // the chunk kernel, where one follows, works on other rows: its CTAs come in
+  // as this kernel's leave
+  asm volatile("griddepcontrol.launch_dependents;");
   const int w = blockIdx.x;
   const WorkerRec rec = p.workers[w];
   int left = rec.n, at = rec.at, h = rec.h, pos = rec.pos;
