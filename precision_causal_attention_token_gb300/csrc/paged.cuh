@@ -27,7 +27,7 @@ enum { kPathDecode8 = 0, kPathDecode16 = 1, kPathDecode32 = 2, kPathChunk = 3 };
 constexpr int kDecodeBlk = 64, kChunkBlk = 128, kChunkRows = 256;
 // What a tile costs beside its blocks, in blocks: its queries, first loads and
 // result (decode: 5 us of about 1 us a block)
-constexpr int kDecodeTileCost = 5, kChunkTileCost = 3;
+constexpr int kDecodeTileCost = 5, kChunkTileCost = 2;
 constexpr int kMaxWorkers = 512, kMaxChunkWorkers = 160;
 constexpr int kMaxReq = 8192;
 
