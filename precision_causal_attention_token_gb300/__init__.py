@@ -376,3 +376,75 @@ class TrainCall:
         self.plan(stream)
         self.forward(q, k, v, stream)
         self.backward(do, stream)
+
+
+@dataclass
+class PagedCall:
+    """Device buffers for serving up to ``n_req`` requests from paged caches of ``layers`` layers, and the calls.
+
+    One step: ``plan(cu_q, kv_len)`` once, then per layer ``append(layer, k, v)`` and ``attend(layer, q)``; all on the
+    current stream, no host synchronisation, so a step can be captured in a CUDA graph (cu_q and kv_len are then read
+    from the tensors given at capture).  A request that ends passes kv_len 0; its pages serve others.  After a plan
+    whose status is ERR_NO_PAGES no page has moved: plan again with other lengths."""
+
+    n_req: int
+    T: int           # new tokens of a step at most
+    H: int
+    Hkv: int
+    d: int
+    page_size: int
+    n_pages: int
+    max_pages: int   # pages of a request at most
+    layers: int = 1
+    max_q: int = 0   # new tokens of a request at most (0: T)
+    cache_dtype: int = BF16
+    in_dtype: int = BF16
+    causal: bool = True
+    softmax_scale: float = 0.0
+    device: object = "cuda"
+
+    def __post_init__(self):
+        import torch
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.cu_q = torch.zeros(self.n_req + 1, **i32)
+        self.kv_len, self.held_len = torch.zeros(self.n_req, **i32), torch.zeros(self.n_req, **i32)
+        self.block_table = torch.zeros(self.n_req, self.max_pages, **i32)
+        self.free_pages = torch.arange(self.n_pages, **i32)
+        self.n_free = torch.full((1,), self.n_pages, **i32)
+        self.slot_map = torch.full((self.T,), -1, **i32)
+        self.prob = make_paged(self.T, self.H, self.Hkv, self.d, self.cu_q, self.kv_len, self.block_table,
+                               page_size=self.page_size, n_pages=self.n_pages, max_q=self.max_q,
+                               cache_dtype=self.cache_dtype, in_dtype=self.in_dtype, causal=self.causal,
+                               softmax_scale=self.softmax_scale)
+        nbytes = flamia_paged_workspace_size(self.prob)
+        if nbytes == 0:
+            raise FlamiaError(ERR_INVALID_ARG, "flamia_paged_workspace_size")
+        self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self.status = self.ws[:4].view(torch.int32)
+        shape = (self.layers, self.n_pages, self.Hkv, self.page_size, self.d)
+        e4m3 = self.cache_dtype == E4M3
+        self.k, self.v = (torch.zeros(shape, dtype=torch.uint8 if e4m3 else torch.bfloat16, device=self.device)
+                          for _ in range(2))
+        self.k_scales, self.v_scales = ((torch.full(shape[:4], 127, dtype=torch.uint8, device=self.device)
+                                         for _ in range(2)) if e4m3 else (None, None))
+        self.caches = [paged_cache(self.k[i], self.v[i], *((self.k_scales[i], self.v_scales[i]) if e4m3 else ()))
+                       for i in range(self.layers)]
+        self.O = torch.zeros(self.T, self.H, self.d, dtype=torch.bfloat16, device=self.device)
+        self.lse = torch.zeros(self.H, self.T, dtype=torch.float32, device=self.device)
+
+    def plan(self, cu_q, kv_len):
+        """cu_q [n_req + 1], kv_len [n_req]: int32 tensors; kv_len counts the step's new tokens too."""
+        import torch
+        self.cu_q.copy_(cu_q, non_blocking=True)
+        self.kv_len.copy_(kv_len, non_blocking=True)
+        flamia_paged_plan(self.prob, self.ws, self.slot_map, self.held_len, self.free_pages, self.n_free, self.n_free)
+        torch.where(self.status == OK, self.kv_len, self.held_len, out=self.held_len)
+
+    def append(self, layer, k, v):
+        """k, v [T, Hkv, d] (in_dtype, contiguous): rows behind cu_q[n_req] are not read."""
+        flamia_paged_append(self.prob, k, v, self.slot_map, self.caches[layer], self.ws)
+
+    def attend(self, layer, q):
+        """q [T, H, d] bf16, contiguous; returns (O, lse), overwritten by the next call."""
+        flamia_paged_fwd(self.prob, q, self.caches[layer], self.O, self.lse, self.ws)
+        return self.O, self.lse
