@@ -376,7 +376,7 @@ flamia_status_t flamia_plan_noalloc(const flamia_problem_t* p, int2* fwd_items, 
  *                head dimension 64 or 128
  *   page_size    16, 32, 64 or 128
  *   n_pages      pages of the pool; n_pages * page_size < 2^31
- *   max_pages    columns of the block table
+ *   max_pages    columns of the block table; max_pages * page_size <= 2^30
  *   cache_dtype  FLAMIA_BF16 or FLAMIA_E4M3
  *   in_dtype     dtype of the K and V rows given to flamia_paged_append:
  *                FLAMIA_BF16 or FLAMIA_F32
@@ -398,7 +398,10 @@ flamia_status_t flamia_plan_noalloc(const flamia_problem_t* p, int2* fwd_items, 
  * Conventions as above (16-byte alignment; the int32 arrays 4-byte).  cu_q,
  * kv_len and block_table must not change between flamia_paged_plan and the
  * last launch that uses its workspace.  One workspace serves one step at a
- * time: launches that may overlap (other streams, other graphs) need one each. */
+ * time: launches that may overlap (other streams, other graphs) need one each.
+ * A launch whose workspace was not planned for the same sizes (everything
+ * above but the dtypes, the scale, the strides and the pointers) writes nothing
+ * and sets FLAMIA_ERR_INVALID_ARG.  The stream's device must be the current one. */
 typedef struct {
   int32_t n_req, T, max_q, H, Hkv, d;
   int32_t page_size, n_pages, max_pages;
@@ -477,6 +480,7 @@ flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, cons
  *   q    device bf16 [T][H][d] (q_stride)
  *   O    device bf16 [T][H][d], contiguous
  *   lse  device float [H][T], natural logarithm (may be NULL)
+ * O must not overlap q or the cache.
  * A table entry outside [0, n_pages) sets FLAMIA_ERR_BAD_PAGE and leaves the
  * request's O and lse undefined; nothing outside the pool is read.  Requires
  * flamia_paged_plan on the same workspace; results do not depend on anything

@@ -37,7 +37,9 @@ struct PagedHeader {
   int32_t workers[2];  // W of each line
   int32_t rows;        // cu_q[n_req], 0 after an inconsistent plan
   int32_t n_free_new;  // for a plan whose n_free and n_free_out are one word
-  int32_t pad[8];
+  int32_t pad[2];
+  uint64_t signature;  // of the problem that was planned
+  int32_t pad2[4];
   unsigned int count[kMaxWorkers];              // decode: partials written, per tile (by its first worker)
   unsigned int count_chunk[2 * kMaxChunkWorkers];  // chunk: also by half
 };
@@ -67,6 +69,7 @@ struct PagedLayout {
 };
 
 struct PagedParams {
+  uint64_t signature;  // of what the plan depends on
   int n_req, T, max_q, H, Hkv, G, page_size, page_shift, n_pages, max_pages, causal, path;
   int W_max[2];   // workers at most, of each line
   int small_rows; // requests of up to so many rows go to the decode kernel (8, 16, 32; 0: none)
@@ -116,6 +119,14 @@ __host__ __device__ __forceinline__ int visible_keys(int causal, int q_len, int 
   if (!causal) return kv_len;
   const int n = kv_len - q_len + tok + 1;
   return n < 0 ? 0 : n;
+}
+
+// Whether the workspace holds a plan of this problem: a launch on any other
+// (never planned, or planned for other sizes) reads nothing more and reports.
+__device__ __forceinline__ bool planned(const PagedParams& p) {
+  if (p.hdr->signature == p.signature) return true;
+  report(&p.hdr->base, FLAMIA_ERR_INVALID_ARG, 0x730);
+  return false;
 }
 
 // Worker that owns block x of a line of `cost` blocks split over W.

@@ -35,7 +35,7 @@ flamia_status_t validate(const flamia_paged_t* p) {
   if (p->in_dtype != FLAMIA_BF16 && p->in_dtype != FLAMIA_F32) return FLAMIA_ERR_UNSUPPORTED;
   if (p->n_req > kMaxReq || p->T > (1 << 30) || p->H / p->Hkv > kChunkRows / 2) return FLAMIA_ERR_UNSUPPORTED;
   if ((int64_t)p->T * p->H * p->d >= (int64_t)1 << 40) return FLAMIA_ERR_UNSUPPORTED;
-  if ((int64_t)p->n_pages * p->page_size > INT32_MAX || (int64_t)p->max_pages * p->page_size > INT32_MAX ||
+  if ((int64_t)p->n_pages * p->page_size > INT32_MAX || (int64_t)p->max_pages * p->page_size > (1 << 30) ||
       (int64_t)p->n_req * p->max_pages > INT32_MAX)
     return FLAMIA_ERR_UNSUPPORTED;
   if (!(p->softmax_scale >= 0.f) || std::isinf(p->softmax_scale)) return FLAMIA_ERR_INVALID_ARG;
@@ -93,6 +93,12 @@ flamia_status_t fill(const flamia_paged_t* p, void* ws, size_t ws_bytes, PagedPa
   a->half_toks = kChunkRows / 2 / a->G;
   const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)p->d);
   a->c_log2 = scale * 1.44269504088896341f;
+  // what the plan's records depend on (FNV-1a)
+  uint64_t sig = 0xcbf29ce484222325ull;
+  for (int x : {p->n_req, p->T, a->max_q, p->H, p->Hkv, p->d, p->page_size, p->n_pages, p->max_pages, a->causal, a->path,
+                a->W_max[0], a->W_max[1]})
+    sig = (sig ^ (uint32_t)x) * 0x100000001b3ull;
+  a->signature = sig;
   a->cu_q = p->cu_q;
   a->kv_len = p->kv_len;
   a->block_table = p->block_table;

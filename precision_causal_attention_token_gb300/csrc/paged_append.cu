@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParam
   constexpr int kLanes = D / kEl;           // lanes of a row (8, 16 or 32)
   constexpr int kToks = kThreads / kLanes;  // tokens of a tile
   const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  if (!planned(p)) return;
   const int rows = p.hdr->rows;
   const int64_t n_slots = (int64_t)p.n_pages << p.page_shift;
   // units: (token tile, K or V, head group)
@@ -91,7 +92,7 @@ cudaError_t launch(const PagedParams& p, int sms, cudaStream_t st) {
   constexpr int kToks = kThreads / (D / (BF16 ? 8 : 4));
   const int tiles = (p.T + kToks - 1) / kToks, groups = (p.Hkv + kHeads - 1) / kHeads;
   const int64_t units = (int64_t)tiles * 2 * groups, most = (int64_t)sms * 8;
-  if (units > INT32_MAX) return cudaErrorInvalidValue;
+  if (units > (1 << 30)) return cudaErrorInvalidValue;
   paged_append_kernel<D, E4M3, BF16><<<(int)(units < most ? units : most), kThreads, 0, st>>>(p, tiles, groups);
   return cudaGetLastError();
 }

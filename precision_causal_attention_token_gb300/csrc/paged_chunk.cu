@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // this grid ends after that one.
   auto wait_for_decode = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   const WorkerRec* rec_at = p.workers + kMaxWorkers + blockIdx.x;
-  if (rec_at->n == 0) {
+  if (rec_at->n == 0 || !planned(p)) {
     wait_for_decode();
     return;
   }

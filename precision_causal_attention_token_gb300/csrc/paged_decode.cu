@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
   // as this kernel's leave
   asm volatile("griddepcontrol.launch_dependents;");
   const int w = blockIdx.x;
-  const WorkerRec rec = p.workers[w];
+  const WorkerRec rec = p.workers[w];  // on its way while the signature is
+  if (!planned(p)) return;
   int left = rec.n, at = rec.at, h = rec.h, pos = rec.pos;
   if (left == 0) return;
   ReqRec rq = rec.q;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         // times 2^(139 - E) it is below 2^13 (E clamped: the factor and its inverse stay normal)
         const int E = min(max((int)(top >> 7), 13), 254);
         const float up = exp2i(139 - E);
-        scale *= exp2i(E - 139);
+        scale = fmaxf(scale * exp2i(E - 139), 1.17549435e-38f);  // above 0: a masked -inf stays one
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll

@@ -76,6 +76,10 @@ __device__ __forceinline__ int tile_places(const PagedParams& p, int line, int q
   return kChunkTileCost + max(1, (visible_keys(p.causal, q_len, kv_len, last) + kChunkBlk - 1) / kChunkBlk);
 }
 
+__device__ void no_work(const PagedParams& p) {
+  for (int w = threadIdx.x; w < kMaxWorkers + kMaxChunkWorkers; w += kPlanThreads) p.workers[w] = WorkerRec{};
+}
+
 // The work split (one CTA): the requests of each line with their places, and
 // where each worker starts.  smem: per [n] places of a head, pre [n + 2] first
 // places, rid [n + 2] the requests; line 0 from entry 0, line 1 behind it,
@@ -106,6 +110,14 @@ __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* per
     if (lane == 0) per[r] = sum;
   }
   __syncthreads();
+  // a worker's places and a head's are 32-bit
+  int big = 0;
+  for (int r = tid; r < n; r += kPlanThreads) big |= per[r] > (1 << 30);
+  if (__syncthreads_or(big)) {
+    if (tid == 0) report(&p.hdr->base, FLAMIA_ERR_UNSUPPORTED, 0x702);
+    no_work(p);
+    return;
+  }
   const int seg = (n + kPlanThreads - 1) / kPlanThreads, r0 = min(n, tid * seg), r1 = min(n, r0 + seg);
   int64_t cnt = 0, mine[2] = {0, 0}, cost[2], all;
   for (int r = r0; r < r1; ++r) {
@@ -118,6 +130,11 @@ __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* per
   const int64_t at = block_scan(cnt, sm, &all);
   const int n0 = (int)(all & 0xFFFFFFFF), n1 = (int)(all >> 32);
   int64_t place[2] = {block_scan(mine[0], sm, &cost[0]), block_scan(mine[1], sm, &cost[1])};
+  if (cost[0] > ((int64_t)1 << 38) || cost[1] > ((int64_t)1 << 37)) {  // 2^30 places of a worker
+    if (tid == 0) report(&p.hdr->base, FLAMIA_ERR_UNSUPPORTED, 0x702);
+    no_work(p);
+    return;
+  }
   int idx[2] = {(int)(at & 0xFFFFFFFF), (int)(at >> 32)};
   for (int r = r0; r < r1; ++r) {
     const int ql = cu[r + 1] - cu[r];
@@ -235,6 +252,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     if (tid == 0) {
       p.hdr->base.status = 0;
       p.hdr->base.status_where = 0;
+      p.hdr->signature = p.signature;
     }
     for (int i = tid; i < kMaxWorkers; i += kPlanThreads) p.hdr->count[i] = 0;
     for (int i = tid; i < 2 * kMaxChunkWorkers; i += kPlanThreads) p.hdr->count_chunk[i] = 0;
@@ -289,7 +307,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     if (!why) {
       split_work(p, cu, per, pre, rid, sm);
     } else {  // no worker has work
-      for (int w = tid; w < kMaxWorkers + kMaxChunkWorkers; w += kPlanThreads) p.workers[w] = WorkerRec{};
+      no_work(p);
     }
     return;
   }

@@ -279,3 +279,106 @@ def test_infinite_values_stay_infinite(kind):
     s.v[page, :, 3, 9], s.v[page, :, 5, 17] = math.inf, -math.inf
     s.v[page, :, 3, 33], s.v[page, :, 6, 33] = math.inf, -math.inf
     s.check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_offsets_past_32_bits(cache, kind):
+    """Pages that lie more than 2^32 bytes into the pool, for the append, the decode and the chunk kernel."""
+    Hkv, ps, d = 8, 128, 128
+    el = 2 if cache == "bf16" else 1
+    n_pages = (1 << 32) // (Hkv * ps * d * el) + 40
+    kv, mq = ([1, 200, 300], 1) if kind == "decode" else ([90, 200, 300], 90)
+    q = [1, 1, 1] if kind == "decode" else [90, 1, 70]
+    small = Step(q, kv, H=16, Hkv=Hkv, ps=ps, cache=cache, seed=3, max_q=mq)
+    base = n_pages - small.n_pages
+    big = [torch.empty(n_pages, Hkv, ps, d, dtype=small.k.dtype, device="cuda") for _ in range(2)]
+    for dst, src in zip(big, (small.k, small.v)):
+        dst[base:] = src
+    scales = []
+    if cache == "e4m3":
+        for src in (small.ks, small.vs):
+            s = torch.full((n_pages, Hkv, ps), 127, dtype=torch.uint8, device="cuda")
+            s[base:] = src
+            scales.append(s)
+    table = torch.where(small.table >= 0, small.table + base, small.table)
+    prob = fl.make_paged(small.T, 16, Hkv, d, small.cu_q, small.kv, table, page_size=ps, n_pages=n_pages, max_q=mq,
+                         cache_dtype=small.prob.cache_dtype)
+    ws = torch.zeros(fl.flamia_paged_workspace_size(prob), dtype=torch.uint8, device="cuda")
+    pool = fl.paged_cache(*big, *scales)
+    slots = torch.empty(small.T, dtype=torch.int32, device="cuda")
+    O, lse = torch.empty_like(small.q).view(small.T, 16, d), torch.empty(16, small.T, device="cuda")
+    fl.flamia_paged_plan(prob, ws, slots)
+    # the new tokens' rows taken out of their slots and put back by the append
+    page, off = slots.long() // ps, slots.long() % ps
+    rows = []
+    for i, dst in enumerate(big):
+        x = dst[page, :, off]
+        rows.append(x if cache == "bf16" else torch.ldexp(x.view(torch.float8_e4m3fn).float(), scales[i][page, :, off].int()[..., None] - 127).bfloat16())
+        dst[page, :, off] = 0
+    fl.flamia_paged_append(prob, rows[0].contiguous(), rows[1].contiguous(), slots, pool, ws)
+    fl.flamia_paged_fwd(prob, small.q, pool, O, lse, ws)
+    torch.cuda.synchronize()
+    assert fl.flamia_get_device_status(ws) == fl.OK
+    want, wl = small.run()
+    assert torch.equal(O, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("kind", ["decode", "chunk"])
+def test_workspace_of_another_plan_is_refused(kind):
+    """A workspace that was never planned, or planned for another problem: nothing is written, the status says so."""
+    s = Step([1, 1] if kind == "decode" else [20, 30], [50, 60], max_q=1 if kind == "decode" else 0)
+    O, lse = torch.full((s.T, s.H, s.d), 5.0, dtype=torch.bfloat16, device="cuda"), None
+    for prepare in (lambda: s.ws.zero_(), lambda: s.ws.fill_(255).narrow(0, 0, 8).zero_(),
+                    lambda: fl.flamia_paged_plan(fl.make_paged(s.T, s.H, s.Hkv, s.d, s.cu_q, s.kv, s.table, page_size=s.ps,
+                                                               n_pages=s.n_pages - 1, max_q=s.prob.max_q), s.ws)):
+        prepare()
+        k = torch.zeros(s.T, s.Hkv, s.d, dtype=torch.bfloat16, device="cuda")
+        before = s.k.clone()
+        fl.flamia_paged_append(s.prob, k, k, torch.zeros(s.T, dtype=torch.int32, device="cuda"), s.pool, s.ws)
+        fl.flamia_paged_fwd(s.prob, s.q, s.pool, O, lse, s.ws)
+        torch.cuda.synchronize()
+        assert fl.flamia_get_device_status(s.ws) == fl.ERR_INVALID_ARG
+        assert (O == 5).all() and torch.equal(before, s.k)
+    s.check()
+
+
+@pytest.mark.parametrize("kind", ["decode", "drafts", "mixed"])
+def test_captured_forward_of_each_kernel(kind):
+    """Plan and forward captured and replayed, without the log-sum-exp, beside the same calls outside a graph."""
+    q, kv, mq = {"decode": ([1, 1], [700, 30], 1), "drafts": ([8, 3], [700, 30], 8),
+                 "mixed": ([100, 1, 1, 30], [400, 5000, 0, 30], 0)}[kind]
+    s = Step(q, kv, H=8, Hkv=2, cache="e4m3", max_q=mq, seed=12)
+    want, _ = s.run()
+    O = torch.zeros_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fl.flamia_paged_plan(s.prob, s.ws)
+        fl.flamia_paged_fwd(s.prob, s.q, s.pool, O, None, s.ws)
+        twice = O * 2  # what follows on the stream sees the whole result
+    for _ in range(20):
+        O.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(O, want) and torch.equal(twice, want * 2)
+
+
+def test_what_follows_on_the_stream_waits():
+    """The kernel behind a mixed call, whose two kernels overlap, sees all rows of both."""
+    s = Step([200, 1, 1, 1, 64], [3000, 9000, 7000, 40, 64], H=8, Hkv=2, ps=64, seed=13)
+    want = s.run()[0].clone()
+    fl.flamia_paged_plan(s.prob, s.ws)
+    for _ in range(30):
+        s.O.fill_(0)
+        fl.flamia_paged_fwd(s.prob, s.q, s.pool, s.O, None, s.ws)
+        assert torch.equal(s.O.clone(), want)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_many_requests(cache):
+    """More requests than workers, most of them short; a call without any new token."""
+    kv = [1 + (37 * i) % 61 for i in range(700)]
+    Step([1] * 700, kv, H=2, Hkv=1, d=64, cache=cache, max_q=1, seed=14).check()
+    s = Step([0, 0, 0], [5, 0, 77], cache=cache, pad=4)
+    O, lse = s.run()
+    assert (O == 77).all() and (lse == 77).all() and fl.flamia_get_device_status(s.ws) == fl.OK

@@ -37,7 +37,7 @@ BAD = [(dict(n_req=0), fl.ERR_INVALID_ARG), (dict(T=0), fl.ERR_INVALID_ARG), (di
        (dict(page_size=48), fl.ERR_UNSUPPORTED), (dict(page_size=256), fl.ERR_UNSUPPORTED),
        (dict(cache_dtype=fl.F32), fl.ERR_UNSUPPORTED), (dict(in_dtype=fl.E4M3), fl.ERR_UNSUPPORTED),
        (dict(n_req=8193), fl.ERR_UNSUPPORTED), (dict(H=258, Hkv=2), fl.ERR_UNSUPPORTED),
-       (dict(n_pages=1 << 27), fl.ERR_UNSUPPORTED), (dict(max_pages=1 << 27), fl.ERR_UNSUPPORTED),
+       (dict(n_pages=1 << 27), fl.ERR_UNSUPPORTED), (dict(max_pages=(1 << 26) + 1), fl.ERR_UNSUPPORTED),
        (dict(n_req=8192, max_pages=1 << 18), fl.ERR_UNSUPPORTED)]
 
 
