@@ -16,6 +16,12 @@ namespace {
 
 constexpr int kThreads = 256, kHeads = 4;
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 template <int D, bool E4M3, bool BF16>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParams p, int tiles, int head_groups) {
   constexpr int kEl = BF16 ? 8 : 4;         // elements a lane holds
@@ -58,19 +64,29 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParam
       for (int e = 0; e < kEl; ++e)
         f[e] = BF16 ? __uint_as_float((e & 1) ? (w[e / 2] & 0xFFFF0000u) : (w[e / 2] << 16)) : __uint_as_float(w[e & 3]);
       if constexpr (E4M3) {
-        uint32_t top = 0;  // the magnitudes order like their bits, infinities and NaN last
+        // The row's largest magnitude: magnitudes order like their bits,
+        // infinities and NaN last.  bf16 in pairs, until the end.
+        uint32_t top = w[0] & (BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
 #pragma unroll
-        for (int e = 0; e < kEl; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+        for (int k = 1; k < 4; ++k)
+          top = BF16 ? max_u16x2(top, w[k] & 0x7FFF7FFFu) : max(top, w[k] & 0x7FFFFFFFu);
 #pragma unroll
-        for (int s = kLanes / 2; s; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+        for (int s = kLanes / 2; s; s >>= 1) {
+          const uint32_t o = __shfl_xor_sync(0xffffffffu, top, s);
+          top = BF16 ? max_u16x2(top, o) : max(top, o);
+        }
+        if (BF16) top = max(top & 0xFFFF0000u, top << 16);
         const bool finite = top < 0x7F800000u;
         const int e = finite ? noclamp_exp_clamped(__uint_as_float(top)) : 0;
         const float inv = exp2i(max(-e, -126));  // 2^-e; e = 127 does not occur
         uint32_t c[kEl / 4];
 #pragma unroll
-        for (int k = 0; k < kEl / 4; ++k)
-          c[k] = finite ? pack_e4m3x4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv)
-                        : 0x7F7F7F7Fu;
+        for (int k = 0; k < kEl / 4; ++k) {
+          float y[4];
+          f2_unpack(f2_mul(f2_pack(f[4 * k], f[4 * k + 1]), f2_pack(inv, inv)), y[0], y[1]);
+          f2_unpack(f2_mul(f2_pack(f[4 * k + 2], f[4 * k + 3]), f2_pack(inv, inv)), y[2], y[3]);
+          c[k] = finite ? pack_e4m3x4(y[0], y[1], y[2], y[3]) : 0x7F7F7F7Fu;
+        }
         if (write) {
           uint8_t* dst = pool + in_page * D + sub * kEl;
           if constexpr (kEl == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[kEl / 4 - 1]);
@@ -91,7 +107,7 @@ template <int D, bool E4M3, bool BF16>
 cudaError_t launch(const PagedParams& p, int sms, cudaStream_t st) {
   constexpr int kToks = kThreads / (D / (BF16 ? 8 : 4));
   const int tiles = (p.T + kToks - 1) / kToks, groups = (p.Hkv + kHeads - 1) / kHeads;
-  const int64_t units = (int64_t)tiles * 2 * groups, most = (int64_t)sms * 8;
+  const int64_t units = (int64_t)tiles * 2 * groups, most = (int64_t)sms * 16;
   if (units > (1 << 30)) return cudaErrorInvalidValue;
   paged_append_kernel<D, E4M3, BF16><<<(int)(units < most ? units : most), kThreads, 0, st>>>(p, tiles, groups);
   return cudaGetLastError();
