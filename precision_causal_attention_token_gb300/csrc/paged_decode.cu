@@ -531,15 +531,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
             if constexpr (FP8) {
 #pragma unroll
               for (int x = 0; x < kW; ++x) {
-                uint32_t c[4][2];  // channel pairs 4x, 4x + 1 and 4x + 2, 4x + 3 of each key
-#pragma unroll
-                for (int k = 0; k < 4; ++k) e4m3x4_to_f16(w[k][x], c[k][0], c[k][1]);
+                // codes of two keys side by side before they are converted: half
+                // the permutations of doing it after
+                uint32_t a01[4], a23[4];  // channels 4x .. 4x + 3: keys 2t, 2t + 1 and 2t + 8, 2t + 9
+                e4m3x4_to_f16(prmt(w[0][x], w[1][x], 0x5140u), a01[0], a01[1]);
+                e4m3x4_to_f16(prmt(w[0][x], w[1][x], 0x7362u), a01[2], a01[3]);
+                e4m3x4_to_f16(prmt(w[2][x], w[3][x], 0x5140u), a23[0], a23[1]);
+                e4m3x4_to_f16(prmt(w[2][x], w[3][x], 0x7362u), a23[2], a23[3]);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                  const uint32_t a0 = prmt(c[0][half], c[1][half], 0x5410u), a1 = prmt(c[0][half], c[1][half], 0x7632u);
-                  const uint32_t a2 = prmt(c[2][half], c[3][half], 0x5410u), a3 = prmt(c[2][half], c[3][half], 0x7632u);
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * x + half][nt], a0, a1, a2, a3, hi[i][nt][0], hi[i][nt][1]);
+                  for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(o[2 * x + half][nt], a01[2 * half], a01[2 * half + 1], a23[2 * half], a23[2 * half + 1], hi[i][nt][0], hi[i][nt][1]);
                 }
               }
             } else {
