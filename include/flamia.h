@@ -367,8 +367,9 @@ flamia_status_t flamia_plan_noalloc(const flamia_problem_t* p, int2* fwd_items, 
  *   n_req        requests of the step, 1..8192
  *   T            rows of the packed per-token tensors (capacity).  Request r
  *                owns the rows [cu_q[r], cu_q[r+1]) of q, k, v, O and the slot
- *                map; rows behind cu_q[n_req] <= T belong to no request and
- *                are neither read nor written (their slots are set to -1).
+ *                map, all of which have T rows; rows behind cu_q[n_req] <= T
+ *                belong to no request: what they hold does not matter, and
+ *                they are not written (their slots are set to -1).
  *   max_q        upper bound of a request's new tokens, 1..T (0 selects T).  The
  *                kernel is chosen by it: up to max_q * H / Hkv = 32 rows a
  *                (request, key/value head) take the decode kernel.
@@ -377,6 +378,7 @@ flamia_status_t flamia_plan_noalloc(const flamia_problem_t* p, int2* fwd_items, 
  *   page_size    16, 32, 64 or 128
  *   n_pages      pages of the pool; n_pages * page_size < 2^31
  *   max_pages    columns of the block table; max_pages * page_size <= 2^30
+ *                (2^25 where max_q * H / Hkv > 32)
  *   cache_dtype  FLAMIA_BF16 or FLAMIA_E4M3
  *   in_dtype     dtype of the K and V rows given to flamia_paged_append:
  *                FLAMIA_BF16 or FLAMIA_F32

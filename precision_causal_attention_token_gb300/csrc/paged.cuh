@@ -30,6 +30,10 @@ constexpr int kDecodeBlk = 64, kChunkBlk = 128, kChunkRows = 256;
 constexpr int kDecodeTileCost = 5, kChunkTileCost = 2;
 constexpr int kMaxWorkers = 512, kMaxChunkWorkers = 160;
 constexpr int kMaxReq = 8192;
+// Keys of a request in a call with chunks: 2^18 blocks of a tile at 1.2 to 4 us
+// each stay below the limit of the chunk kernel's waits, whose longest is for
+// a tile's end.
+constexpr int kMaxChunkKeys = 1 << 25;
 
 struct PagedHeader {
   WsHeader base;       // status words first, as flamia_get_device_status reads them

@@ -38,6 +38,7 @@ flamia_status_t validate(const flamia_paged_t* p) {
   if ((int64_t)p->n_pages * p->page_size > INT32_MAX || (int64_t)p->max_pages * p->page_size > (1 << 30) ||
       (int64_t)p->n_req * p->max_pages > INT32_MAX)
     return FLAMIA_ERR_UNSUPPORTED;
+  if (path_of(p) == kPathChunk && (int64_t)p->max_pages * p->page_size > kMaxChunkKeys) return FLAMIA_ERR_UNSUPPORTED;
   if (!(p->softmax_scale >= 0.f) || std::isinf(p->softmax_scale)) return FLAMIA_ERR_INVALID_ARG;
   const int64_t kv_el = p->in_dtype == FLAMIA_BF16 ? 8 : 4;  // elements of 16 bytes
   if (p->q_stride && (p->q_stride < (int64_t)p->H * p->d || p->q_stride % 8)) return FLAMIA_ERR_INVALID_ARG;

@@ -161,3 +161,29 @@ def test_bf16_instruction_descriptor_refusals(lib):
 def test_kernels_use_the_checked_bf16_descriptors():
     src = open(os.path.join(os.path.dirname(fl.__file__), "csrc", "paged_chunk.cu")).read()
     assert set(re.findall(r"\bbf16_idesc\([^()]*\)", src)) == {"bf16_idesc(128, 128, 0, 0)", "bf16_idesc(128, D, 0, 1)"}
+
+
+def test_a_chunk_call_holds_up_to_2_25_keys_a_request(lib):
+    """The limit counts where some request may take the chunk kernel: more than 32 rows (here max_q * 4)."""
+    for max_q, pages, ok in ((9, 1 << 21, True), (9, (1 << 21) + 1, False), (8, (1 << 21) + 1, True),
+                             (8, 1 << 26, True), (0, (1 << 21) + 1, False)):
+        p = _prob(max_q=max_q, max_pages=pages)
+        assert (fl.flamia_paged_workspace_size(p) > 0) == ok
+        if not ok:
+            assert lib.flamia_paged_plan(p, None, None, None, None, None, 0x100000, 1 << 40, None) == fl.ERR_UNSUPPORTED
+
+
+def test_paged_call_checks_what_it_is_given():
+    """Shapes, dtypes and strides, before anything runs (tensors of T rows, whatever cu_q says)."""
+    import torch
+    c = fl.PagedCall(n_req=2, T=6, H=4, Hkv=2, d=64, page_size=16, n_pages=8, max_pages=3, device="cpu")
+    kv, q = torch.zeros(6, 2, 64, dtype=torch.bfloat16), torch.zeros(6, 4, 64, dtype=torch.bfloat16)
+    cu, n = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    wide = torch.zeros(6, 4, 64, dtype=torch.bfloat16)
+    for call in (lambda: c.append(0, kv[:5], kv), lambda: c.append(0, kv, kv[:5]), lambda: c.append(0, kv.float(), kv),
+                 lambda: c.append(0, wide[:, :2], kv), lambda: c.attend(0, q[:5]), lambda: c.attend(0, q.half()),
+                 lambda: c.attend(0, torch.cat([q, q], 1)[:, :4]), lambda: c.plan(cu[:2], n), lambda: c.plan(cu, n[:1]),
+                 lambda: c.plan(cu.long(), n), lambda: c.plan(cu, n.long())):
+        with pytest.raises(fl.FlamiaError) as e:
+            call()
+        assert e.value.status == fl.ERR_INVALID_ARG
