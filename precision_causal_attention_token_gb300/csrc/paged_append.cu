@@ -4,10 +4,12 @@
 // and written as one contiguous run of its page: rounded to bf16, or as E4M3
 // codes with the row's own no-clamp exponent, whose maximum the group forms by
 // shuffles.  Every byte is read and written once; HBM bound at large sizes, a
-// launch's latency at small ones.  A CTA takes a few consecutive tokens and
+// launch's latency at small ones: 46 us for 46,806 tokens of 8 heads x 128 from
+// bf16 to E4M3 (289 MB, 6.3 TB/s), 2.6 us for 65.  A CTA takes a few consecutive tokens and
 // heads at a time, so that what it reads is contiguous (tokens of all heads)
-// and so is what it writes (a head's tokens); a thread keeps kHeads rows in
-// flight.
+// and so is what it writes (a head's tokens: with a token's rows in a row
+// instead, the stores came in 128-byte pieces and the same call took 83 us); a
+// thread keeps kHeads rows in flight.
 #include "paged.cuh"
 
 namespace flamia {
