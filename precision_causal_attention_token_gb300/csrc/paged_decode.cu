@@ -693,17 +693,29 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         auto slot_of = [&](int i) { return (int64_t)(i == 0 ? 2 * w0 + 1 : 2 * (w0 + i)); };
         float* wt = reinterpret_cast<float*>(smem);  // [n][kQ]; the join's buffers are free
         const int me = tid % kSpan;
+        constexpr int kOwn = 4;  // a thread's first partials are read once
+        float2 own[kOwn];
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+          const int i = me + j * kSpan;
+          own[j] = i < n ? __ldcg(p.part_ml + slot_of(i) * C::kQ + row) : make_float2(-INFINITY, 0.f);
+        }
         M = -INFINITY;
-        for (int i = me; i < n; i += kSpan) M = fmaxf(M, __ldcg(p.part_ml + slot_of(i) * C::kQ + row).x);
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) M = fmaxf(M, own[j].x);
+        for (int i = me + kOwn * kSpan; i < n; i += kSpan) M = fmaxf(M, __ldcg(p.part_ml + slot_of(i) * C::kQ + row).x);
 #pragma unroll
         for (int k = kSpan / 2; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
         L = 0.f;
-        for (int i = me; i < n; i += kSpan) {
-          const float2 x = __ldcg(p.part_ml + slot_of(i) * C::kQ + row);
+        auto weigh = [&](int i, float2 x) {
           const float a = x.x == M ? 1.f : ex2_approx(x.x - M);
           L += a * x.y;
           wt[i * C::kQ + row] = a;
-        }
+        };
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+          if (me + j * kSpan < n) weigh(me + j * kSpan, own[j]);
+        for (int i = me + kOwn * kSpan; i < n; i += kSpan) weigh(i, __ldcg(p.part_ml + slot_of(i) * C::kQ + row));
 #pragma unroll
         for (int k = kSpan / 2; k; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
         __syncwarp();
