@@ -35,6 +35,13 @@ def test_decode_long_context_is_split(cache, d):
 
 
 @pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("H", [8, 16, 32])
+def test_one_head_split_over_every_worker(cache, H):
+    """One tile for the whole GPU: hundreds of partial results in one join, at 8, 16 and 32 rows."""
+    Step([1], [180011], H=H, Hkv=1, ps=128, cache=cache, seed=H, max_q=1).check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("causal", [True, False])
 def test_drafted_tokens(cache, causal):
     """A few new tokens a request, the decode kernel's 16 rows full and not, rows without a key."""
