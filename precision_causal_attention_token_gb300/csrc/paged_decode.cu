@@ -503,8 +503,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
             }
         }
       };
-      if (FP8 && nan_key) weights(std::true_type{});
-      else weights(std::false_type{});
+      if (FP8 && nan_key) {
+        weights(std::true_type{});
+        // its codes may be NaN too: the NaN comes with the weight, and rows that
+        // do not see it have the weight 0 (0 x NaN)
+        for (int key = 0; key < C::kChunk; ++key)
+          if (scl.b[warp][it & 1][1][key] == 255 && lane < C::kRowB / 4)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + key * C::kRowB + lane * 4), "r"(0) : "memory");
+        __syncwarp();
+      } else {
+        weights(std::false_type{});
+      }
       // ---------------------------------------------- O^T += V^T P^T
       // tok >= 0 (careful): only the columns of token tok, over the keys that
       // it sees, and the lower terms over finite values

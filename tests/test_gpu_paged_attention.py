@@ -144,6 +144,28 @@ def test_nan_reaches_only_rows_that_see_it(cache, kind):
         assert ((O[n:].double() - wO[n:]).abs() <= tO[n:]).all() and torch.isfinite(lse[:, n:]).all()
 
 
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q,H", [(4, 2), (4, 4), (5, 6), (40, 2)])
+def test_an_e4m3_row_that_is_not_finite_and_later_tokens(which, d, q, H):
+    """A row as the append kernel stores it (NaN codes under byte 255): NaN for the new tokens from its own on, the
+    same values as before for the earlier ones and for the other head.  8, 16 and 32 rows, and a chunk."""
+    for at in (0, q // 2, q - 1):  # which of the request's new tokens
+        s = Step([q, 2], [301, 64], H=2 * H, Hkv=2, d=d, ps=32, cache="e4m3", seed=q + H, max_q=q)
+        wO, wl, tO, tl = s.reference(*s.rounding())
+        j = 301 - q + at
+        page, off = s.table_host[0][j // 32], j % 32
+        codes, scales = (s.k, s.ks) if which == "k" else (s.v, s.vs)
+        codes[page, 1, off], scales[page, 1, off] = 0x7F, 255
+        O, lse = s.run()
+        sees = torch.zeros(s.T, 2 * H, dtype=torch.bool, device=s.dev)
+        sees[at:q, H:] = True
+        assert torch.isnan(O[sees]).all()
+        assert ((O.double() - wO).abs() <= tO)[~sees].all()
+        off_l = ((lse.double() - wl).abs() <= tl).T
+        assert off_l[~sees].all() and (torch.isnan(lse.T[sees]).all() if which == "k" else off_l[sees].all())
+
+
 @pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("kind", ["decode", "chunk"])
 def test_layouts(cache, kind):
