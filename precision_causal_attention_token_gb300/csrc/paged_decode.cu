@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
     // Request a chunk's K (or V) and its scale bytes: one group of copies
     // each.  A copy instruction takes 512 contiguous bytes: with K in the
     // fragments' own order (64-byte pieces of eight rows) the decode of 65,522
-    // tokens ran at 5.4 TB/s.
+    // tokens took 74 us in place of 59.
     // 16-byte piece c of row r lies at r * kRowB + 16 * (c ^ swap(r)): the reads
     // below then meet no bank twice.
     auto request = [&](int it, int pg, auto is_v) {
