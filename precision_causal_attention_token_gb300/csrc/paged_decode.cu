@@ -69,7 +69,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
-// 16 bytes to shared memory; of them `n` (16 or 0) are read, the rest is zero.
+// 16 bytes to shared memory; of them the first `n` are read, the rest is zero.
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint32_t n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -275,10 +275,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
           const int rr = i * kRowsAt + row;
           copy16(dst + (16 * s + rr) * C::kRowB + ((piece ^ C::swap(kV, rr)) << 4), src + i * 512, key + rr < kend ? 16 : 0);
         }
-        if constexpr (FP8) {  // 16 bytes of one page
+        if constexpr (FP8) {
+          // 16 bytes of one page; zero for keys from kend on, whose slots hold
+          // what an earlier owner left: the reference below is a maximum
           if (lane == s)
             copy16(scales + ((it & 1) * 2 + kV) * 64 + 16 * s, (kV ? p.v_scales : p.k_scales) + (int64_t)id * p.Hkv * p.page_size + in_page,
-                   key < kend ? 16 : 0);
+                   min(max(kend - key, 0), 16));
         }
       }
       copy_commit();
