@@ -22,8 +22,15 @@
 // puts the row's largest element at 2^13, so what f16 cannot hold lies 2^-37
 // below it); the key's scale multiplies its scores.  The weights are f16
 // (2^-11 relative), times 2^(e - E + 7) with e the key's V exponent and E the
-// largest seen so far: at most 2^15, and f16's normal range leaves 29 binades
-// below the largest; E's rise rescales the accumulators.
+// largest seen so far: at most 2^15; E's rise rescales the accumulators.  E
+// counts keys that a row may not see, that have no weight in it or that hold
+// zeros, and what lies far below it leaves f16's range.  So a warp whose keys'
+// exponents turn out to lie more than 12 apart (a weight of 2^-9 of the
+// reference still has all its bits then, and none is off by more than 2^-20 of
+// it) takes its keys once more, with V as bf16 (code times scale is exact) and
+// the weights as two bf16 terms (16 requests of 8,000 tokens whose warps all
+// do: 57 -> 68 us at 4 rows, 85 -> 116 at 32; more where the first pass is
+// nearly done when it finds out).
 //
 // Measured (152 SMs, H = 32, Hkv = 8, d = 128): one request of 65,522 bf16
 // tokens 57 us (268 MB; 46 us at the last SM's last load, then the join), 64
@@ -47,6 +54,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 4096;  // bytes of a chunk's K (or V)
+constexpr int kSpread = 12;  // binades between V rows that f16 weights serve
 constexpr int kRingB = kWarps * 4 * kUnit;  // two chunks a warp
 // 2 CTAs of an SM (3: 59 against 57 us on 65,522 tokens; more partials to join)
 constexpr int kCtas = 2;
@@ -292,9 +300,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
     float m[NT][2], l[NT][2];
     // bf16: an infinity in V times the lower term, or times the weight 0 of a
     // row that may not see it, gives a NaN that the formula does not have.  So
-    // a warp that ends with a NaN takes its keys once more, carefully.
-    bool careful = false;
-  again:
+    // a warp that ends with a NaN takes its keys once more, carefully; E4M3: one
+    // that meets V exponents more than kSpread apart.
+    // A loop of its own: in one with the usual pass, the 32-row kernel spilled
+    // (drafts 63 -> 72 us).
+    [[maybe_unused]] int e_ref = 0;  // E + 127: the largest V scale byte so far
+   auto pass = [&](auto careful_) {  // true: to be done carefully
+    constexpr bool careful = decltype(careful_)::value;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
@@ -302,7 +314,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
 #pragma unroll
       for (int i = 0; i < C::kMT; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
     }
-    [[maybe_unused]] int e_ref = 0;  // E + 127: the largest V scale byte so far
+    e_ref = FP8 && careful ? 134 : 0;  // 134: no factor
+    [[maybe_unused]] int e_low = 255;  // the smallest that this lane has read
     int pg = 0, pg_next = 0;
     if (n_it > 0) {
       pg = page_group(0);
@@ -451,11 +464,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         for (int i = 0; i < C::kSub; ++i) {
           const int b = sv[16 * i + (lane & 15)];
           e_top = max(e_top, b == 255 ? 0 : b);
+          if (key0 + 16 * i + (lane & 15) < kend) e_low = min(e_low, b);
           nan_key |= b == 255;
         }
         nan_key = __any_sync(0xffffffffu, nan_key);
-        if (__any_sync(0xffffffffu, e_top > e_ref)) {
-          e_top = __reduce_max_sync(0xffffffffu, e_top);
+        if (!careful &&
+            __any_sync(0xffffffffu, e_top > e_ref || e_low < e_ref - kSpread)) {
+          e_top = __reduce_max_sync(0xffffffffu, max(e_top, e_ref));
+          if (e_top - __reduce_min_sync(0xffffffffu, e_low) > kSpread) {
+            copy_wait<0>();  // the ring's copies in flight
+            __syncwarp();
+            return true;
+          }
           const float a = e_top - e_ref < 127 ? exp2i(e_ref - e_top) : 0.f;
           e_ref = e_top;
 #pragma unroll
@@ -506,13 +526,75 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         }
       };
       if (FP8 && nan_key) {
-        weights(std::true_type{});
         // its codes may be NaN too: the NaN comes with the weight, and rows that
         // do not see it have the weight 0 (0 x NaN)
         for (int key = 0; key < C::kChunk; ++key)
           if (scl.b[warp][it & 1][1][key] == 255 && lane < C::kRowB / 4)
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + key * C::kRowB + lane * 4), "r"(0) : "memory");
         __syncwarp();
+      }
+      // E4M3, careful: V as bf16 values, two bf16 terms a weight; eight rows of
+      // one key tile at a time, so that it needs no registers beside the usual
+      // pass's (all rows at once spilled 500 bytes of the 32-row kernel)
+      auto add_careful = [&] {
+        const uint8_t* sv = scl.b[warp][it & 1][1];
+#pragma unroll
+        for (int i = 0; i < C::kSub; ++i) {
+          // 2^120 times the scales of keys 2t, 2t + 1 (then 2t + 8, 2t + 9) in two
+          // factors, as bf16 pairs
+          uint32_t f[2][2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t b0 = min((int)sv[16 * i + 8 * k + 2 * t], 254), b1 = min((int)sv[16 * i + 8 * k + 2 * t + 1], 254);
+            f[k][0] = ((min(b0, 134u) + 120u) << 7) | ((min(b1, 134u) + 120u) << 23);
+            f[k][1] = ((max(b0, 134u) - 7u) << 7) | ((max(b1, 134u) - 7u) << 23);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t ph[2], pl[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float y[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float x = s[i][nt][2 * k + e];
+                y[e] = ex2_approx(__fmaf_rn(x, cq[nt][e], neg[nt][e]));
+                l[nt][e] += y[e];
+                if (sv[16 * i + 8 * k + g] == 255 && x != -INFINITY) y[e] = __uint_as_float(0x7FC00000u);
+              }
+              const uint32_t a = pack_bf16x2(y[0], y[1]);
+              ph[k] = transpose8(a);
+              pl[k] = transpose8(pack_bf16x2(y[0] - bf16_lo(a), y[1] - bf16_hi(a)));
+            }
+#pragma unroll
+            for (int x = 0; x < C::kVW; ++x) {
+              uint32_t w[4];  // channels 4x .. 4x + 3 of four keys
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int rk = 2 * t + (k & 1) + 8 * (k >> 1);
+                const uint32_t piece = C::kVW == 2 ? g >> 1 : g, in = C::kVW == 2 ? (g & 1) * 8 + 4 * x : 4 * x;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[k])
+                             : "r"(vb + (16 * i + rk) * C::kRowB + ((piece ^ C::swap(true, rk)) << 4) + in) : "memory");
+              }
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t a[4];  // channels 4x + 2 half, + 1: keys 2t, 2t + 1; the same of 2t + 8, 2t + 9
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t two = prmt(w[k & 2], w[(k & 2) + 1], 0x5410u + 0x2222u * half) >> (8 * (k & 1)) & 0x00FF00FFu;
+                  a[k] = bf16x2_mul(bf16x2_mul(e4m3_to_bf16x2(two), f[k >> 1][0]), f[k >> 1][1]);
+                }
+                mma_bf16(o[2 * x + half][nt], a[0], a[1], a[2], a[3], ph[0], ph[1]);
+                mma_bf16(o[2 * x + half][nt], a[0], a[1], a[2], a[3], pl[0], pl[1]);
+              }
+            }
+          }
+        }
+      };
+      if constexpr (FP8 && careful) {
+        add_careful();
+      } else if (FP8 && nan_key) {
+        weights(std::true_type{});
       } else {
         weights(std::false_type{});
       }
@@ -599,9 +681,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
           }
         }
       };
-      if (FP8 || !careful) {
+      if constexpr (!careful) {
         add_pv(-1);
-      } else {
+      } else if constexpr (!FP8) {
 #pragma unroll 1
         for (int tok = 0; tok < rq.q_len; ++tok) add_pv(tok);
       }
@@ -610,15 +692,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
       else copy_commit();
     }
 
+    if (FP8 || careful) return false;
     float sum = 0.f;  // NaN where one of them is, and for infinities of both signs
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < C::kMT; ++i) sum += (o[i][nt][0] + o[i][nt][1]) + (o[i][nt][2] + o[i][nt][3]);
-    if (!FP8 && !careful && __any_sync(0xffffffffu, sum != sum)) {
-      careful = true;
-      goto again;
-    }
+    return (bool)__any_sync(0xffffffffu, sum != sum);
+   };
+    if (pass(std::false_type{})) pass(std::true_type{});
 
     // ------------------------------------------------ join the warps
     if constexpr (FP8) {  // the accumulators hold 2^(134 - e_ref) times the sum; in two normal factors
