@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // this grid ends after that one.
   auto wait_for_decode = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   const WorkerRec* rec_at = p.workers + kMaxWorkers + blockIdx.x;
-  if (rec_at->n == 0 || !planned(p)) {
+  const int places = rec_at->n;  // on its way while the signature is
+  if (!planned(p) || places == 0) {
     wait_for_decode();
     return;
   }
