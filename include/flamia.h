@@ -454,7 +454,11 @@ size_t flamia_paged_workspace_size(const flamia_paged_t* p);
  * FLAMIA_ERR_BAD_SEQLENS (cu_q, old_len or kv_len inconsistent, more than
  * max_q new tokens or more than max_pages pages), FLAMIA_ERR_BAD_PAGE (*n_free
  * outside [0, n_pages], or more pages given back than the stack has room
- * for), FLAMIA_ERR_NO_PAGES (fewer pages than the step needs).  Then no page
+ * for), FLAMIA_ERR_NO_PAGES (fewer pages than the step needs),
+ * FLAMIA_ERR_UNSUPPORTED (more attention than the work split counts: a
+ * request's tiles of 256 rows of one key/value head times the blocks of 128
+ * keys of its last tile above 2^31, or their sum over requests and heads above
+ * 2^38, with two blocks more for each tile).  Then no page
  * moves, *n_free_out = *n_free, every slot is -1, and launches that use the
  * workspace write nothing.  A new token whose page id (of the table or the
  * stack) lies outside [0, n_pages) gets slot -2, which flamia_paged_append

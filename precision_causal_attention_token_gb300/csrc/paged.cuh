@@ -34,6 +34,10 @@ constexpr int kMaxReq = 8192;
 // each stay below the limit of the chunk kernel's waits, whose longest is for
 // a tile's end.
 constexpr int kMaxChunkKeys = 1 << 25;
+// Places of a head's tiles of one request and of a line, at most: positions
+// within a head's tiles and a worker's share (kMaxPlaces over 128 or more
+// workers) are 32-bit.
+constexpr int64_t kMaxHeadPlaces = INT32_MAX, kMaxPlaces = (int64_t)1 << 38;
 
 struct PagedHeader {
   WsHeader base;       // status words first, as flamia_get_device_status reads them
@@ -78,6 +82,7 @@ struct PagedParams {
   int W_max[2];   // workers at most, of each line
   int small_rows; // requests of up to so many rows go to the decode kernel (8, 16, 32; 0: none)
   int half_toks;  // tokens of a tile's half (chunk kernel): 128 / G
+  int count_places;  // sizes at which the plan may pass the limits of places
   float c_log2;   // softmax_scale * log2(e)
   const int32_t* cu_q;
   const int32_t* kv_len;

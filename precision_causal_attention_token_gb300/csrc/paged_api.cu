@@ -92,6 +92,14 @@ flamia_status_t fill(const flamia_paged_t* p, void* ws, size_t ws_bytes, PagedPa
   a->small_rows = L.path == kPathDecode8 ? 8 : L.path == kPathDecode16 ? 16 : L.path == kPathDecode32 ? 32
                   : a->G <= 8 ? 8 : a->G <= 16 ? 16 : 0;
   a->half_toks = kChunkRows / 2 / a->G;
+  {
+    // tiles of a head, of one request and of all, times the longest there can be
+    const double keys = (double)p->max_pages * p->page_size, half = a->half_toks;
+    const double chunk_tile = keys / kChunkBlk + kChunkTileCost + 1, decode_tile = keys / kDecodeBlk + kDecodeTileCost + 1;
+    a->count_places = (a->max_q / (2 * half) + 1) * chunk_tile > (double)kMaxHeadPlaces ||
+                      (p->T / (2 * half) + p->n_req) * chunk_tile * p->Hkv > (double)kMaxPlaces ||
+                      p->n_req * decode_tile * p->Hkv > (double)kMaxPlaces;
+  }
   const float scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)p->d);
   a->c_log2 = scale * 1.44269504088896341f;
   // what the plan's records depend on (FNV-1a)

@@ -78,6 +78,24 @@ __device__ __forceinline__ int tile_places(const PagedParams& p, int line, int q
   return kChunkTileCost + max(1, (visible_keys(p.causal, q_len, kv_len, last) + kChunkBlk - 1) / kChunkBlk);
 }
 
+// Whether the step passes the limits of places, with a request's tiles all
+// taken as its longest (the last): every CTA of the launch finds the same,
+// before any page moves.
+__device__ bool too_large(const PagedParams& p, const int32_t* cu, int r0, int r1, int64_t* sm) {
+  int64_t mine[2] = {0, 0}, all[2];
+  int big = 0;
+  for (int r = r0; r < r1; ++r) {
+    const int ql = cu[r + 1] - cu[r], line = line_of(p, ql), nt = tiles_of(p, ql);
+    if (nt == 0) continue;
+    const int64_t head = (int64_t)nt * tile_places(p, line, ql, p.kv_len[r], nt - 1);
+    big |= head > kMaxHeadPlaces;
+    mine[line] += min(min(head, kMaxHeadPlaces) * p.Hkv, kMaxPlaces + 1);  // below 2^62; n_req of them below 2^52
+  }
+  block_scan(mine[0], sm, &all[0]);
+  block_scan(mine[1], sm, &all[1]);
+  return __syncthreads_or(big) || all[0] > kMaxPlaces || all[1] > kMaxPlaces;
+}
+
 __device__ void no_work(const PagedParams& p) {
   for (int w = threadIdx.x; w < kMaxWorkers + kMaxChunkWorkers; w += kPlanThreads) p.workers[w] = WorkerRec{};
 }
@@ -112,14 +130,6 @@ __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* per
     if (lane == 0) per[r] = sum;
   }
   __syncthreads();
-  // a worker's places and a head's are 32-bit
-  int big = 0;
-  for (int r = tid; r < n; r += kPlanThreads) big |= per[r] > (1 << 30);
-  if (__syncthreads_or(big)) {
-    if (tid == 0) report(&p.hdr->base, FLAMIA_ERR_UNSUPPORTED, 0x702);
-    no_work(p);
-    return;
-  }
   const int seg = (n + kPlanThreads - 1) / kPlanThreads, r0 = min(n, tid * seg), r1 = min(n, r0 + seg);
   int64_t cnt = 0, mine[2] = {0, 0}, cost[2], all;
   for (int r = r0; r < r1; ++r) {
@@ -132,11 +142,6 @@ __device__ void split_work(const PagedParams& p, const int32_t* cu, int64_t* per
   const int64_t at = block_scan(cnt, sm, &all);
   const int n0 = (int)(all & 0xFFFFFFFF), n1 = (int)(all >> 32);
   int64_t place[2] = {block_scan(mine[0], sm, &cost[0]), block_scan(mine[1], sm, &cost[1])};
-  if (cost[0] > ((int64_t)1 << 38) || cost[1] > ((int64_t)1 << 37)) {  // 2^30 places of a worker
-    if (tid == 0) report(&p.hdr->base, FLAMIA_ERR_UNSUPPORTED, 0x702);
-    no_work(p);
-    return;
-  }
   int idx[2] = {(int)(at & 0xFFFFFFFF), (int)(at >> 32)};
   for (int r = r0; r < r1; ++r) {
     const int ql = cu[r + 1] - cu[r];
@@ -298,6 +303,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     if (n_free < 0 || n_free > p.n_pages || (int64_t)n_free + n_given > p.n_pages) why = FLAMIA_ERR_BAD_PAGE;
     else if (n_taken > n_free + n_given) why = FLAMIA_ERR_NO_PAGES;
   }
+  if (p.count_places && !why && too_large(p, cu, r0, r1, sm)) why = FLAMIA_ERR_UNSUPPORTED;
   __syncthreads();
   const int top = n_free + n_given;
   if (first) {
