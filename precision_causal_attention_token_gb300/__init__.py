@@ -63,6 +63,7 @@ class Paged(ctypes.Structure):
 class Cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("v_scales", ctypes.c_void_p), ("page_stride", ctypes.c_int64)]
+    pool = None  # (Hkv, page_size, d, cache_dtype), n_pages of the tensors that paged_cache was given
 
 
 _lib = None
@@ -248,7 +249,9 @@ def _int32(t, n=None):
 
 def paged_cache(k, v, k_scales=None, v_scales=None) -> Cache:
     """One layer's pool: k, v [n_pages, Hkv, page_size, d] (bf16, or uint8 E4M3 codes with uint8 scales
-    [n_pages, Hkv, page_size]).  Pages may be strided (k = pool[:, 0], v = pool[:, 1]); a page is contiguous."""
+    [n_pages, Hkv, page_size]).  Pages may be strided (k = pool[:, 0], v = pool[:, 1]); a page is contiguous.  The calls
+    refuse a pool of another type or page shape than the problem's, or of fewer pages."""
+    import torch
     if k.shape != v.shape or k.stride() != v.stride() or k.dim() != 4 or k.dtype != v.dtype:
         raise ValueError("k and v must be [n_pages, Hkv, page_size, d] of one type and layout")
     if k[0].is_contiguous() is False:
@@ -257,7 +260,10 @@ def paged_cache(k, v, k_scales=None, v_scales=None) -> Cache:
         if s is not None and (s.shape != k.shape[:3] or s.element_size() != 1 or not s.is_contiguous()):
             raise ValueError("scales must be contiguous bytes [n_pages, Hkv, page_size]")
     stride = k.stride(0) if k.shape[0] > 1 else 0
-    return Cache(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), stride)
+    cache = Cache(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), stride)
+    dtype = {torch.bfloat16: BF16, torch.uint8: E4M3, torch.float8_e4m3fn: E4M3}.get(k.dtype)
+    cache.pool = (*k.shape[1:], dtype), k.shape[0]
+    return cache
 
 
 def flamia_paged_workspace_size(prob: Paged) -> int:
@@ -286,13 +292,22 @@ def flamia_paged_plan(prob: Paged, ws, slot_map=None, old_len=None, free_pages=N
                 _ptr(n_free_out))
 
 
+def _check_pool(prob, cache, where):
+    if cache.pool is not None:
+        page, n_pages = cache.pool
+        if page != (prob.Hkv, prob.page_size, prob.d, prob.cache_dtype) or n_pages < prob.n_pages:
+            raise FlamiaError(ERR_INVALID_ARG, where)
+
+
 def flamia_paged_append(prob: Paged, k, v, slot_map, cache: Cache, ws, stream=None):
     """The step's K and V rows into their slots of one layer's cache."""
+    _check_pool(prob, cache, "flamia_paged_append")
     _paged_call("flamia_paged_append", ws, stream, prob, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), cache)
 
 
 def flamia_paged_fwd(prob: Paged, q, cache: Cache, O, lse, ws, stream=None):
     """Attention of the step's queries over one layer's cache (lse may be None)."""
+    _check_pool(prob, cache, "flamia_paged_fwd")
     _paged_call("flamia_paged_fwd", ws, stream, prob, q.data_ptr(), cache, O.data_ptr(), _ptr(lse))
 
 
