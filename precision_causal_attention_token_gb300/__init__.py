@@ -256,6 +256,8 @@ def paged_cache(k, v, k_scales=None, v_scales=None) -> Cache:
         raise ValueError("k and v must be [n_pages, Hkv, page_size, d] of one type and layout")
     if k[0].is_contiguous() is False:
         raise ValueError("the pages of k and v must be contiguous")
+    if k.shape[0] > 1 and k.stride(0) < k[0].numel():
+        raise ValueError("the pages of k (and of v) must not share memory")
     for s in (k_scales, v_scales):
         if s is not None and (s.shape != k.shape[:3] or s.element_size() != 1 or not s.is_contiguous()):
             raise ValueError("scales must be contiguous bytes [n_pages, Hkv, page_size]")

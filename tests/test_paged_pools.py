@@ -41,3 +41,12 @@ def _refuses(prob, k, ok, monkeypatch):
                 call()
             assert e.value.status == fl.ERR_INVALID_ARG
     assert len(calls) == (2 if ok else 0)
+
+
+def test_pages_that_share_memory_are_refused():
+    """An expanded pool: one page's memory for all of them, which would be read and written as if it were a whole pool."""
+    one, two = torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(5 * 1024 + 2048, dtype=torch.bfloat16)
+    fl.paged_cache(one, one)
+    for k in (one.expand(4, -1, -1, -1), two.as_strided((5, 2, 16, 64), (1024, 1024, 64, 1))):
+        with pytest.raises(ValueError):
+            fl.paged_cache(k, k)
