@@ -451,15 +451,16 @@ class PagedCall:
         self.kv_dtype = torch.bfloat16 if self.in_dtype == BF16 else torch.float32
 
     @staticmethod
-    def _check(where, *tensors):
+    def _check(where, device, *tensors):
         for x, shape, dtype in tensors:
-            if tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_contiguous():
+            if (tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_contiguous() or
+                    device not in (None, x.device)):
                 raise FlamiaError(ERR_INVALID_ARG, "PagedCall." + where)
 
     def plan(self, cu_q, kv_len):
         """cu_q [n_req + 1], kv_len [n_req]: int32 tensors; kv_len counts the step's new tokens too."""
         import torch
-        self._check("plan", (cu_q, self.cu_q.shape, torch.int32), (kv_len, self.kv_len.shape, torch.int32))
+        self._check("plan", None, (cu_q, self.cu_q.shape, torch.int32), (kv_len, self.kv_len.shape, torch.int32))
         self.cu_q.copy_(cu_q, non_blocking=True)
         self.kv_len.copy_(kv_len, non_blocking=True)
         flamia_paged_plan(self.prob, self.ws, self.slot_map, self.held_len, self.free_pages, self.n_free, self.n_free)
@@ -468,11 +469,11 @@ class PagedCall:
     def append(self, layer, k, v):
         """k, v [T, Hkv, d] (in_dtype, contiguous); rows behind cu_q[n_req] may hold anything."""
         rows, dtype = (self.T, self.Hkv, self.d), self.kv_dtype
-        self._check("append", (k, rows, dtype), (v, rows, dtype))
+        self._check("append", self.ws.device, (k, rows, dtype), (v, rows, dtype))
         flamia_paged_append(self.prob, k, v, self.slot_map, self.caches[layer], self.ws)
 
     def attend(self, layer, q):
         """q [T, H, d] bf16, contiguous; returns (O, lse), overwritten by the next call."""
-        self._check("attend", (q, self.O.shape, self.O.dtype))
+        self._check("attend", self.ws.device, (q, self.O.shape, self.O.dtype))
         flamia_paged_fwd(self.prob, q, self.caches[layer], self.O, self.lse, self.ws)
         return self.O, self.lse

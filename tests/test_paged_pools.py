@@ -50,3 +50,14 @@ def test_pages_that_share_memory_are_refused():
     for k in (one.expand(4, -1, -1, -1), two.as_strided((5, 2, 16, 64), (1024, 1024, 64, 1))):
         with pytest.raises(ValueError):
             fl.paged_cache(k, k)
+
+
+def test_paged_call_refuses_tensors_of_another_device():
+    """Before anything is launched: a pointer of another device is no address on this one."""
+    c = fl.PagedCall(n_req=2, T=6, H=4, Hkv=2, d=64, page_size=16, n_pages=8, max_pages=3, device="cpu")
+    away = lambda h: torch.zeros(6, h, 64, dtype=torch.bfloat16, device="meta")  # noqa: E731
+    here = torch.zeros(6, 2, 64, dtype=torch.bfloat16)
+    for call in (lambda: c.append(0, away(2), here), lambda: c.append(0, here, away(2)), lambda: c.attend(0, away(4))):
+        with pytest.raises(fl.FlamiaError) as e:
+            call()
+        assert e.value.status == fl.ERR_INVALID_ARG
