@@ -20,7 +20,8 @@
 // E4M3: codes become f16 (exact, one instruction for two).  The queries are
 // f16 with a power-of-two row scale (bf16's 8 significant bits fit; the scale
 // puts the row's largest element at 2^13, so what f16 cannot hold lies 2^-37
-// below it); the key's scale multiplies its scores.  The weights are f16
+// below it); the key's scale, less 2^12, multiplies its scores, which so stay
+// below 2^128 for keys up to 2^119 at any query.  The weights are f16
 // (2^-11 relative), times 2^(e - E + 7) with e the key's V exponent and E the
 // largest seen so far: at most 2^15; E's rise rescales the accumulators.  E
 // counts keys that a row may not see, that have no weight in it or that hold
@@ -207,7 +208,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         // times 2^(139 - E) it is below 2^13 (E clamped: the factor and its inverse stay normal)
         const int E = min(max((int)(top >> 7), 13), 254);
         const float up = exp2i(139 - E);
-        scale = fmaxf(scale * exp2i(E - 139), 1.17549435e-38f);  // above 0: a masked -inf stays one
+        // with the 2^12 that the keys' scales lack; above 0: a masked -inf stays one
+        scale = fminf(fmaxf(scale * exp2i(E - 127), 1.17549435e-38f), 3.4e38f);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         const uint8_t* sk = scl.b[warp][it & 1][0];
 #pragma unroll
         for (int i = 0; i < C::kSub; ++i) {
-          const float f0 = ue8m0(sk[16 * i + g]), f1 = ue8m0(sk[16 * i + 8 + g]);
+          const float f0 = ue8m0(sk[16 * i + g]) * 0x1p-12f, f1 = ue8m0(sk[16 * i + 8 + g]) * 0x1p-12f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -141,3 +141,14 @@ def test_a_nan_row_beside_sizes_far_apart(q):
     compare(O[:first], wO[:first], tO[:first], "O")
     compare(lse, wl, tl, "lse")
     assert math.isfinite(float(lse.abs().max()))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("up", [115, 60, -60, -115])
+def test_large_keys_and_small_queries(kind, d, up):
+    """Keys of 2^115 against queries of 2^-115, and the other way: the scores are ordinary numbers."""
+    s = step(kind, d=d, ps=16, seed=13)
+    s.ks += up
+    s.q_rows.copy_((s.q_rows.float() * 2.0 ** -up).bfloat16())
+    check(s)
