@@ -28,7 +28,7 @@ def check(s):
         kv = s.kv_len[r]
         for h in range(s.Hkv):
             _, V = s.rows_of(r, h)
-            sums = torch.cat([torch.zeros_like(V[:1]), V.abs().cumsum(0)])  # of the first keys
+            sums = torch.cat([V.new_zeros(1, s.d), V.abs().cumsum(0)])  # of the first keys
             sees = [max(0, kv - n + i + 1) if s.causal else kv for i in range(n)]
             tO[row:row + n, h * G:(h + 1) * G] += FLOOR * sums[sees][:, None]  # few rows: also in a call with chunks
         row += n
