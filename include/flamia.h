@@ -481,8 +481,16 @@ flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, cons
  * <q_i, k_j> over the keys j that row i sees,
  *   O_i = sum_j exp(x_ij - lse_i) v_j,   lse_i = ln sum_j exp(x_ij).
  * Query head h reads key/value head h / (H / Hkv).  Scores, softmax
- * statistics and accumulators are fp32; the weights are rounded to bf16 for
- * the P V product (decode kernel: to two bf16 terms).
+ * statistics and accumulators are fp32.  Rounding of the weights for the P V
+ * product, relative to each:
+ *   chunk kernel                  bf16, 2^-8
+ *   decode kernel, bf16 cache     two bf16 terms, 2^-16
+ *   decode kernel, E4M3 cache     f16, 2^-11, and below that at most 2^-20 of
+ *                                 the row's largest weight; two bf16 terms
+ *                                 where the scale bytes of the V rows that a
+ *                                 warp takes lie more than 12 apart
+ * Keys that a row does not see, and what slots behind a request's last token
+ * hold, change no row's precision beyond that.
  *   q    device bf16 [T][H][d] (q_stride)
  *   O    device bf16 [T][H][d], contiguous
  *   lse  device float [H][T], natural logarithm (may be NULL)

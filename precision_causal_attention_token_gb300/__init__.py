@@ -402,7 +402,7 @@ class PagedCall:
     One step: ``plan(cu_q, kv_len)`` once, then per layer ``append(layer, k, v)`` and ``attend(layer, q)``; all on the
     current stream, no host synchronisation, so a step can be captured in a CUDA graph (cu_q and kv_len are then read
     from the tensors given at capture).  A request that ends passes kv_len 0; its pages serve others.  After a plan
-    whose status is ERR_NO_PAGES no page has moved: plan again with other lengths."""
+    whose status is not OK (ERR_NO_PAGES, say) no page has moved: plan again with other lengths."""
 
     n_req: int
     T: int           # new tokens of a step at most
@@ -458,7 +458,8 @@ class PagedCall:
                 raise FlamiaError(ERR_INVALID_ARG, "PagedCall." + where)
 
     def plan(self, cu_q, kv_len):
-        """cu_q [n_req + 1], kv_len [n_req]: int32 tensors; kv_len counts the step's new tokens too."""
+        """cu_q [n_req + 1], kv_len [n_req]: int32 tensors; kv_len counts the step's new tokens too.  They are copied
+        on the stream: pinned host tensors must keep their values until that has run."""
         import torch
         self._check("plan", None, (cu_q, self.cu_q.shape, torch.int32), (kv_len, self.kv_len.shape, torch.int32))
         self.cu_q.copy_(cu_q, non_blocking=True)

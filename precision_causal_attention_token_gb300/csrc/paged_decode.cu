@@ -35,7 +35,7 @@
 //
 // Measured (152 SMs, H = 32, Hkv = 8, d = 128): one request of 65,522 bf16
 // tokens 57 us (268 MB; 46 us at the last SM's last load, then the join), 64
-// requests in E4M3 109 us (578 MB, 5.3 TB/s; the SMs' loops end between 73 and
+// requests in E4M3 108 to 114 us (578 MB, 5.2 TB/s; the SMs' loops end between 73 and
 // 105 us, the same SMs first every time), 6 short requests 7.7 us, 16 requests of 2 to 8
 // drafted tokens in E4M3 62 us.  Up to 16 rows HBM bounds it; with 32 the
 // latency of one warp's 1,100 instructions a chunk does, at eight warps an SM
