@@ -62,7 +62,7 @@ typedef enum {
 /* [SUM] §3.4: the two default training paths. */
 typedef enum { FLAMIA_PATH_MXFP8 = 0, FLAMIA_PATH_NVFP4_FP8 = 1 } flamia_path_t;
 
-typedef enum { FLAMIA_F32 = 0, FLAMIA_BF16 = 1, FLAMIA_E4M3 = 2 /* paged caches only */ } flamia_dtype_t;
+typedef enum { FLAMIA_F32 = 0, FLAMIA_BF16 = 1, FLAMIA_E4M3 = 2, FLAMIA_E2M1 = 3 /* both: paged caches only */ } flamia_dtype_t;
 
 typedef enum { FLAMIA_ROLE_QKV = 0, FLAMIA_ROLE_DO = 1 } flamia_role_t;
 
@@ -353,13 +353,20 @@ flamia_status_t flamia_plan_noalloc(const flamia_problem_t* p, int2* fwd_items, 
  * The cache of a layer is a pool of pages; a page holds `page_size`
  * consecutive tokens of one request for all key/value heads, head-major, so
  * that one head's tokens of a page are one contiguous run:
- *   K, V codes  [n_pages][Hkv][page_size][d]   bf16 or E4M3
- *   scales      [n_pages][Hkv][page_size]      E4M3 only: the UE8M0 byte of
+ *   K, V codes  [n_pages][Hkv][page_size][d]   bf16 or E4M3; E2M1:
+ *               [n_pages][Hkv][page_size][d/2], two codes a byte, channel 2k in
+ *               the low nibble (as flamia_operand_t's codes4)
+ *   scales      [n_pages][Hkv][page_size]      E4M3 and E2M1: the UE8M0 byte of
  *               each (token, head) row, as flamia_quantize's exact option
- *               writes them: the row's value is code * 2^(byte - 127).  Byte
- *               255 marks a row that holds a NaN or an infinity: all of it
+ *               writes them for E4M3: the row's value is code * 2^(byte - 127).
+ *               Byte 255 marks a row that holds a NaN or an infinity: all of it
  *               reads as NaN.  (A NaN code 0x7F or 0xFF under any other byte is
  *               not written by flamia_paged_append and must not occur.)
+ *   blocks      [n_pages][Hkv][page_size][d/16]  E2M1 only: the E4M3 scale of
+ *               each 16 channels of a row, not negative: the value is
+ *               code * block scale * 2^(byte - 127).  The exponent is a power of
+ *               two, unlike gscale4 of flamia_operand_t, so that a value keeps
+ *               at most six significant bits and is exact in bf16 and f16.
  * Token j of request r lies in page block_table[r][j / page_size], row
  * j % page_size; its slot is page * page_size + row.
  *
@@ -379,7 +386,7 @@ flamia_status_t flamia_plan_noalloc(const flamia_problem_t* p, int2* fwd_items, 
  *   n_pages      pages of the pool; n_pages * page_size < 2^31
  *   max_pages    columns of the block table; max_pages * page_size <= 2^30
  *                (2^25 where max_q * H / Hkv > 32)
- *   cache_dtype  FLAMIA_BF16 or FLAMIA_E4M3
+ *   cache_dtype  FLAMIA_BF16, FLAMIA_E4M3 or FLAMIA_E2M1 (4 bits a value)
  *   in_dtype     dtype of the K and V rows given to flamia_paged_append:
  *                FLAMIA_BF16 or FLAMIA_F32
  *   causal       1: new token i of a request, at position kv_len - q_len + i,
@@ -416,15 +423,18 @@ typedef struct {
 } flamia_paged_t;
 
 /* One layer's cache (device pointers, caller-owned; k_scales and v_scales
- * are NULL for bf16).  page_stride: elements between two pages of k and of v
- * (0: Hkv * page_size * d, contiguous; else at least that, a multiple of 16
- * bytes), so that K and V pages can be interleaved in one buffer. */
+ * are NULL for bf16, k_blocks and v_blocks read for E2M1 only).  page_stride:
+ * elements between two pages of k and of v (0: Hkv * page_size * d, contiguous;
+ * else at least that, a multiple of 16 bytes), so that K and V pages can be
+ * interleaved in one buffer. */
 typedef struct {
   void* k;
   void* v;
   void* k_scales;
   void* v_scales;
   int64_t page_stride;
+  void* k_blocks;
+  void* v_blocks;
 } flamia_cache_t;
 
 /* Bytes of device workspace for `p` (0 if `p` is invalid). */
@@ -471,7 +481,10 @@ flamia_status_t flamia_paged_plan(const flamia_paged_t* p, int32_t* slot_map, co
  * their slots: rounded to bf16, or as E4M3 codes with the row's no-clamp
  * exponent (the smallest e with max|x| <= 448 2^e, clamped to [-127, 127]; 0
  * for a zero row), byte for byte those of flamia_quantize with `exact` for
- * finite rows.  A slot of -1 skips the row; slots must be distinct.  Any
+ * finite rows; or as E2M1 codes: e is the smallest exponent with max|x| <=
+ * 2688 2^e (2688 = 6 * 448; clamped alike, 0 for a zero row), a block scale s
+ * the smallest E4M3 value with 6 s 2^e >= its 16 channels' max|x|, a code
+ * RNE(x 2^-e / s) (0 where s is 0), of the exact quotient.  A slot of -1 skips the row; slots must be distinct.  Any
  * other slot outside the pool is skipped and sets FLAMIA_ERR_BAD_PAGE.  Requires
  * flamia_paged_plan on the same workspace. */
 flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, const void* v, const int32_t* slot_map,
@@ -485,7 +498,7 @@ flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, cons
  * product, relative to each:
  *   chunk kernel                  bf16, 2^-8
  *   decode kernel, bf16 cache     two bf16 terms, 2^-16
- *   decode kernel, E4M3 cache     f16, 2^-11, and below that at most 2^-20 of
+ *   decode kernel, E4M3 or E2M1   f16, 2^-11, and below that at most 2^-20 of
  *                                 the row's largest weight; two bf16 terms
  *                                 where the scale bytes of the V rows that a
  *                                 warp takes lie more than 12 apart

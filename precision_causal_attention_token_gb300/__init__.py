@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(_PKG, "lib", "libflamia.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE_TOO_SMALL, ERR_CUDA, ERR_TIMEOUT, ERR_BAD_SEQLENS = range(7)
 ERR_NO_PAGES, ERR_BAD_PAGE = 7, 8
 PATH_MXFP8, PATH_NVFP4_FP8 = 0, 1
-F32, BF16, E4M3 = 0, 1, 2
+F32, BF16, E4M3, E2M1 = 0, 1, 2, 3
 ROLE_QKV, ROLE_DO = 0, 1
 
 EXPORTED = ("flamia_workspace_size", "flamia_plan", "flamia_quantize", "flamia_fwd", "flamia_bwd",
@@ -62,7 +62,8 @@ class Paged(ctypes.Structure):
 
 class Cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
-                ("v_scales", ctypes.c_void_p), ("page_stride", ctypes.c_int64)]
+                ("v_scales", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("k_blocks", ctypes.c_void_p),
+                ("v_blocks", ctypes.c_void_p)]
     pool = None  # (Hkv, page_size, d, cache_dtype), n_pages of the tensors that paged_cache was given
 
 
@@ -247,10 +248,12 @@ def _int32(t, n=None):
                          f"{t.dtype}")
 
 
-def paged_cache(k, v, k_scales=None, v_scales=None) -> Cache:
+def paged_cache(k, v, k_scales=None, v_scales=None, k_blocks=None, v_blocks=None) -> Cache:
     """One layer's pool: k, v [n_pages, Hkv, page_size, d] (bf16, or uint8 E4M3 codes with uint8 scales
-    [n_pages, Hkv, page_size]).  Pages may be strided (k = pool[:, 0], v = pool[:, 1]); a page is contiguous.  The calls
-    refuse a pool of another type or page shape than the problem's, or of fewer pages."""
+    [n_pages, Hkv, page_size]), or uint8 [n_pages, Hkv, page_size, d / 2] (two E2M1 codes a byte) with such scales and
+    block scales [n_pages, Hkv, page_size, d / 16] (uint8 or float8_e4m3fn).  Pages may be strided (k = pool[:, 0],
+    v = pool[:, 1]); a page is contiguous.  The calls refuse a pool of another type or page shape than the problem's, or
+    of fewer pages."""
     import torch
     if k.shape != v.shape or k.stride() != v.stride() or k.dim() != 4 or k.dtype != v.dtype:
         raise ValueError("k and v must be [n_pages, Hkv, page_size, d] of one type and layout")
@@ -261,10 +264,19 @@ def paged_cache(k, v, k_scales=None, v_scales=None) -> Cache:
     for s in (k_scales, v_scales):
         if s is not None and (s.shape != k.shape[:3] or s.element_size() != 1 or not s.is_contiguous()):
             raise ValueError("scales must be contiguous bytes [n_pages, Hkv, page_size]")
+    e2m1 = k_blocks is not None or v_blocks is not None
+    if e2m1:
+        for s in (k_blocks, v_blocks):
+            if (s is None or s.shape[:3] != k.shape[:3] or s.dim() != 4 or 8 * s.shape[3] != k.shape[3] or
+                    s.element_size() != 1 or not s.is_contiguous()):
+                raise ValueError("block scales must be contiguous bytes [n_pages, Hkv, page_size, d / 16]")
+        if k.dtype != torch.uint8 or k_scales is None or v_scales is None:
+            raise ValueError("block scales go with uint8 codes and their scales")
     stride = k.stride(0) if k.shape[0] > 1 else 0
-    cache = Cache(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), stride)
-    dtype = {torch.bfloat16: BF16, torch.uint8: E4M3, torch.float8_e4m3fn: E4M3}.get(k.dtype)
-    cache.pool = (*k.shape[1:], dtype), k.shape[0]
+    cache = Cache(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), 2 * stride if e2m1 else stride, _ptr(k_blocks),
+                  _ptr(v_blocks))
+    dtype = E2M1 if e2m1 else {torch.bfloat16: BF16, torch.uint8: E4M3, torch.float8_e4m3fn: E4M3}.get(k.dtype)
+    cache.pool = (*k.shape[1:3], k.shape[3] * (2 if e2m1 else 1), dtype), k.shape[0]
     return cache
 
 
@@ -438,14 +450,17 @@ class PagedCall:
             raise FlamiaError(ERR_INVALID_ARG, "flamia_paged_workspace_size")
         self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.status = self.ws[:4].view(torch.int32)
-        shape = (self.layers, self.n_pages, self.Hkv, self.page_size, self.d)
-        e4m3 = self.cache_dtype == E4M3
-        self.k, self.v = (torch.zeros(shape, dtype=torch.uint8 if e4m3 else torch.bfloat16, device=self.device)
-                          for _ in range(2))
-        self.k_scales, self.v_scales = ((torch.full(shape[:4], 127, dtype=torch.uint8, device=self.device)
-                                         for _ in range(2)) if e4m3 else (None, None))
-        self.caches = [paged_cache(self.k[i], self.v[i], *((self.k_scales[i], self.v_scales[i]) if e4m3 else ()))
-                       for i in range(self.layers)]
+        rows = (self.layers, self.n_pages, self.Hkv, self.page_size)
+        codes, e2m1 = self.cache_dtype in (E4M3, E2M1), self.cache_dtype == E2M1
+
+        def pair(shape, fill, dtype=torch.uint8):
+            return [torch.full(shape, fill, dtype=dtype, device=self.device) for _ in range(2)]
+
+        self.k, self.v = pair((*rows, self.d // 2 if e2m1 else self.d), 0, torch.uint8 if codes else torch.bfloat16)
+        self.k_scales, self.v_scales = pair(rows, 127) if codes else (None, None)
+        self.k_blocks, self.v_blocks = pair((*rows, self.d // 16), 0) if e2m1 else (None, None)
+        pools = [x for x in (self.k, self.v, self.k_scales, self.v_scales, self.k_blocks, self.v_blocks) if x is not None]
+        self.caches = [paged_cache(*layer) for layer in zip(*pools)]
         self.O = torch.zeros(self.T, self.H, self.d, dtype=torch.bfloat16, device=self.device)
         self.lse = torch.zeros(self.H, self.T, dtype=torch.float32, device=self.device)
         self.kv_dtype = torch.bfloat16 if self.in_dtype == BF16 else torch.float32

@@ -23,6 +23,8 @@ namespace flamia {
 // Requests with few rows (one new token, a few drafted ones) are served by
 // the decode kernel, the others by the chunk kernel: two lines.
 // ---------------------------------------------------------------------------
+// What the cache holds.
+enum { kCacheBF16 = 0, kCacheE4M3 = 1, kCacheE2M1 = 2 };
 enum { kPathDecode8 = 0, kPathDecode16 = 1, kPathDecode32 = 2, kPathChunk = 3 };
 constexpr int kDecodeBlk = 64, kChunkBlk = 128, kChunkRows = 256;
 // What a tile costs beside its blocks, in blocks: its queries, first loads and
@@ -110,15 +112,17 @@ struct PagedParams {
   uint8_t* v;
   uint8_t* k_scales;
   uint8_t* v_scales;
+  uint8_t* k_blocks;  // E2M1: block scales
+  uint8_t* v_blocks;
   int64_t page_bytes;  // between pages of k (and of v)
   __nv_bfloat16* O;
   float* lse;
 };
 
 cudaError_t launch_paged_plan(const PagedParams& p, cudaStream_t st);
-cudaError_t launch_paged_append(const PagedParams& p, int d, bool e4m3, bool in_bf16, int sms, cudaStream_t st);
-cudaError_t launch_paged_decode(const PagedParams& p, int d, bool e4m3, cudaStream_t st);
-cudaError_t launch_paged_chunk(const PagedParams& p, int d, bool e4m3, const CUtensorMap& mq, const CUtensorMap& mk,
+cudaError_t launch_paged_append(const PagedParams& p, int d, int cache, bool in_bf16, int sms, cudaStream_t st);
+cudaError_t launch_paged_decode(const PagedParams& p, int d, int cache, cudaStream_t st);
+cudaError_t launch_paged_chunk(const PagedParams& p, int d, int cache, const CUtensorMap& mq, const CUtensorMap& mk,
                                const CUtensorMap& mv, cudaStream_t st);
 // Workers of a launch on a GPU with `sms` SMs: what the kernel keeps resident.
 int paged_decode_workers(int sms);

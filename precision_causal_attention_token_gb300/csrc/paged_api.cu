@@ -31,7 +31,7 @@ flamia_status_t validate(const flamia_paged_t* p) {
     return FLAMIA_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return FLAMIA_ERR_UNSUPPORTED;
   if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) return FLAMIA_ERR_UNSUPPORTED;
-  if (p->cache_dtype != FLAMIA_BF16 && p->cache_dtype != FLAMIA_E4M3) return FLAMIA_ERR_UNSUPPORTED;
+  if (p->cache_dtype != FLAMIA_BF16 && p->cache_dtype != FLAMIA_E4M3 && p->cache_dtype != FLAMIA_E2M1) return FLAMIA_ERR_UNSUPPORTED;
   if (p->in_dtype != FLAMIA_BF16 && p->in_dtype != FLAMIA_F32) return FLAMIA_ERR_UNSUPPORTED;
   if (p->n_req > kMaxReq || p->T > (1 << 30) || p->H / p->Hkv > kChunkRows / 2) return FLAMIA_ERR_UNSUPPORTED;
   if ((int64_t)p->T * p->H * p->d >= (int64_t)1 << 40) return FLAMIA_ERR_UNSUPPORTED;
@@ -124,17 +124,26 @@ flamia_status_t fill(const flamia_paged_t* p, void* ws, size_t ws_bytes, PagedPa
   return FLAMIA_OK;
 }
 
+int cache_of(const flamia_paged_t* p) {
+  return p->cache_dtype == FLAMIA_BF16 ? kCacheBF16 : p->cache_dtype == FLAMIA_E4M3 ? kCacheE4M3 : kCacheE2M1;
+}
+
 flamia_status_t fill_cache(const flamia_paged_t* p, const flamia_cache_t* c, PagedParams* a) {
   if (!c || !dev16(c->k) || !dev16(c->v)) return FLAMIA_ERR_INVALID_ARG;
-  const bool e4m3 = p->cache_dtype == FLAMIA_E4M3;
-  if (e4m3 ? !dev16(c->k_scales) || !dev16(c->v_scales) : c->k_scales || c->v_scales) return FLAMIA_ERR_INVALID_ARG;
-  const int64_t page = (int64_t)p->Hkv * p->page_size * p->d, el = e4m3 ? 1 : 2;
-  if (c->page_stride && (c->page_stride < page || c->page_stride * el % 16)) return FLAMIA_ERR_INVALID_ARG;
-  a->page_bytes = (c->page_stride ? c->page_stride : page) * el;
+  const int cache = cache_of(p);
+  if (cache != kCacheBF16 ? !dev16(c->k_scales) || !dev16(c->v_scales) : c->k_scales || c->v_scales) return FLAMIA_ERR_INVALID_ARG;
+  if (cache == kCacheE2M1 && (!dev16(c->k_blocks) || !dev16(c->v_blocks))) return FLAMIA_ERR_INVALID_ARG;
+  const int64_t page = (int64_t)p->Hkv * p->page_size * p->d, per_16 = cache == kCacheBF16 ? 8 : cache == kCacheE4M3 ? 16 : 32;
+  if (c->page_stride && (c->page_stride < page || c->page_stride % per_16)) return FLAMIA_ERR_INVALID_ARG;
+  a->page_bytes = (c->page_stride ? c->page_stride : page) / per_16 * 16;
   a->k = static_cast<uint8_t*>(c->k);
   a->v = static_cast<uint8_t*>(c->v);
   a->k_scales = static_cast<uint8_t*>(c->k_scales);
   a->v_scales = static_cast<uint8_t*>(c->v_scales);
+  if (cache == kCacheE2M1) {
+    a->k_blocks = static_cast<uint8_t*>(c->k_blocks);
+    a->v_blocks = static_cast<uint8_t*>(c->v_blocks);
+  }
   return FLAMIA_OK;
 }
 
@@ -214,7 +223,7 @@ flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, cons
   a.k_new = k;
   a.v_new = v;
   a.slots = slot_map;
-  return of(launch_paged_append(a, p->d, p->cache_dtype == FLAMIA_E4M3, p->in_dtype == FLAMIA_BF16, sm_count(), stream));
+  return of(launch_paged_append(a, p->d, cache_of(p), p->in_dtype == FLAMIA_BF16, sm_count(), stream));
 }
 
 flamia_status_t flamia_paged_fwd(const flamia_paged_t* p, const void* q, const flamia_cache_t* cache, void* O, float* lse,
@@ -227,15 +236,15 @@ flamia_status_t flamia_paged_fwd(const flamia_paged_t* p, const void* q, const f
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.O = static_cast<__nv_bfloat16*>(O);
   a.lse = lse;
-  const bool e4m3 = p->cache_dtype == FLAMIA_E4M3;
+  const int kind = cache_of(p);
   if (a.small_rows) {
-    const cudaError_t e = launch_paged_decode(a, p->d, e4m3, stream);
+    const cudaError_t e = launch_paged_decode(a, p->d, kind, stream);
     if (e != cudaSuccess || a.path != kPathChunk) return of(e);
   }
   CUtensorMap mq{}, mk{}, mv{};
-  if (!make_q_map(&mq, a, p->d) || (!e4m3 && (!make_pages_map(&mk, a.k, a, p->d) || !make_pages_map(&mv, a.v, a, p->d))))
+  if (!make_q_map(&mq, a, p->d) || (kind == kCacheBF16 && (!make_pages_map(&mk, a.k, a, p->d) || !make_pages_map(&mv, a.v, a, p->d))))
     return FLAMIA_ERR_CUDA;
-  return of(launch_paged_chunk(a, p->d, e4m3, mq, mk, mv, stream));
+  return of(launch_paged_chunk(a, p->d, kind, mq, mk, mv, stream));
 }
 
 }  // extern "C"

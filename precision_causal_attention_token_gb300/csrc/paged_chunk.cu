@@ -15,16 +15,16 @@
 //              row's accumulator), and writes the weights back as bf16 over
 //              the scores, from where the P V product reads them as its A
 //              operand: P never touches shared memory.
-//   warps 8-11 loaders.  E4M3: each block's codes from the raw ring into bf16
-//              tiles, times the row's scale (exact).  Both: zeros in rows past
+//   warps 8-11 loaders.  E4M3, E2M1: each block's codes from the raw ring into
+//              bf16 tiles, times the row's scale (and the block's; exact).  All: zeros in rows past
 //              the request's last key, where pages hold what an earlier owner
 //              left: 0 x NaN is NaN.  For the same reason they take infinities
 //              and NaN out of V in the blocks that some row sees in part, and
 //              leave word of the first such key, so that the rows that do see
 //              it get them back.
 //   warp 12    producer: the block's pages, one copy per page and 64 channels
-//              (bf16, TMA into the swizzled tile) or one per page (E4M3 codes
-//              and scale bytes, into the raw ring).
+//              (bf16, TMA into the swizzled tile) or one per page (codes, scale
+//              bytes and E2M1's block scales, into the raw ring).
 //   warp 13    MMA issuer.
 //   warp 14    scheduler: the worker's tiles (the plan's split).
 //   warp 15    the queries of each half, as soon as its last scores of the
@@ -41,6 +41,7 @@
 // the MMAs' operands share: a step's operands take 1,536 of its 2,048 tensor
 // cycles, codes and converted tiles 1,024 more.
 #include <climits>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -66,19 +67,24 @@ struct Frag {
   int end;
 };
 
-template <int D, bool FP8>
+// FP8 below: codes under a row exponent (E4M3, E2M1), converted by the loaders.
+template <int D, int CACHE>
 struct Cfg {
+  static constexpr bool kCodes = CACHE != kCacheBF16, kFp4 = CACHE == kCacheE2M1;
   static constexpr int kTileB = 128 * D * 2;        // bytes of a bf16 tile of 128 rows
-  static constexpr int kStages = FP8 ? 3 : 4;       // K/V tiles
-  static constexpr int kRaw = FP8 ? 3 : 0;          // raw E4M3 tiles
-  static constexpr int kRawB = 128 * D;
+  static constexpr int kStages = kCodes ? 3 : 4;    // K/V tiles
+  static constexpr int kRaw = kCodes ? 3 : 0;       // raw tiles of codes
+  static constexpr int kCodeB = kFp4 ? D / 2 : D;   // bytes of a row's codes
+  static constexpr int kBlkB = kFp4 ? D / 16 : 0;   // and of its block scales, behind the tile's codes
+  static constexpr int kRawB = 128 * (kCodeB + kBlkB);
 };
 
-template <int D, bool FP8>
+template <int D, int CACHE>
 struct __align__(1024) Tiles {
-  uint8_t q[2][Cfg<D, FP8>::kTileB];  // [half][d / 64][128 rows][128 bytes]
-  uint8_t kv[Cfg<D, FP8>::kStages][Cfg<D, FP8>::kTileB];
-  uint8_t raw[FP8 ? Cfg<D, FP8>::kRaw : 1][FP8 ? Cfg<D, FP8>::kRawB : 1024];
+  using C = Cfg<D, CACHE>;
+  uint8_t q[2][C::kTileB];  // [half][d / 64][128 rows][128 bytes]
+  uint8_t kv[C::kStages][C::kTileB];
+  uint8_t raw[C::kCodes ? C::kRaw : 1][C::kCodes ? C::kRawB : 1024];
   uint8_t out[8][2048];  // softmax warps: 32 rows x 32 channels of O on their way out
 };
 
@@ -94,8 +100,8 @@ struct Ctl {
   int abort_flag;
 };
 
-template <int D, bool FP8>
-constexpr size_t smem_bytes() { return sizeof(Tiles<D, FP8>) + sizeof(Ctl) + 1024; }
+template <int D, int CACHE>
+constexpr size_t smem_bytes() { return sizeof(Tiles<D, CACHE>) + sizeof(Ctl) + 1024; }
 
 // D[tmem] (+)= A[smem] * B[smem], bf16, fp32 accumulate.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -124,6 +130,23 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// Eight E2M1 codes times `f` (a bf16 pair) times 2^-112 as four bf16 pairs, exact.
+// The f16 value's exponent and mantissa move to bits 4-10 and 6, where bf16's
+// bias reads them as 2^-112 of it; its sign lands on bit 12 and moves on to 15
+// (0x1000 + 7 * 0x1000).
+__device__ __forceinline__ void e2m1_to_bf16(uint32_t w, uint32_t f, uint32_t* y) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t t = h[k] >> 3;
+    y[k] = bf16x2_mul(t + (t & 0x10001000u) * 7u, f);
+  }
+}
+
 // S[half] = Q[half] K^T: both K-major, 128-byte swizzled rows of 64 channels.
 template <int D>
 __device__ __forceinline__ void issue_s(uint32_t d, const uint8_t* q, const uint8_t* k) {
@@ -145,15 +168,16 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, const uint8_
     mma_ts(d, pcol + 8 * kk, smem_desc(va + kk * 16 * 128, 128 * 128, 1024, kSwz128), bf16_idesc(128, D, 0, 1), acc || kk > 0);
 }
 
-template <int D, bool FP8>
+template <int D, int CACHE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const PagedParams p, const __grid_constant__ CUtensorMap map_q,
                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-  using C = Cfg<D, FP8>;
+  using C = Cfg<D, CACHE>;
+  constexpr bool FP8 = C::kCodes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_base_1k(smem_raw);
-  Tiles<D, FP8>& tl = *reinterpret_cast<Tiles<D, FP8>*>(base);
-  Ctl& c = *reinterpret_cast<Ctl*>(base + sizeof(Tiles<D, FP8>));
+  Tiles<D, CACHE>& tl = *reinterpret_cast<Tiles<D, CACHE>*>(base);
+  Ctl& c = *reinterpret_cast<Ctl*>(base + sizeof(Tiles<D, CACHE>));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   WsHeader* hdr = &p.hdr->base;
   volatile int* abort_flag = &c.abort_flag;
@@ -316,11 +340,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (FP8) {
               const int s = it % C::kRaw;
               if (!(ok = mbar_wait_warp(&c.raw_empty[s], ((it / C::kRaw) & 1) ^ 1, abort_flag, hdr, 0x803))) break;
-              if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[s], np * ps * (D + 1));
+              if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[s], np * ps * (C::kCodeB + C::kBlkB + 1));
               __syncwarp();
               if (lane < np) {
-                bulk_load(tl.raw[s] + lane * ps * D, (kv ? p.v : p.k) + id * p.page_bytes + (int64_t)f.h * ps * D, ps * D,
-                          &c.raw_full[s]);
+                bulk_load(tl.raw[s] + lane * ps * C::kCodeB, (kv ? p.v : p.k) + id * p.page_bytes + (int64_t)f.h * ps * C::kCodeB,
+                          ps * C::kCodeB, &c.raw_full[s]);
+                if constexpr (C::kFp4)
+                  bulk_load(tl.raw[s] + 128 * C::kCodeB + lane * ps * C::kBlkB,
+                            (kv ? p.v_blocks : p.k_blocks) + ((int64_t)id * p.Hkv + f.h) * ps * C::kBlkB, ps * C::kBlkB, &c.raw_full[s]);
                 bulk_load(c.scales[s] + lane * ps, (kv ? p.v_scales : p.k_scales) + ((int64_t)id * p.Hkv + f.h) * ps, ps,
                           &c.raw_full[s]);
               }
@@ -465,15 +492,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int kRawCh = D / 16, kStep = 128 / kRawCh, kBatch = kRawCh;
           const int ch = lt % kRawCh, row0 = lt / kRawCh;
           const int flip = (ch >> 2) & 1;
-          const uint8_t* src = tl.raw[rs] + row0 * D + ch * 16;
+          const uint8_t* src = tl.raw[rs] + row0 * C::kCodeB + ch * (C::kCodeB / (D / 16));
+          using Raw = std::conditional_t<C::kFp4, uint2, uint4>;  // 16 channels' codes
           uint8_t* dst = tl.kv[s] + (ch / 4) * 128 * 128 + row0 * 128;
           const uint32_t at0 = (((2 * ch) & 7) ^ (row0 & 7)) << 4, at1 = at0 ^ 16;
-          auto convert = [](const uint4& x, uint32_t f, uint32_t (&y)[8]) {
-            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+          // sc <= 134: times 2^(sc - 127)
+          auto convert = [&](const Raw& x, int i, uint32_t sc, uint32_t (&y)[8]) {
+            if constexpr (C::kFp4) {
+              // 2^112 undoes the conversion's bias
+              const uint32_t b = tl.raw[rs][128 * C::kCodeB + (row0 + i * kStep) * C::kBlkB + ch];
+              const float s = unpack_e4m3x2((uint16_t)b).x * __uint_as_float((sc + 112u) << 23);
+              const uint32_t f = prmt(__float_as_uint(s), 0u, 0x3232u);
+              e2m1_to_bf16(x.x, f, &y[0]);
+              e2m1_to_bf16(x.y, f, &y[4]);
+            } else {
+              // 2^120 undoes the conversion's bias: (byte + 120) << 7 in both halves
+              const uint32_t f = sc * 0x00800080u + 120u * 0x00800080u;
+              const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              y[2 * k] = bf16x2_mul(e4m3_to_bf16x2(prmt(wd[k], 0u, 0x4140u)), f);
-              y[2 * k + 1] = bf16x2_mul(e4m3_to_bf16x2(prmt(wd[k], 0u, 0x4342u)), f);
+              for (int k = 0; k < 4; ++k) {
+                y[2 * k] = bf16x2_mul(e4m3_to_bf16x2(prmt(wd[k], 0u, 0x4140u)), f);
+                y[2 * k + 1] = bf16x2_mul(e4m3_to_bf16x2(prmt(wd[k], 0u, 0x4342u)), f);
+              }
             }
           };
           auto put = [&](int i, const uint32_t (&y)[8]) {
@@ -492,14 +532,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
             for (int i0 = 0; i0 < kRawCh; i0 += kBatch) {
-              uint4 x[kBatch];
+              Raw x[kBatch];
 #pragma unroll
-              for (int i = 0; i < kBatch; ++i) x[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * kStep * D);
+              for (int i = 0; i < kBatch; ++i) x[i] = *reinterpret_cast<const Raw*>(src + (i0 + i) * kStep * C::kCodeB);
 #pragma unroll
               for (int i = 0; i < kBatch; ++i) {
                 uint32_t y[8];
-                // 2^120 undoes the conversion's bias: (byte + 120) << 7 in both halves
-                convert(x[i], sb[i0 + i] * 0x00800080u + 120u * 0x00800080u, y);
+                convert(x[i], i0 + i, sb[i0 + i], y);
                 put(i0 + i, y);
               }
             }
@@ -513,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 8; ++k) y[k] = 0u;
               if (row < keys) {
                 if (sc != 255u) {  // a scale above 2^7: in two factors
-                  convert(*reinterpret_cast<const uint4*>(src + i * kStep * D), min(sc, 134u) * 0x00800080u + 120u * 0x00800080u, y);
+                  convert(*reinterpret_cast<const Raw*>(src + i * kStep * C::kCodeB), i, min(sc, 134u), y);
                   const uint32_t f2 = ((max(sc, 134u) - 134u + 127u) << 7) * 0x10001u;
 #pragma unroll
                   for (int k = 0; k < 8; ++k) y[k] = bf16x2_mul(y[k], f2);
@@ -841,18 +880,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_for_decode();
 }
 
-template <int D, bool FP8>
+template <int D, int CACHE>
 cudaError_t launch(const PagedParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
-  constexpr size_t smem = smem_bytes<D, FP8>();
+  constexpr size_t smem = smem_bytes<D, CACHE>();
   static_assert(smem <= 232448, "shared memory");
-  using T = Tiles<D, FP8>;
-  static_assert(offsetof(T, kv) % 1024 == 0 && offsetof(T, raw) % 1024 == 0 && offsetof(T, out) % 1024 == 0, "tile alignment");
+  using T = Tiles<D, CACHE>;
+  static_assert(offsetof(T, kv) % 1024 == 0 && offsetof(T, raw) % 1024 == 0 && offsetof(T, out) % 128 == 0, "tile alignment");
   static bool attr_set[64] = {};  // per device: raised once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(paged_chunk_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(paged_chunk_kernel<D, CACHE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
@@ -866,15 +905,16 @@ cudaError_t launch(const PagedParams& p, const CUtensorMap& mq, const CUtensorMa
   cfg.stream = st;
   cfg.attrs = &early;
   cfg.numAttrs = p.small_rows ? 1 : 0;  // a decode kernel came before
-  return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<D, FP8>, p, mq, mk, mv);
+  return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<D, CACHE>, p, mq, mk, mv);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_chunk(const PagedParams& p, int d, bool e4m3, const CUtensorMap& mq, const CUtensorMap& mk,
+cudaError_t launch_paged_chunk(const PagedParams& p, int d, int cache, const CUtensorMap& mq, const CUtensorMap& mk,
                                const CUtensorMap& mv, cudaStream_t st) {
-  if (d == 128) return e4m3 ? launch<128, true>(p, mq, mk, mv, st) : launch<128, false>(p, mq, mk, mv, st);
-  return e4m3 ? launch<64, true>(p, mq, mk, mv, st) : launch<64, false>(p, mq, mk, mv, st);
+  if (cache == kCacheE2M1) return d == 128 ? launch<128, kCacheE2M1>(p, mq, mk, mv, st) : launch<64, kCacheE2M1>(p, mq, mk, mv, st);
+  if (cache == kCacheE4M3) return d == 128 ? launch<128, kCacheE4M3>(p, mq, mk, mv, st) : launch<64, kCacheE4M3>(p, mq, mk, mv, st);
+  return d == 128 ? launch<128, kCacheBF16>(p, mq, mk, mv, st) : launch<64, kCacheBF16>(p, mq, mk, mv, st);
 }
 
 }  // namespace flamia

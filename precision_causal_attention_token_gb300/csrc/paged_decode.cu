@@ -54,9 +54,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnit = 4096;  // bytes of a chunk's K (or V)
 constexpr int kSpread = 12;  // binades between V rows that f16 weights serve
-constexpr int kRingB = kWarps * 4 * kUnit;  // two chunks a warp
 // 2 CTAs of an SM (3: 59 against 57 us on 65,522 tokens; more partials to join)
 constexpr int kCtas = 2;
 
@@ -102,21 +100,51 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
 }
+// Eight E2M1 codes -> four f16 pairs, exact: pair b from byte b, its low nibble in the low half.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+// Two E4M3 codes in bits 0-15 -> f16 pair, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float f16_lo(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v & 0xFFFFu))); }
+__device__ __forceinline__ float f16_hi(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v >> 16))); }
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
-template <int D, bool FP8, int NT>
+template <int D, int CACHE, int NT>
 struct Decode {
-  static constexpr int kRowB = D * (FP8 ? 1 : 2);   // bytes of a cached row
-  static constexpr int kChunk = 4096 / kRowB;       // keys a warp takes at a time
+  static constexpr bool kFp4 = CACHE == kCacheE2M1;
+  static constexpr int kRowB = kFp4 ? D / 2 : D * (CACHE == kCacheE4M3 ? 1 : 2);  // bytes of a cached row
+  // keys a warp takes at a time: 4 KB, up to 64 keys (32 rows of a head of 128 in E2M1: as many registers as in E4M3)
+  static constexpr int kChunk = kFp4 ? (NT == 4 && D == 128 ? 32 : 64) : 4096 / kRowB;
+  static constexpr int kUnit = kChunk * kRowB;      // bytes of a chunk's K (or V)
+  static constexpr int kRingB = kWarps * 4 * kUnit; // two chunks a warp
   static constexpr int kSub = kChunk / 16;          // m16 key tiles of a chunk
-  static constexpr int kKJ = kRowB / 64;            // 16-byte loads of a K row, 4 lanes side by side
+  static constexpr int kKJ = kRowB >= 64 ? kRowB / 64 : 1;  // loads of a K row (16 bytes; 8 of a row of 32), 4 lanes side by side
   static constexpr int kVW = kRowB / 32;            // 32-bit words of a V row per lane, 8 lanes side by side
   static constexpr int kMT = D / 16;                // m16 channel tiles
   static constexpr int kQ = 8 * NT;                 // query rows
+  static constexpr int kBlk = D / 16;               // E2M1: block scales of a row
   // 32 rows: the queries' fragments stay in shared memory, the registers hold
   // the 128 accumulators
   static constexpr bool kQShared = NT == 4;
@@ -124,16 +152,20 @@ struct Decode {
   // of a shared-memory phase read eight different 16-byte columns of the
   // banks' 128 bytes.  K: rows g, g + 1, four pieces side by side; V: rows 2t
   // (or 2t + 1) for t = 0..3, pieces g, g + 1.  Rows of 64 bytes: two to a
-  // 128-byte line, so the line counts in place of the row.
+  // 128-byte line, so the line counts in place of the row.  Rows of 32 bytes:
+  // no pieces trade places, but the rows of every other line do (V: rows 0, 2,
+  // 4, 6 then fill a line's four places).
   __host__ __device__ static constexpr int swap(bool v, int r) {
+    if (kRowB == 32) return 0;
     if (kRowB == 64) return v ? ((r >> 1) & 3) : 0;
     return v ? (r & 6) : (r & 1) << 2;
   }
+  __host__ __device__ static constexpr int row_at(int r) { return (kRowB == 32 ? r ^ ((r >> 2) & 1) : r) * kRowB; }
 };
 
 // Dynamic shared memory: the warps' rings and, after a tile's last key, the
-// join's buffers in the same place; then the E4M3 scale bytes and, for 32
-// rows, the queries.
+// join's buffers in the same place; then the rows' scale bytes (E4M3, E2M1), the
+// E2M1 block scales and, for 32 rows, the queries.
 template <int D, int NT>
 struct Join {
   float o[kWarps][8 * NT][D + 4];
@@ -142,24 +174,35 @@ struct Join {
 struct Scales {
   uint8_t b[kWarps][2][2][64];  // [warp][chunk mod 2][K, V][key]
 };
+template <int D, int CACHE>
+struct __align__(16) Blocks {
+  uint8_t b[kWarps][2][2][CACHE == kCacheE2M1 ? 64 * (D / 16) : 16];  // [warp][chunk mod 2][K, V][key][block]
+};
 template <int D>
 struct Queries {
   uint2 q[4][D / 16][32];  // [8 rows][K step][lane]
   float scale[32];
 };
-template <int D, int NT>
+// The rings, the join's buffers or the join's weights: the largest.
+template <int D, int CACHE, int NT>
 constexpr size_t ring_bytes() {
-  return sizeof(Join<D, NT>) > kRingB ? (sizeof(Join<D, NT>) + 15) / 16 * 16 : kRingB;
+  size_t n = Decode<D, CACHE, NT>::kRingB;
+  if (sizeof(Join<D, NT>) > n) n = (sizeof(Join<D, NT>) + 15) / 16 * 16;
+  if (sizeof(float) * kMaxWorkers * 8 * NT > n) n = sizeof(float) * kMaxWorkers * 8 * NT;
+  return n;
 }
 
-template <int D, bool FP8, int NT>
+template <int D, int CACHE, int NT>
 __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const PagedParams p) {
-  using C = Decode<D, FP8, NT>;
+  using C = Decode<D, CACHE, NT>;
+  constexpr bool FP8 = CACHE != kCacheBF16, FP4 = C::kFp4;  // FP8: codes under a row exponent, as f16; FP4: of four bits
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int sm_last;
   Join<D, NT>& sm = *reinterpret_cast<Join<D, NT>*>(smem);
-  Scales& scl = *reinterpret_cast<Scales*>(smem + ring_bytes<D, NT>());
-  [[maybe_unused]] Queries<D>& qsm = *reinterpret_cast<Queries<D>*>(smem + ring_bytes<D, NT>() + sizeof(Scales));
+  constexpr size_t kScalesAt = ring_bytes<D, CACHE, NT>(), kBlocksAt = kScalesAt + sizeof(Scales);
+  Scales& scl = *reinterpret_cast<Scales*>(smem + kScalesAt);
+  [[maybe_unused]] Blocks<D, CACHE>& blks = *reinterpret_cast<Blocks<D, CACHE>*>(smem + kBlocksAt);
+  [[maybe_unused]] Queries<D>& qsm = *reinterpret_cast<Queries<D>*>(smem + kBlocksAt + (FP4 ? sizeof(Blocks<D, CACHE>) : 0));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   PagedHeader* hdr = p.hdr;
   // the chunk kernel, where one follows, works on other rows: its CTAs come in
@@ -189,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         // K step ks of lane t: channels d .. d + 3, as the K loads deal them
-        const int d = FP8 ? (ks >> 2) * 64 + t * 16 + (ks & 3) * 4 : (ks >> 1) * 32 + t * 8 + (ks & 1) * 4;
+        const int d = FP4 ? t * (D / 4) + ks * 4 : FP8 ? (ks >> 2) * 64 + t * 16 + (ks & 3) * 4 : (ks >> 1) * 32 + t * 8 + (ks & 1) * 4;
         uint2 x = make_uint2(0, 0);
         if (row < rows) x = __ldg(reinterpret_cast<const uint2*>(src + d));
         f[ks][0] = x.x;
@@ -260,8 +303,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
       }
       return id;
     };
+    constexpr int kUnit = C::kUnit;
     const uint32_t ring = smem_u32(smem) + warp * 4 * kUnit;  // K, V of even chunks, K, V of odd ones
     const uint32_t scales = smem_u32(scl.b[warp]);
+    [[maybe_unused]] const uint32_t blocks4 = smem_u32(blks.b[warp]);
+    constexpr int kBlkB = 64 * (D / 16);  // E2M1: bytes of a chunk's block scales
     // Request a chunk's K (or V) and its scale bytes: one group of copies
     // each.  A copy instruction takes 512 contiguous bytes: with K in the
     // fragments' own order (64-byte pieces of eight rows) the decode of 65,522
@@ -283,7 +329,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
 #pragma unroll
         for (int i = 0; i < 16 / kRowsAt; ++i) {
           const int rr = i * kRowsAt + row;
-          copy16(dst + (16 * s + rr) * C::kRowB + ((piece ^ C::swap(kV, rr)) << 4), src + i * 512, key + rr < kend ? 16 : 0);
+          copy16(dst + C::row_at(16 * s + rr) + ((piece ^ C::swap(kV, rr)) << 4), src + i * 512, key + rr < kend ? 16 : 0);
+        }
+        if constexpr (FP4) {  // the block scales, zero like the scale bytes below: 0 x NaN is NaN
+          const int piece4 = lane % C::kBlk;
+          if (lane / C::kBlk == s)
+            copy16(blocks4 + ((it & 1) * 2 + kV) * kBlkB + s * 16 * C::kBlk + piece4 * 16,
+                   (kV ? p.v_blocks : p.k_blocks) + ((int64_t)id * p.Hkv * p.page_size + in_page) * C::kBlk + piece4 * 16,
+                   min(max(min(kend - key, 16) * C::kBlk - piece4 * 16, 0), 16));
         }
         if constexpr (FP8) {
           // 16 bytes of one page; zero for keys from kend on, whose slots hold
@@ -349,16 +402,40 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.f;
       // the queries' fragments of a K step serve all key tiles
-      constexpr int kU = FP8 ? 4 : 2;  // K steps of a 64-byte piece
+      constexpr int kU = FP4 ? D / 16 : FP8 ? 4 : 2;  // K steps of a load
 #pragma unroll
       for (int j = 0; j < C::kKJ; ++j) {
         uint32_t x[C::kSub][4], y[C::kSub][4];
 #pragma unroll
         for (int i = 0; i < C::kSub; ++i) {
-          const uint32_t a = kb + (16 * i + g) * C::kRowB + (((4 * j + t) ^ C::swap(false, g)) << 4);  // g and g + 8 alike
-          const uint4 u0 = lds16(a), u1 = lds16(a + 8 * C::kRowB);
-          x[i][0] = u0.x, x[i][1] = u0.y, x[i][2] = u0.z, x[i][3] = u0.w;
-          y[i][0] = u1.x, y[i][1] = u1.y, y[i][2] = u1.z, y[i][3] = u1.w;
+          if constexpr (C::kRowB == 32) {
+            const uint32_t a = kb + C::row_at(16 * i + g) + t * 8;  // g and g + 8 alike
+            const uint2 u0 = lds8(a), u1 = lds8(a + 8 * C::kRowB);
+            x[i][0] = u0.x, x[i][1] = u0.y;
+            y[i][0] = u1.x, y[i][1] = u1.y;
+          } else {
+            const uint32_t a = kb + (16 * i + g) * C::kRowB + (((4 * j + t) ^ C::swap(false, g)) << 4);  // g and g + 8 alike
+            const uint4 u0 = lds16(a), u1 = lds16(a + 8 * C::kRowB);
+            x[i][0] = u0.x, x[i][1] = u0.y, x[i][2] = u0.z, x[i][3] = u0.w;
+            y[i][0] = u1.x, y[i][1] = u1.y, y[i][2] = u1.z, y[i][3] = u1.w;
+          }
+        }
+        // E2M1: the block scales of this lane's channels, as f16 pairs of one value
+        [[maybe_unused]] uint32_t sx[C::kSub][2], sy[C::kSub][2];
+        if constexpr (FP4) {
+          const uint8_t* bk = blks.b[warp][it & 1][0];
+#pragma unroll
+          for (int i = 0; i < C::kSub; ++i) {
+            if constexpr (D == 128) {
+              const uint32_t s0 = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(bk + (16 * i + g) * C::kBlk + 2 * t));
+              const uint32_t s1 = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(bk + (16 * i + 8 + g) * C::kBlk + 2 * t));
+              sx[i][0] = prmt(s0, 0u, 0x1010u), sx[i][1] = prmt(s0, 0u, 0x3232u);
+              sy[i][0] = prmt(s1, 0u, 0x1010u), sy[i][1] = prmt(s1, 0u, 0x3232u);
+            } else {
+              sx[i][0] = sx[i][1] = e4m3x2_to_f16(bk[(16 * i + g) * C::kBlk + t] * 0x0101u);
+              sy[i][0] = sy[i][1] = e4m3x2_to_f16(bk[(16 * i + 8 + g) * C::kBlk + t] * 0x0101u);
+            }
+          }
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
@@ -376,7 +453,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
           }
 #pragma unroll
           for (int i = 0; i < C::kSub; ++i) {
-            if constexpr (FP8) {
+            if constexpr (FP4) {  // K step u: bytes 2 (u mod 2), + 1 of word u / 2
+              uint32_t hx[4], hy[4];
+              e2m1x8_to_f16(x[i][u / 2], hx);
+              e2m1x8_to_f16(y[i][u / 2], hy);
+              const uint32_t fx = sx[i][u / 4], fy = sy[i][u / 4];
+              const uint32_t a0 = f16x2_mul(hx[2 * (u & 1)], fx), a2 = f16x2_mul(hx[2 * (u & 1) + 1], fx);
+              const uint32_t a1 = f16x2_mul(hy[2 * (u & 1)], fy), a3 = f16x2_mul(hy[2 * (u & 1) + 1], fy);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(s[i][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+            } else if constexpr (FP8) {
               uint32_t a0, a1, a2, a3;
               e4m3x4_to_f16(x[i][u], a0, a2);
               e4m3x4_to_f16(y[i][u], a1, a3);
@@ -531,11 +617,48 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         // its codes may be NaN too: the NaN comes with the weight, and rows that
         // do not see it have the weight 0 (0 x NaN)
         for (int key = 0; key < C::kChunk; ++key)
-          if (scl.b[warp][it & 1][1][key] == 255 && lane < C::kRowB / 4)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + key * C::kRowB + lane * 4), "r"(0) : "memory");
+          if (scl.b[warp][it & 1][1][key] == 255) {
+            if (lane < C::kRowB / 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + C::row_at(key) + lane * 4), "r"(0) : "memory");
+            if (FP4 && lane < C::kBlk) blks.b[warp][it & 1][1][key * C::kBlk + lane] = 0;
+          }
         __syncwarp();
       }
-      // E4M3, careful: V as bf16 values, two bf16 terms a weight; eight rows of
+      // E2M1: this lane's channels of one key tile's V as f16 pairs of two keys:
+      // word x, tile q of it: channels 8x + 2q (a[0]: keys 2t, 2t + 1; a[2]: 2t + 8,
+      // 2t + 9) and 8x + 2q + 1 (a[1], a[3]), block scales in.  The nibbles of two
+      // keys are put side by side before they are converted.
+      [[maybe_unused]] auto v_tiles = [&](int i, auto use) {
+        uint32_t w[4][2], f[2];
+        const uint8_t* bv = blks.b[warp][it & 1][1] + 16 * i * C::kBlk + (D == 128 ? g : g >> 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rk = 2 * t + (k & 1) + 8 * (k >> 1);
+          if constexpr (C::kVW == 2) {
+            const uint2 x = lds8(vb + C::row_at(16 * i + rk) + ((((g >> 1) ^ C::swap(true, rk)) << 4) | (g & 1) << 3));
+            w[k][0] = x.x;
+            w[k][1] = x.y;
+          } else {
+            w[k][0] = lds4(vb + C::row_at(16 * i + rk) + 4 * g);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          f[k] = e4m3x2_to_f16((uint32_t)bv[(2 * t + 8 * k) * C::kBlk] | (uint32_t)bv[(2 * t + 8 * k + 1) * C::kBlk] << 8);
+#pragma unroll
+        for (int x = 0; x < C::kVW; ++x) {
+          uint32_t h[4][4];  // even channels of keys 2t, 2t + 1; odd ones; the same of 2t + 8, 2t + 9
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w0 = w[2 * k][x], w1 = w[2 * k + 1][x];
+            e2m1x8_to_f16((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), h[2 * k]);
+            e2m1x8_to_f16(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), h[2 * k + 1]);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            use(4 * x + q, f16x2_mul(h[0][q], f[0]), f16x2_mul(h[1][q], f[0]), f16x2_mul(h[2][q], f[1]), f16x2_mul(h[3][q], f[1]));
+        }
+      };
+      // E4M3 and E2M1, careful: V as bf16 values, two bf16 terms a weight; eight rows of
       // one key tile at a time, so that it needs no registers beside the usual
       // pass's (all rows at once spilled 500 bytes of the 32-row kernel)
       auto add_careful = [&] {
@@ -544,9 +667,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
         for (int i = 0; i < C::kSub; ++i) {
           // 2^120 times the scales of keys 2t, 2t + 1 (then 2t + 8, 2t + 9) in two
           // factors, as bf16 pairs
-          uint32_t f[2][2];
+          [[maybe_unused]] uint32_t f[2][2];
+          [[maybe_unused]] float fv[4];  // E2M1: the scales
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
+            if constexpr (FP4) {
+              fv[2 * k] = ue8m0(min((int)sv[16 * i + 8 * k + 2 * t], 254));
+              fv[2 * k + 1] = ue8m0(min((int)sv[16 * i + 8 * k + 2 * t + 1], 254));
+              continue;
+            }
             const uint32_t b0 = min((int)sv[16 * i + 8 * k + 2 * t], 254), b1 = min((int)sv[16 * i + 8 * k + 2 * t + 1], 254);
             f[k][0] = ((min(b0, 134u) + 120u) << 7) | ((min(b1, 134u) + 120u) << 23);
             f[k][1] = ((max(b0, 134u) - 7u) << 7) | ((max(b1, 134u) - 7u) << 23);
@@ -568,26 +697,38 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
               ph[k] = transpose8(a);
               pl[k] = transpose8(pack_bf16x2(y[0] - bf16_lo(a), y[1] - bf16_hi(a)));
             }
+            if constexpr (FP4) {
+              v_tiles(i, [&](int mt, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+                const uint32_t h[4] = {v0, v1, v2, v3};
+                uint32_t a[4];  // six significant bits: exact
 #pragma unroll
-            for (int x = 0; x < C::kVW; ++x) {
-              uint32_t w[4];  // channels 4x .. 4x + 3 of four keys
+                for (int k = 0; k < 4; ++k)
+                  a[k] = pack_bf16x2(f16_lo(h[k]) * fv[2 * (k >> 1)], f16_hi(h[k]) * fv[2 * (k >> 1) + 1]);
+                mma_bf16(o[mt][nt], a[0], a[1], a[2], a[3], ph[0], ph[1]);
+                mma_bf16(o[mt][nt], a[0], a[1], a[2], a[3], pl[0], pl[1]);
+              });
+            } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int rk = 2 * t + (k & 1) + 8 * (k >> 1);
-                const uint32_t piece = C::kVW == 2 ? g >> 1 : g, in = C::kVW == 2 ? (g & 1) * 8 + 4 * x : 4 * x;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[k])
-                             : "r"(vb + (16 * i + rk) * C::kRowB + ((piece ^ C::swap(true, rk)) << 4) + in) : "memory");
-              }
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint32_t a[4];  // channels 4x + 2 half, + 1: keys 2t, 2t + 1; the same of 2t + 8, 2t + 9
+              for (int x = 0; x < C::kVW; ++x) {
+                uint32_t w[4];  // channels 4x .. 4x + 3 of four keys
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const uint32_t two = prmt(w[k & 2], w[(k & 2) + 1], 0x5410u + 0x2222u * half) >> (8 * (k & 1)) & 0x00FF00FFu;
-                  a[k] = bf16x2_mul(bf16x2_mul(e4m3_to_bf16x2(two), f[k >> 1][0]), f[k >> 1][1]);
+                  const int rk = 2 * t + (k & 1) + 8 * (k >> 1);
+                  const uint32_t piece = C::kVW == 2 ? g >> 1 : g, in = C::kVW == 2 ? (g & 1) * 8 + 4 * x : 4 * x;
+                  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[k])
+                               : "r"(vb + (16 * i + rk) * C::kRowB + ((piece ^ C::swap(true, rk)) << 4) + in) : "memory");
                 }
-                mma_bf16(o[2 * x + half][nt], a[0], a[1], a[2], a[3], ph[0], ph[1]);
-                mma_bf16(o[2 * x + half][nt], a[0], a[1], a[2], a[3], pl[0], pl[1]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  uint32_t a[4];  // channels 4x + 2 half, + 1: keys 2t, 2t + 1; the same of 2t + 8, 2t + 9
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t two = prmt(w[k & 2], w[(k & 2) + 1], 0x5410u + 0x2222u * half) >> (8 * (k & 1)) & 0x00FF00FFu;
+                    a[k] = bf16x2_mul(bf16x2_mul(e4m3_to_bf16x2(two), f[k >> 1][0]), f[k >> 1][1]);
+                  }
+                  mma_bf16(o[2 * x + half][nt], a[0], a[1], a[2], a[3], ph[0], ph[1]);
+                  mma_bf16(o[2 * x + half][nt], a[0], a[1], a[2], a[3], pl[0], pl[1]);
+                }
               }
             }
           }
@@ -683,7 +824,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
           }
         }
       };
-      if constexpr (!careful) {
+      if constexpr (FP4 && !careful) {
+#pragma unroll
+        for (int i = 0; i < C::kSub; ++i)
+          v_tiles(i, [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[mt][nt], a0, a1, a2, a3, hi[i][nt][0], hi[i][nt][1]);
+          });
+      } else if constexpr (!careful) {
         add_pv(-1);
       } else if constexpr (!FP8) {
 #pragma unroll 1
@@ -859,34 +1007,35 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
   }
 }
 
-template <int D, bool FP8, int NT>
+template <int D, int CACHE, int NT>
 cudaError_t launch(const PagedParams& p, cudaStream_t st) {
-  constexpr size_t smem = ring_bytes<D, NT>() + sizeof(Scales) + (NT == 4 ? sizeof(Queries<D>) : 0);
-  static_assert(sizeof(float) * kMaxWorkers * 8 * NT <= ring_bytes<D, NT>(), "the weights lie in the rings' place");
+  constexpr size_t smem = ring_bytes<D, CACHE, NT>() + sizeof(Scales) + (CACHE == kCacheE2M1 ? sizeof(Blocks<D, CACHE>) : 0) +
+                          (NT == 4 ? sizeof(Queries<D>) : 0);
   static bool attr_set[64] = {};  // per device: raised once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(paged_decode_kernel<D, FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(paged_decode_kernel<D, CACHE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  paged_decode_kernel<D, FP8, NT><<<p.W_max[0], kThreads, smem, st>>>(p);
+  paged_decode_kernel<D, CACHE, NT><<<p.W_max[0], kThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
-template <int D, bool FP8>
+template <int D, int CACHE>
 cudaError_t launch_n(const PagedParams& p, cudaStream_t st) {
-  return p.small_rows == 8 ? launch<D, FP8, 1>(p, st) : p.small_rows == 16 ? launch<D, FP8, 2>(p, st) : launch<D, FP8, 4>(p, st);
+  return p.small_rows == 8 ? launch<D, CACHE, 1>(p, st) : p.small_rows == 16 ? launch<D, CACHE, 2>(p, st) : launch<D, CACHE, 4>(p, st);
 }
 
 }  // namespace
 
 int paged_decode_workers(int sms) { return sms * kCtas; }
 
-cudaError_t launch_paged_decode(const PagedParams& p, int d, bool e4m3, cudaStream_t st) {
-  if (d == 128) return e4m3 ? launch_n<128, true>(p, st) : launch_n<128, false>(p, st);
-  return e4m3 ? launch_n<64, true>(p, st) : launch_n<64, false>(p, st);
+cudaError_t launch_paged_decode(const PagedParams& p, int d, int cache, cudaStream_t st) {
+  if (cache == kCacheE2M1) return d == 128 ? launch_n<128, kCacheE2M1>(p, st) : launch_n<64, kCacheE2M1>(p, st);
+  if (cache == kCacheE4M3) return d == 128 ? launch_n<128, kCacheE4M3>(p, st) : launch_n<64, kCacheE4M3>(p, st);
+  return d == 128 ? launch_n<128, kCacheBF16>(p, st) : launch_n<64, kCacheBF16>(p, st);
 }
 
 }  // namespace flamia
