@@ -451,7 +451,7 @@ size_t flamia_paged_workspace_size(const flamia_paged_t* p);
  * entries are written; what is left of S stays in free_pages and its length
  * goes to *n_free_out.  So a finished request passes kv_len 0, one whose
  * drafted tokens were rejected a smaller kv_len.  Pages must belong to one
- * request only.  Table entries outside the taken pages are not written.
+ * request only (flamia_paged_plan_shared: to several).  Table entries outside the taken pages are not written.
  *   old_len     int32 [n_req]
  *   free_pages  int32 [n_pages] stack of free page ids
  *   n_free, n_free_out  int32 [1]; may be the same word
@@ -476,6 +476,91 @@ size_t flamia_paged_workspace_size(const flamia_paged_t* p);
 flamia_status_t flamia_paged_plan(const flamia_paged_t* p, int32_t* slot_map, const int32_t* old_len,
                                   int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out, void* ws,
                                   size_t ws_bytes, cudaStream_t stream);
+
+/* ---- Pages that requests share -------------------------------------------
+ * One prompt's pages can serve many requests (answers sampled in parallel, the
+ * beams of a beam search, cached prompts): their table entries name the same
+ * page, and refs[page] counts them.  A step is then
+ *   flamia_paged_plan_shared   in place of flamia_paged_plan
+ *   flamia_paged_copy          its list of copies, in every layer
+ *   per layer: append and attention as before.
+ * These calls take a second workspace, `pages_ws` of
+ * flamia_paged_pages_workspace_size bytes, which need not be initialised and
+ * keeps nothing from call to call but its status word (flamia_paged_copy only
+ * adds to that one).  One call at a time. */
+size_t flamia_paged_pages_workspace_size(const flamia_paged_t* p);
+
+/* The page management of a step whose requests may share pages, then what
+ * flamia_paged_plan does with old_len NULL (slot map, work split).
+ *   src       int32 [n_req] (may be NULL: src[r] = r): the request, as it was
+ *             before the step, that request r continues; -1: none, it starts
+ *             empty.  Several may continue one (a fork); a request that none
+ *             continues ends.
+ *   old_len   int32 [n_req]: tokens that the rows of block_table hold before
+ *   refs      int32 [n_pages]: table entries that hold each page, plus holders
+ *             that the caller counts beside the tables (such a page is neither
+ *             freed nor written); 0 for free pages
+ *   free_pages, n_free, n_free_out   as in flamia_paged_plan
+ *   copies    int32 [n_req][2], n_copies int32 [1]: pages to copy in every
+ *             layer before anything is appended, (source, destination).  No
+ *             destination is a source.
+ * With p the page size, q_r = cu_q[r+1] - cu_q[r] and w_r = max(0, kv_len[r] -
+ * q_r) the tokens that request r keeps, its row gets the first
+ *   keep_r = min(ceil(old_len[src[r]] / p), ceil(w_r / p))
+ * entries of row src[r] as it was (0 for src[r] = -1).  Let total be each
+ * page's count once every row holds these and no others.
+ *   - A page of the old rows whose total is 0 goes onto the free stack, in the
+ *     order of the old entries (row, then table order) that held it first.
+ *   - Request r writes into entry w_r / p if q_r > 0, w_r < kv_len[r], w_r is
+ *     no multiple of p and w_r / p < keep_r.  If that page has other holders
+ *     than writers, each of its writers gets a new page in its place and a
+ *     line in `copies` (in request order); if all its holders write, the first
+ *     of them keeps it.
+ *   - New pages come off the end of the stack in request order, table order:
+ *     copies, and entries keep_r .. ceil(kv_len[r] / p) - 1.
+ * Table entries from ceil(kv_len[r] / p) on are left as they were.  A page
+ * must not occur twice in a row.
+ * Device-side conditions, all checked before anything is written (in both
+ * workspaces' status words): FLAMIA_ERR_BAD_SEQLENS (as in flamia_paged_plan;
+ * src outside [-1, n_req)), FLAMIA_ERR_BAD_PAGE (*n_free out of range, a table
+ * entry that the step reads outside [0, n_pages), counts below the entries
+ * that it sees, more pages freed than the stack has room for),
+ * FLAMIA_ERR_NO_PAGES.  Then nothing moves, *n_free_out = *n_free, *n_copies =
+ * 0, every slot is -1, and launches that use `ws` write nothing.
+ * FLAMIA_ERR_UNSUPPORTED (from the host) where the sizes allow a step that
+ * flamia_paged_plan would refuse with it. */
+flamia_status_t flamia_paged_plan_shared(const flamia_paged_t* p, int32_t* slot_map, const int32_t* src,
+                                         const int32_t* old_len, int32_t* refs, int32_t* free_pages, const int32_t* n_free,
+                                         int32_t* n_free_out, int32_t* copies, int32_t* n_copies, void* pages_ws,
+                                         size_t pages_ws_bytes, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Copies pages in n_layers layers: for each of the first *n_copies (source,
+ * destination) pairs of `copies` (int32 [max_copies][2]), page `source` of
+ * src[l] to page `destination` of dst[l], whole, with its scales.  src and dst
+ * are host arrays of n_layers caches and may be the same; of `p` Hkv, d,
+ * page_size, n_pages and cache_dtype count.  No destination may be a source of
+ * the same pool, nor occur twice.  *n_copies outside [0, max_copies] copies
+ * nothing and sets FLAMIA_ERR_INVALID_ARG, a page outside [0, n_pages) skips
+ * its pair and sets FLAMIA_ERR_BAD_PAGE (in pages_ws). */
+flamia_status_t flamia_paged_copy(const flamia_paged_t* p, int32_t n_layers, const flamia_cache_t* src,
+                                  const flamia_cache_t* dst, const int32_t* copies, int32_t max_copies,
+                                  const int32_t* n_copies, void* pages_ws, size_t pages_ws_bytes, cudaStream_t stream);
+
+/* Compacts the pool: with U = n_pages - *n_free pages in use, the k-th page in
+ * use with an id >= U goes to the k-th free id < U, so that ids 0 .. U - 1 are
+ * in use and the pool can be cut there.  Rewrites the entries of block_table
+ * (request r holds ceil(len[r] / page_size); len int32 [n_req]), moves the
+ * counts (refs may be NULL), sets free_pages[i] = n_pages - 1 - i for i <
+ * *n_free, and writes the moves to copies (int32 [n_pages][2], 8-byte aligned)
+ * and *n_copies for flamia_paged_copy, which must run before the pages are
+ * used.  They are also the new ids of pages held beside the tables.
+ * Conditions, checked before anything is written but `copies` (in pages_ws):
+ * FLAMIA_ERR_BAD_SEQLENS (len), FLAMIA_ERR_BAD_PAGE (*n_free out of range, a
+ * free page out of range or twice on the stack, a table entry out of range or
+ * on the stack).  Then nothing moves and *n_copies = 0. */
+flamia_status_t flamia_paged_compact(const flamia_paged_t* p, const int32_t* len, int32_t* refs, int32_t* free_pages,
+                                     const int32_t* n_free, int32_t* copies, int32_t* n_copies, void* pages_ws,
+                                     size_t pages_ws_bytes, cudaStream_t stream);
 
 /* Writes the step's K and V rows (in_dtype, [T][Hkv][d], kv_stride) into
  * their slots: rounded to bf16, or as E4M3 codes with the row's no-clamp

@@ -24,7 +24,8 @@ EXPORTED = ("flamia_workspace_size", "flamia_plan", "flamia_quantize", "flamia_f
             "flamia_get_device_status", "flamia_clear_device_status", "flamia_status_string",
             "flamia_debug_set_phat_dump", "flamia_debug_withhold_first_item", "flamia_debug_workspace_offset",
             "flamia_plan_noalloc", "flamia_debug_mma_idesc", "flamia_debug_smem_desc",
-            "flamia_paged_workspace_size", "flamia_paged_plan", "flamia_paged_append", "flamia_paged_fwd")
+            "flamia_paged_workspace_size", "flamia_paged_plan", "flamia_paged_append", "flamia_paged_fwd",
+            "flamia_paged_pages_workspace_size", "flamia_paged_plan_shared", "flamia_paged_copy", "flamia_paged_compact")
 WS_FWD_ITEMS, WS_BWD_ITEMS, WS_DQ_PRESCALE = range(3)
 MMA_F8F6F4, MMA_MXF8F6F4, MMA_MXF4NVF4 = range(3)
 MMA_BF16 = 4
@@ -110,6 +111,11 @@ def load_library(path: str = LIB_PATH):
     L.flamia_paged_plan.restype, L.flamia_paged_plan.argtypes = i32, [G, vp, vp, vp, vp, vp, vp, sz, vp]
     L.flamia_paged_append.restype, L.flamia_paged_append.argtypes = i32, [G, vp, vp, vp, K, vp, sz, vp]
     L.flamia_paged_fwd.restype, L.flamia_paged_fwd.argtypes = i32, [G, vp, K, vp, vp, vp, sz, vp]
+    L.flamia_paged_pages_workspace_size.restype, L.flamia_paged_pages_workspace_size.argtypes = sz, [G]
+    L.flamia_paged_plan_shared.restype = i32
+    L.flamia_paged_plan_shared.argtypes = [G] + 9 * [vp] + [vp, sz, vp, sz, vp]
+    L.flamia_paged_copy.restype, L.flamia_paged_copy.argtypes = i32, [G, i32, K, K, vp, i32, vp, vp, sz, vp]
+    L.flamia_paged_compact.restype, L.flamia_paged_compact.argtypes = i32, [G] + 6 * [vp] + [vp, sz, vp]
     _lib = L
     return L
 
@@ -306,6 +312,53 @@ def flamia_paged_plan(prob: Paged, ws, slot_map=None, old_len=None, free_pages=N
                 _ptr(n_free_out))
 
 
+def flamia_paged_pages_workspace_size(prob: Paged) -> int:
+    """Bytes of the second workspace that the calls on shared pages take (see include/flamia.h)."""
+    return int(load_library().flamia_paged_pages_workspace_size(ctypes.byref(prob)))
+
+
+def _words(where, *pairs):
+    """int32 tensors of at least so many words in a row (None passes)."""
+    import torch
+    for t, n in pairs:
+        if t is not None and (t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous()):
+            raise FlamiaError(ERR_INVALID_ARG, where)
+
+
+def flamia_paged_plan_shared(prob: Paged, ws, pages_ws, slot_map, src, old_len, refs, free_pages, n_free, n_free_out, copies,
+                             n_copies, stream=None):
+    """Once per step of requests that share pages: forks (src), counts, copies on write, then as flamia_paged_plan.
+    copies [n_req, 2] and n_copies list the pages that flamia_paged_copy must copy before anything is appended."""
+    _words("flamia_paged_plan_shared", (slot_map, prob.T), (src, prob.n_req), (old_len, prob.n_req), (refs, prob.n_pages),
+           (free_pages, prob.n_pages), (n_free, 1), (n_free_out, 1), (copies, 2 * prob.n_req), (n_copies, 1))
+    _paged_call("flamia_paged_plan_shared", ws, stream, prob, _ptr(slot_map), _ptr(src), _ptr(old_len), _ptr(refs),
+                _ptr(free_pages), _ptr(n_free), _ptr(n_free_out), _ptr(copies), _ptr(n_copies), pages_ws.data_ptr(),
+                pages_ws.nbytes)
+
+
+def flamia_paged_copy(prob: Paged, src, dst, copies, n_copies, pages_ws, stream=None):
+    """Pages copied in every layer: src and dst are lists of caches (paged_cache), which may be the same list."""
+    n = len(src)
+    if n == 0 or len(dst) != n:
+        raise FlamiaError(ERR_INVALID_ARG, "flamia_paged_copy")
+    for cache in src if dst is src else (*src, *dst):
+        _check_pool(prob, cache, "flamia_paged_copy")
+    _words("flamia_paged_copy", (copies, 0), (n_copies, 1))
+    a = (Cache * n)(*src)
+    b = a if dst is src else (Cache * n)(*dst)
+    _paged_call("flamia_paged_copy", pages_ws, stream, prob, n, a, b, copies.data_ptr(), copies.numel() // 2,
+                n_copies.data_ptr())
+
+
+def flamia_paged_compact(prob: Paged, pages_ws, length, refs, free_pages, n_free, copies, n_copies, stream=None):
+    """The pages in use to the low end of the pool: tables, counts (refs may be None) and stack rewritten, the moves
+    listed in copies [n_pages, 2] and n_copies for flamia_paged_copy."""
+    _words("flamia_paged_compact", (length, prob.n_req), (refs, prob.n_pages), (free_pages, prob.n_pages), (n_free, 1),
+           (copies, 2 * prob.n_pages), (n_copies, 1))
+    _paged_call("flamia_paged_compact", pages_ws, stream, prob, _ptr(length), _ptr(refs), _ptr(free_pages), _ptr(n_free),
+                _ptr(copies), _ptr(n_copies))
+
+
 def _check_pool(prob, cache, where):
     if cache.pool is not None:
         page, n_pages = cache.pool
@@ -414,7 +467,11 @@ class PagedCall:
     One step: ``plan(cu_q, kv_len)`` once, then per layer ``append(layer, k, v)`` and ``attend(layer, q)``; all on the
     current stream, no host synchronisation, so a step can be captured in a CUDA graph (cu_q and kv_len are then read
     from the tensors given at capture).  A request that ends passes kv_len 0; its pages serve others.  After a plan
-    whose status is not OK (ERR_NO_PAGES, say) no page has moved: plan again with other lengths."""
+    whose status is not OK (ERR_NO_PAGES, say) no page has moved: plan again with other lengths.
+
+    With ``shared`` requests may hold the same pages: ``plan(cu_q, kv_len, src)`` says which request (as it was before
+    the step) each one continues, -1 none; forks share pages, and one that is written to is copied first.  ``compact()``
+    moves the pages in use to the low end of the pools."""
 
     n_req: int
     T: int           # new tokens of a step at most
@@ -431,6 +488,7 @@ class PagedCall:
     causal: bool = True
     softmax_scale: float = 0.0
     device: object = "cuda"
+    shared: bool = False
 
     def __post_init__(self):
         import torch
@@ -461,6 +519,12 @@ class PagedCall:
         self.k_blocks, self.v_blocks = pair((*rows, self.d // 16), 0) if e2m1 else (None, None)
         pools = [x for x in (self.k, self.v, self.k_scales, self.v_scales, self.k_blocks, self.v_blocks) if x is not None]
         self.caches = [paged_cache(*layer) for layer in zip(*pools)]
+        if self.shared:
+            self.refs = torch.zeros(self.n_pages, **i32)
+            self.same = torch.arange(self.n_req, **i32)
+            self.src = self.same.clone()
+            self.copies, self.n_copies = torch.zeros(max(self.n_req, self.n_pages), 2, **i32), torch.zeros(1, **i32)
+            self.pages_ws = torch.zeros(flamia_paged_pages_workspace_size(self.prob), dtype=torch.uint8, device=self.device)
         self.O = torch.zeros(self.T, self.H, self.d, dtype=torch.bfloat16, device=self.device)
         self.lse = torch.zeros(self.H, self.T, dtype=torch.float32, device=self.device)
         self.kv_dtype = torch.bfloat16 if self.in_dtype == BF16 else torch.float32
@@ -472,15 +536,34 @@ class PagedCall:
                     device not in (None, x.device)):
                 raise FlamiaError(ERR_INVALID_ARG, "PagedCall." + where)
 
-    def plan(self, cu_q, kv_len):
+    def plan(self, cu_q, kv_len, src=None):
         """cu_q [n_req + 1], kv_len [n_req]: int32 tensors; kv_len counts the step's new tokens too.  They are copied
-        on the stream: pinned host tensors must keep their values until that has run."""
+        on the stream: pinned host tensors must keep their values until that has run.  src [n_req] int32 (``shared``
+        only; None: each continues itself): see the class."""
         import torch
-        self._check("plan", None, (cu_q, self.cu_q.shape, torch.int32), (kv_len, self.kv_len.shape, torch.int32))
+        self._check("plan", None, (cu_q, self.cu_q.shape, torch.int32), (kv_len, self.kv_len.shape, torch.int32),
+                    *(() if src is None else ((src, self.kv_len.shape, torch.int32),)))
+        if src is not None and not self.shared:
+            raise FlamiaError(ERR_INVALID_ARG, "PagedCall.plan")
         self.cu_q.copy_(cu_q, non_blocking=True)
         self.kv_len.copy_(kv_len, non_blocking=True)
-        flamia_paged_plan(self.prob, self.ws, self.slot_map, self.held_len, self.free_pages, self.n_free, self.n_free)
+        if self.shared:
+            self.src.copy_(self.same if src is None else src, non_blocking=True)
+            flamia_paged_plan_shared(self.prob, self.ws, self.pages_ws, self.slot_map, self.src, self.held_len, self.refs,
+                                     self.free_pages, self.n_free, self.n_free, self.copies, self.n_copies)
+            flamia_paged_copy(self.prob, self.caches, self.caches, self.copies, self.n_copies, self.pages_ws)
+        else:
+            flamia_paged_plan(self.prob, self.ws, self.slot_map, self.held_len, self.free_pages, self.n_free, self.n_free)
         torch.where(self.status == OK, self.kv_len, self.held_len, out=self.held_len)
+
+    def compact(self):
+        """The pages in use to ids 0 .. n_pages - n_free - 1 of every layer's pools, tables and data (``shared`` only).
+        Between steps: the next plan must follow before append and attend."""
+        if not self.shared:
+            raise FlamiaError(ERR_INVALID_ARG, "PagedCall.compact")
+        flamia_paged_compact(self.prob, self.pages_ws, self.held_len, self.refs, self.free_pages, self.n_free, self.copies,
+                             self.n_copies)
+        flamia_paged_copy(self.prob, self.caches, self.caches, self.copies, self.n_copies, self.pages_ws)
 
     def append(self, layer, k, v):
         """k, v [T, Hkv, d] (in_dtype, contiguous); rows behind cu_q[n_req] may hold anything."""

@@ -103,6 +103,7 @@ struct PagedParams {
   int32_t* free_pages;
   const int32_t* n_free;
   int32_t* n_free_out;
+  const uint32_t* before;  // status of the page management that ran before in the same call (NULL: none)
   // append, forward
   const void* k_new;
   const void* v_new;

@@ -4,7 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include "kernels.h"
-#include "paged.cuh"
+#include "paged_pages.cuh"
 
 using namespace flamia;
 
@@ -147,6 +147,50 @@ flamia_status_t fill_cache(const flamia_paged_t* p, const flamia_cache_t* c, Pag
   return FLAMIA_OK;
 }
 
+PagesLayout pages_layout(const flamia_paged_t& p) {
+  PagesLayout L{};
+  auto a256 = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t table = sizeof(int32_t) * (size_t)p.n_req * p.max_pages;
+  L.header = 0;
+  L.pages = sizeof(PagesHeader);
+  size_t o = a256(L.pages + sizeof(PageRec) * (size_t)p.n_pages);
+  L.staged = o; o = a256(o + table);
+  L.freed = o; o = a256(o + table);
+  L.n_freed = o; o = a256(o + sizeof(int32_t) * p.n_req);
+  L.copy = o; o = a256(o + sizeof(int32_t) * p.n_req);
+  L.total = o;
+  return L;
+}
+
+flamia_status_t fill_pages(const flamia_paged_t* p, void* pages_ws, size_t bytes, PagesParams* a) {
+  flamia_status_t s = validate(p);
+  if (s != FLAMIA_OK) return s;
+  const PagesLayout L = pages_layout(*p);
+  if (!dev16(pages_ws)) return FLAMIA_ERR_INVALID_ARG;
+  if (bytes < L.total) return FLAMIA_ERR_WORKSPACE_TOO_SMALL;
+  *a = PagesParams{};
+  a->n_req = p->n_req;
+  a->T = p->T;
+  a->max_q = max_q_of(p);
+  a->page_size = p->page_size;
+  a->page_shift = p->page_size == 16 ? 4 : p->page_size == 32 ? 5 : p->page_size == 64 ? 6 : 7;
+  a->n_pages = p->n_pages;
+  a->max_pages = p->max_pages;
+  a->cu_q = p->cu_q;
+  a->kv_len = p->kv_len;
+  a->block_table = p->block_table;
+  uint8_t* b = static_cast<uint8_t*>(pages_ws);
+  a->hdr = reinterpret_cast<PagesHeader*>(b + L.header);
+  a->pages = reinterpret_cast<PageRec*>(b + L.pages);
+  a->staged = reinterpret_cast<int32_t*>(b + L.staged);
+  a->freed = reinterpret_cast<int32_t*>(b + L.freed);
+  a->n_freed = reinterpret_cast<int32_t*>(b + L.n_freed);
+  a->copy = reinterpret_cast<int32_t*>(b + L.copy);
+  a->bits = reinterpret_cast<uint32_t*>(b + L.pages);
+  a->rank = reinterpret_cast<int32_t*>(b + L.pages + 4 * (size_t)p->n_pages);
+  return FLAMIA_OK;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
@@ -211,6 +255,99 @@ flamia_status_t flamia_paged_plan(const flamia_paged_t* p, int32_t* slot_map, co
   cudaError_t e = launch_paged_plan(a, stream);
   if (e == cudaSuccess && same) e = cudaMemcpyAsync(n_free_out, a.n_free_out, sizeof(int32_t), cudaMemcpyDeviceToDevice, stream);
   return of(e);
+}
+
+size_t flamia_paged_pages_workspace_size(const flamia_paged_t* p) {
+  return validate(p) == FLAMIA_OK ? pages_layout(*p).total : 0;
+}
+
+flamia_status_t flamia_paged_plan_shared(const flamia_paged_t* p, int32_t* slot_map, const int32_t* src,
+                                         const int32_t* old_len, int32_t* refs, int32_t* free_pages, const int32_t* n_free,
+                                         int32_t* n_free_out, int32_t* copies, int32_t* n_copies, void* pages_ws,
+                                         size_t pages_ws_bytes, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  PagedParams a;
+  PagesParams b;
+  flamia_status_t s = fill(p, ws, ws_bytes, &a);
+  if (s != FLAMIA_OK) return s;
+  if ((s = fill_pages(p, pages_ws, pages_ws_bytes, &b)) != FLAMIA_OK) return s;
+  if (a.count_places) return FLAMIA_ERR_UNSUPPORTED;  // the plan could refuse the step once its pages have moved
+  if (!dev4(old_len) || !dev4(refs) || !dev4(free_pages) || !dev4(n_free) || !dev4(n_free_out) || !dev4(copies) ||
+      !dev4(n_copies) || !aligned(src, 4) || !aligned(slot_map, 4))
+    return FLAMIA_ERR_INVALID_ARG;
+  b.src = src;
+  b.old_len = old_len;
+  b.refs = refs;
+  b.free_pages = free_pages;
+  b.n_free = n_free;
+  b.n_free_out = n_free_out;
+  b.copies = copies;
+  b.n_copies = n_copies;
+  a.slot_map = slot_map;
+  a.before = &b.hdr->fail;
+  const cudaError_t e = launch_paged_share(b, sm_count(), stream);
+  return of(e != cudaSuccess ? e : launch_paged_plan(a, stream));
+}
+
+flamia_status_t flamia_paged_compact(const flamia_paged_t* p, const int32_t* len, int32_t* refs, int32_t* free_pages,
+                                     const int32_t* n_free, int32_t* copies, int32_t* n_copies, void* pages_ws,
+                                     size_t pages_ws_bytes, cudaStream_t stream) {
+  PagesParams b;
+  flamia_status_t s = fill_pages(p, pages_ws, pages_ws_bytes, &b);
+  if (s != FLAMIA_OK) return s;
+  if (!dev4(len) || !aligned(refs, 4) || !dev4(free_pages) || !dev4(n_free) || !copies || !aligned(copies, 8) || !dev4(n_copies))
+    return FLAMIA_ERR_INVALID_ARG;
+  b.old_len = len;
+  b.refs = refs;
+  b.free_pages = free_pages;
+  b.n_free = n_free;
+  b.copies = copies;
+  b.n_copies = n_copies;
+  return of(launch_paged_compact(b, sm_count(), stream));
+}
+
+flamia_status_t flamia_paged_copy(const flamia_paged_t* p, int32_t n_layers, const flamia_cache_t* src,
+                                  const flamia_cache_t* dst, const int32_t* copies, int32_t max_copies,
+                                  const int32_t* n_copies, void* pages_ws, size_t pages_ws_bytes, cudaStream_t stream) {
+  PagesParams b;
+  flamia_status_t s = fill_pages(p, pages_ws, pages_ws_bytes, &b);
+  if (s != FLAMIA_OK) return s;
+  if (n_layers < 1 || !src || !dst || !dev4(copies) || max_copies < 0 || !dev4(n_copies)) return FLAMIA_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n_layers; ++i) {  // all of them before the first launch
+    PagedParams c;
+    if ((s = fill_cache(p, src + i, &c)) != FLAMIA_OK || (s = fill_cache(p, dst + i, &c)) != FLAMIA_OK) return s;
+  }
+  const int kind = cache_of(p);
+  const int64_t rows = (int64_t)p->Hkv * p->page_size, kv = rows * p->d;
+  if (kv / 8 > (1 << 28)) return FLAMIA_ERR_UNSUPPORTED;  // 16-byte pieces of a page count in 32 bits
+  for (int32_t l0 = 0; l0 < n_layers; l0 += kCopyLayers) {
+    CopyParams a{};
+    a.layers = n_layers - l0 < kCopyLayers ? n_layers - l0 : kCopyLayers;
+    for (int i = 0; i < a.layers; ++i) {
+      PagedParams from{}, to{};
+      fill_cache(p, src + l0 + i, &from);
+      fill_cache(p, dst + l0 + i, &to);
+      CopyLayer& c = a.layer[i];
+      const uint8_t* f[6] = {from.k, from.v, from.k_scales, from.v_scales, from.k_blocks, from.v_blocks};
+      uint8_t* t[6] = {to.k, to.v, to.k_scales, to.v_scales, to.k_blocks, to.v_blocks};
+      for (int j = 0; j < 6; ++j) {
+        c.src[j] = f[j];
+        c.dst[j] = t[j];
+      }
+      a.src_stride[i] = from.page_bytes;
+      a.dst_stride[i] = to.page_bytes;
+    }
+    a.n_pages = p->n_pages;
+    a.kv_vecs = (int)(kv / (kind == kCacheBF16 ? 8 : kind == kCacheE4M3 ? 16 : 32));
+    a.scale_vecs = kind == kCacheBF16 ? 0 : (int)(rows / 16);
+    a.block_vecs = kind == kCacheE2M1 ? (int)(kv / 256) : 0;
+    a.copies = copies;
+    a.n_copies = n_copies;
+    a.max_copies = max_copies;
+    a.hdr = b.hdr;
+    const cudaError_t e = launch_paged_copy(a, sm_count(), stream);
+    if (e != cudaSuccess) return of(e);
+  }
+  return FLAMIA_OK;
 }
 
 flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, const void* v, const int32_t* slot_map,

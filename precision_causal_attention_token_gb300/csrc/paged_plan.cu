@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     }
   }
   bad = __syncthreads_or(bad);
-  uint32_t why = bad ? FLAMIA_ERR_BAD_SEQLENS : FLAMIA_OK;
+  uint32_t why = bad ? FLAMIA_ERR_BAD_SEQLENS : p.before ? *p.before : (uint32_t)FLAMIA_OK;
   int n_free = 0, n_taken = 0, n_given = 0;
   if (manage && !bad) {
     n_free = *p.n_free;
