@@ -17,8 +17,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libflamia.so")
 UNITS = ["api.cu", "plan.cu", "quantize.cu", "fwd.cu", "bwd.cu", "paged_api.cu", "paged_plan.cu", "paged_append.cu",
-         "paged_decode.cu", "paged_chunk.cu", "paged_pages.cu", "paged_copy.cu"]
-HEADERS = ["common.cuh", "attn_common.cuh", "kernels.h", "paged.cuh", "paged_pages.cuh"]
+         "paged_decode.cu", "paged_decode4.cu", "paged_chunk.cu", "paged_pages.cu", "paged_copy.cu"]
+HEADERS = ["common.cuh", "attn_common.cuh", "kernels.h", "paged.cuh", "paged_decode.cuh", "paged_pages.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

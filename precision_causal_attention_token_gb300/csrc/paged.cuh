@@ -123,6 +123,7 @@ struct PagedParams {
 cudaError_t launch_paged_plan(const PagedParams& p, cudaStream_t st);
 cudaError_t launch_paged_append(const PagedParams& p, int d, int cache, bool in_bf16, int sms, cudaStream_t st);
 cudaError_t launch_paged_decode(const PagedParams& p, int d, int cache, cudaStream_t st);
+cudaError_t launch_paged_decode4(const PagedParams& p, int d, cudaStream_t st);
 cudaError_t launch_paged_chunk(const PagedParams& p, int d, int cache, const CUtensorMap& mq, const CUtensorMap& mk,
                                const CUtensorMap& mv, cudaStream_t st);
 // Workers of a launch on a GPU with `sms` SMs: what the kernel keeps resident.

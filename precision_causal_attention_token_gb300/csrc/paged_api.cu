@@ -375,7 +375,7 @@ flamia_status_t flamia_paged_fwd(const flamia_paged_t* p, const void* q, const f
   a.lse = lse;
   const int kind = cache_of(p);
   if (a.small_rows) {
-    const cudaError_t e = launch_paged_decode(a, p->d, kind, stream);
+    const cudaError_t e = kind == kCacheE2M1 ? launch_paged_decode4(a, p->d, stream) : launch_paged_decode(a, p->d, kind, stream);
     if (e != cudaSuccess || a.path != kPathChunk) return of(e);
   }
   CUtensorMap mq{}, mk{}, mv{};
