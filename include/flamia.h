@@ -292,6 +292,7 @@ flamia_status_t flamia_debug_withhold_first_item(int32_t on);
  *     FLAMIA_MMA_MXF4NVF4 kind::mxf4nvf4.block_scale.scale_vec::4X, E2M1
  *                         operands, UE4M3 scales (one per 16 K-elements);
  *     FLAMIA_MMA_BF16     kind::f16, BF16 x BF16, fp32 accumulator;
+ *     FLAMIA_MMA_F16      kind::f16, F16 x F16, fp32 accumulator;
  *   for an M x N tile (cta_group::1: M = 64 with N a multiple of 8, or
  *   M = 128 with N a multiple of 16; 8 or 16 <= N <= 256).  a_mn / b_mn = 1
  *   selects an MN-major operand (0 or 1; 0 for the E2M1 kind), a_sf_id /
@@ -307,7 +308,8 @@ typedef enum {
   FLAMIA_MMA_F8F6F4 = 0,
   FLAMIA_MMA_MXF8F6F4 = 1,
   FLAMIA_MMA_MXF4NVF4 = 2,
-  FLAMIA_MMA_BF16 = 4 /* the paged chunk kernel's */
+  FLAMIA_MMA_BF16 = 4, /* the paged chunk kernel's */
+  FLAMIA_MMA_F16 = 5   /* and its E2M1 tiles' */
 } flamia_mma_kind_t;
 typedef enum { FLAMIA_SWZ_NONE = 0, FLAMIA_SWZ_128B = 2, FLAMIA_SWZ_64B = 4, FLAMIA_SWZ_32B = 6 } flamia_swizzle_t;
 flamia_status_t flamia_debug_mma_idesc(int32_t kind, uint32_t M, uint32_t N, int32_t a_mn, int32_t b_mn,
@@ -582,6 +584,10 @@ flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, cons
  * statistics and accumulators are fp32.  Rounding of the weights for the P V
  * product, relative to each:
  *   chunk kernel                  bf16, 2^-8
+ *   chunk kernel, E2M1            f16, 2^-11, and below that at most 2^-25 of
+ *                                 the row's largest weight; bf16 in blocks of
+ *                                 128 keys where a V row's scale byte is not
+ *                                 112 to 127
  *   decode kernel, bf16 cache     two bf16 terms, 2^-16
  *   decode kernel, E4M3 or E2M1   f16, 2^-11, and below that at most 2^-20 of
  *                                 the row's largest weight; two bf16 terms

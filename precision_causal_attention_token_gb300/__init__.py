@@ -28,7 +28,7 @@ EXPORTED = ("flamia_workspace_size", "flamia_plan", "flamia_quantize", "flamia_f
             "flamia_paged_pages_workspace_size", "flamia_paged_plan_shared", "flamia_paged_copy", "flamia_paged_compact")
 WS_FWD_ITEMS, WS_BWD_ITEMS, WS_DQ_PRESCALE = range(3)
 MMA_F8F6F4, MMA_MXF8F6F4, MMA_MXF4NVF4 = range(3)
-MMA_BF16 = 4
+MMA_BF16, MMA_F16 = 4, 5
 SWZ_NONE, SWZ_128B, SWZ_64B, SWZ_32B = 0, 2, 4, 6
 
 

@@ -415,6 +415,10 @@ flamia_status_t flamia_debug_mma_idesc(int32_t kind, uint32_t M, uint32_t N, int
       if (a_sf_id || b_sf_id) return FLAMIA_ERR_INVALID_ARG;
       *out = bf16_idesc(M, N, (uint32_t)a_mn, (uint32_t)b_mn);
       return FLAMIA_OK;
+    case FLAMIA_MMA_F16:
+      if (a_sf_id || b_sf_id) return FLAMIA_ERR_INVALID_ARG;
+      *out = f16_idesc(M, N, (uint32_t)a_mn, (uint32_t)b_mn);
+      return FLAMIA_OK;
   }
   return FLAMIA_ERR_INVALID_ARG;
 }

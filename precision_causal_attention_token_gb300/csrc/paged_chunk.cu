@@ -33,13 +33,15 @@
 // The row's weights are rounded to bf16 once (2^-8 relative); sums use the
 // unrounded ones.
 //
-// Measured (152 SMs, H = 32, Hkv = 8, d = 128): 2,048 new tokens over 32,768 in
-// bf16 720 us (1,575 TFLOP/s; 808 back to back under the power limit), in E4M3
-// 850; four times 4,096 from nothing (16 heads each) 231 us in bf16, 294 in
-// E4M3.  bf16 is bound by the tensor cores, and by 3 to 4 us between one tile's last
-// product and the next one's first; E4M3 by shared memory, which conversion and
-// the MMAs' operands share: a step's operands take 1,536 of its 2,048 tensor
-// cycles, codes and converted tiles 1,024 more.
+// E2M1: f16 in place of bf16 in both products.  Codes times block scale times a
+// row's power of two are exact there for rows of a usual size (exponent bytes
+// 112 to 127: row maxima from 0.04 to 2,688) at two instructions a pair of
+// values, while bf16 takes five (2,048 over 32,768: 890 against 877 us, four times
+// 4,096: 360 against 308); K and V are held 16 times themselves.  The loaders turn
+// the queries into f16, with a power of two a row.  A block with other rows: K
+// goes without its rows' exponents and the softmax warps multiply them into the
+// scores; V, and the weights with it, as bf16.  2,048 over 32,768 took 905 us when each
+// row's scale was read after the stores of the row before.
 #include <climits>
 #include <type_traits>
 
@@ -88,7 +90,7 @@ struct __align__(1024) Tiles {
   uint8_t out[8][2048];  // softmax warps: 32 rows x 32 channels of O on their way out
 };
 
-struct Ctl {
+struct __align__(16) Ctl {
   uint8_t scales[4][128];  // raw ring: scale bytes
   uint64_t q_full[2], q_empty[2], kv_full[5], kv_empty[5], raw_full[4], raw_empty[4];
   uint64_t s_full[2], p_full[2], o_full[2], fix[5], wg[2];
@@ -100,8 +102,22 @@ struct Ctl {
   int abort_flag;
 };
 
+// E2M1: that the queries as f16 are there; per row (of four fragments in turn)
+// the exponent field E of its largest element, which the f16 row holds times
+// 2^(139 - E); per key block (of four in turn) whether K lacks its rows'
+// exponents, which are then beside it, and whether V, and so the weights, are bf16.
+struct __align__(16) Ctl4 {
+  uint64_t q_ready[2];
+  uint8_t q_exp[4][2][128];
+  uint8_t k_exp[4][128];
+  int odd_k[4], odd_v[4];
+};
+static_assert(sizeof(Ctl) % 16 == 0, "Ctl4 behind it");
+
 template <int D, int CACHE>
-constexpr size_t smem_bytes() { return sizeof(Tiles<D, CACHE>) + sizeof(Ctl) + 1024; }
+constexpr size_t smem_bytes() {
+  return sizeof(Tiles<D, CACHE>) + sizeof(Ctl) + (CACHE == kCacheE2M1 ? sizeof(Ctl4) : 0) + 1024;
+}
 
 // D[tmem] (+)= A[smem] * B[smem], bf16, fp32 accumulate.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -136,36 +152,38 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // (0x1000 + 7 * 0x1000).
 __device__ __forceinline__ void e2m1_to_bf16(uint32_t w, uint32_t f, uint32_t* y) {
   uint32_t h[4];
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+  e2m1x8_to_f16(w, h);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint32_t t = h[k] >> 3;
     y[k] = bf16x2_mul(t + (t & 0x10001000u) * 7u, f);
   }
 }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 // S[half] = Q[half] K^T: both K-major, 128-byte swizzled rows of 64 channels.
 template <int D>
-__device__ __forceinline__ void issue_s(uint32_t d, const uint8_t* q, const uint8_t* k) {
+__device__ __forceinline__ void issue_s(uint32_t d, const uint8_t* q, const uint8_t* k, uint32_t idesc) {
   const uint32_t qa = smem_u32(q), ka = smem_u32(k);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = (kk / 4) * 128 * 128 + (kk % 4) * 32;
-    mma_ss(d, smem_desc(qa + off, 16, 1024, kSwz128), smem_desc(ka + off, 16, 1024, kSwz128), bf16_idesc(128, 128, 0, 0), kk > 0);
+    mma_ss(d, smem_desc(qa + off, 16, 1024, kSwz128), smem_desc(ka + off, 16, 1024, kSwz128), idesc, kk > 0);
   }
 }
 // O[half] += P[half] V: P in tensor memory, V's rows are keys (MN-major B):
 // 64 channels a 128-byte row, the next 64 channels 16 KB on (leading
 // offset), the next 8 keys 1 KB on (stride offset).
 template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, const uint8_t* v, bool acc) {
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pcol, const uint8_t* v, bool acc, uint32_t idesc) {
   const uint32_t va = smem_u32(v);
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
-    mma_ts(d, pcol + 8 * kk, smem_desc(va + kk * 16 * 128, 128 * 128, 1024, kSwz128), bf16_idesc(128, D, 0, 1), acc || kk > 0);
+    mma_ts(d, pcol + 8 * kk, smem_desc(va + kk * 16 * 128, 128 * 128, 1024, kSwz128), idesc, acc || kk > 0);
 }
 
 template <int D, int CACHE>
@@ -178,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* base = smem_base_1k(smem_raw);
   Tiles<D, CACHE>& tl = *reinterpret_cast<Tiles<D, CACHE>*>(base);
   Ctl& c = *reinterpret_cast<Ctl*>(base + sizeof(Tiles<D, CACHE>));
+  [[maybe_unused]] Ctl4& c4 = *reinterpret_cast<Ctl4*>(base + sizeof(Tiles<D, CACHE>) + sizeof(Ctl));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   WsHeader* hdr = &p.hdr->base;
   volatile int* abort_flag = &c.abort_flag;
@@ -195,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&c.q_full[s], 1);
+      if (C::kFp4) mbar_init(&c4.q_ready[s], 128);
       mbar_init(&c.q_empty[s], 1);
     }
     for (int s = 0; s < 5; ++s) {
@@ -393,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0, pc[2] = {0, 0}, qc[2] = {0, 0}, fixed = 0;  // fixed: phase bits of fix[]
       bool ok = true;
       const uint32_t elected = elect_one();
+      constexpr uint32_t kIdescS = C::kFp4 ? f16_idesc(128, 128, 0, 0) : bf16_idesc(128, 128, 0, 0);
       Frag f;
       for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x805); ++n) {
         const int nh[2] = {f.n0, f.n1};
@@ -408,11 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf)
                 if (ok && nh[hf]) {
-                  ok = mbar_wait(&c.q_full[hf], qc[hf] & 1, abort_flag, hdr, 0x806);
+                  ok = mbar_wait(C::kFp4 ? &c4.q_ready[hf] : &c.q_full[hf], qc[hf] & 1, abort_flag, hdr, 0x806);
                   if (!ok) continue;
                   ++qc[hf];
                   tc_fence_after();
-                  issue_s<D>(tb + kColS + 128 * hf, tl.q[hf], tl.kv[it % C::kStages]);
+                  issue_s<D>(tb + kColS + 128 * hf, tl.q[hf], tl.kv[it % C::kStages], kIdescS);
                   tc_commit(&c.s_full[hf]);
                   if (nh[hf] == 1) tc_commit(&c.q_empty[hf]);
                 }
@@ -430,6 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = mbar_wait(&c.fix[s], (fixed >> s) & 1, abort_flag, hdr, 0x808))) break;
                 fixed ^= 1u << s;
               }
+              const bool v_f16 = C::kFp4 && *reinterpret_cast<volatile int*>(&c4.odd_v[(it / 2 + b) & 3]) == 0;
+              const uint32_t idesc_v = v_f16 ? f16_idesc(128, D, 0, 1) : bf16_idesc(128, D, 0, 1);
               bool k_in = false;
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {
@@ -438,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (!ok) continue;
                   ++pc[hf];
                   tc_fence_after();
-                  issue_pv<D>(tb + kColO + 128 * hf, tb + kColS + 128 * hf, vt, b > 0);
+                  issue_pv<D>(tb + kColO + 128 * hf, tb + kColS + 128 * hf, vt, b > 0, idesc_v);
                   if (b + 1 == nh[hf]) tc_commit(&c.o_full[hf]);
                 }
                 if (ok && b + 1 < nh[hf]) {
@@ -448,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     k_in = true;
                     tc_fence_after();
                   }
-                  issue_s<D>(tb + kColS + 128 * hf, tl.q[hf], kt);
+                  issue_s<D>(tb + kColS + 128 * hf, tl.q[hf], kt, kIdescS);
                   tc_commit(&c.s_full[hf]);
                   // the queries are free once the last block's scores are formed
                   if (b + 2 == nh[hf]) tc_commit(&c.q_empty[hf]);
@@ -470,6 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- loaders
     const int lt = tid - 256;
     uint32_t it = 0;
+    [[maybe_unused]] uint32_t q_uses[2] = {0, 0};
+    [[maybe_unused]] bool v_in = true;  // E2M1: V of the present block can be f16
     bool ok = true;
     Frag f;
     for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x80a); ++n) {
@@ -479,7 +504,150 @@ __global__ void __launch_bounds__(kThreads, 1)
       // no loader warp is at the one four on before this one has gone on.
       if (lt == 0) c.odd_key[(n + 4) % 8] = INT_MAX;
       int* odd_key = &c.odd_key[n % 8];
-      if constexpr (FP8) {
+      if constexpr (C::kFp4) {
+        for (int b = 0; ok && b < 2 * f.load; ++b, ++it) {
+          const int rs = it % C::kRaw, s = it % C::kStages, slot = (it >> 1) & 3;
+          const int keys = f.kv_len - (f.kb0 + b / 2) * kChunkBlk;  // rows from here on are cleared
+          if (!(ok = mbar_wait_warp(&c.raw_full[rs], (it / C::kRaw) & 1, abort_flag, hdr, 0x80c))) break;
+          if (!(ok = mbar_wait_warp(&c.kv_empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag, hdr, 0x80d))) break;
+          // A thread takes the same 16 channels (one block) of every kStep-th row;
+          // the two 64-channel columns as for E4M3.
+          constexpr int kCh = D / 16, kStep = 128 / kCh;
+          const int ch = lt % kCh, row0 = lt / kCh, flip = (ch >> 2) & 1;
+          const uint8_t* src = tl.raw[rs] + row0 * C::kCodeB + ch * 8;
+          const uint8_t* blk = tl.raw[rs] + 128 * C::kCodeB + row0 * C::kBlkB + ch;
+          const uint8_t* exps = c.scales[rs] + row0;
+          uint8_t* dst = tl.kv[s] + (ch / 4) * 128 * 128 + row0 * 128;
+          const uint32_t at0 = (((2 * ch) & 7) ^ (row0 & 7)) << 4, at1 = at0 ^ 16;
+          auto put = [&](int i, const uint32_t (&y)[8]) {
+            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+            uint8_t* d = dst + i * kStep * 128;
+            *reinterpret_cast<uint4*>(d + (flip ? at1 : at0)) = flip ? hi : lo;
+            *reinterpret_cast<uint4*>(d + (flip ? at0 : at1)) = flip ? lo : hi;
+          };
+          // as f16: 16 values times 16 2^(sc - 127), 112 <= sc <= 127: whole numbers times
+          // 2^-21, at most 43,008, so exact
+          auto factor = [](uint32_t b, uint32_t sc) {
+            return f16x2_mul(e4m3x2_to_f16(b * 0x0101u), sc * 0x04000400u - 108u * 0x04000400u);
+          };
+          auto to_f16 = [](const uint2& x, uint32_t f, uint32_t (&y)[8]) {
+            uint32_t h[4];
+            e2m1x8_to_f16(x.x, h);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = f16x2_mul(h[k], f);
+            e2m1x8_to_f16(x.y, h);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[4 + k] = f16x2_mul(h[k], f);
+          };
+          // Whether all rows that count have exponent bytes 112 to 127.  V's are looked
+          // at before K goes out, so that the softmax warps know with the scores what
+          // V will be.
+          auto in_range = [&](int r) {
+            uint32_t e4 = *reinterpret_cast<const uint32_t*>(&c.scales[r][4 * lane]);
+            if (keys < kChunkBlk) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (4 * lane + k >= keys) e4 = (e4 & ~(255u << (8 * k))) | 0x70u << (8 * k);
+            }
+            return (bool)__all_sync(0xffffffffu, (e4 & 0xF0F0F0F0u) == 0x70707070u);
+          };
+          const bool in = b & 1 ? v_in : in_range(rs);
+          if (!(b & 1)) {
+            const int rv = (it + 1) % C::kRaw;
+            if (!(ok = mbar_wait_warp(&c.raw_full[rv], ((it + 1) / C::kRaw) & 1, abort_flag, hdr, 0x819))) break;
+            v_in = in_range(rv);
+            if (lt == 0) {
+              c4.odd_k[slot] = !in;
+              c4.odd_v[slot] = !v_in;
+            }
+          }
+          if (in && keys >= kChunkBlk) {
+            // Two rows' loads before their stores, which they could not pass (the compiler
+            // does not know that they are apart).  Rolled: with the code of more rows the
+            // roles outgrow the instruction cache (four and eight 4,096: 320, 339 us; two: 308).
+#pragma unroll 1
+            for (int i0 = 0; i0 < kCh; i0 += 2) {
+              uint2 x[2];
+              uint32_t fac[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                x[i] = *reinterpret_cast<const uint2*>(src + (i0 + i) * kStep * C::kCodeB);
+                fac[i] = factor(blk[(i0 + i) * kStep * C::kBlkB], exps[(i0 + i) * kStep]);
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t y[8];
+                to_f16(x[i], fac[i], y);
+                put(i0 + i, y);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < kCh; ++i) {
+              const int row = row0 + i * kStep;
+              const uint32_t sc = exps[i * kStep];
+              const uint2 x = *reinterpret_cast<const uint2*>(src + i * kStep * C::kCodeB);
+              uint32_t y[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = 0u;
+              if (row < keys) {
+                if (in) {
+                  to_f16(x, factor(blk[i * kStep * C::kBlkB], sc), y);
+                } else if (!(b & 1)) {  // K without its exponent, which goes to the scores
+                  to_f16(x, factor(blk[i * kStep * C::kBlkB], 123u), y);  // codes times block scale
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) y[k] = sc == 255u ? 0x7E007E00u : y[k];
+                } else if (sc == 255u) {
+                  atomicMin(odd_key, (f.kb0 + b / 2) * kChunkBlk + row);
+                } else {  // V as bf16, times 16 like the others; a scale above 2^3 in two factors
+                  const float bs = unpack_e4m3x2((uint16_t)blk[i * kStep * C::kBlkB]).x * __uint_as_float((min(sc, 130u) + 116u) << 23);
+                  const uint32_t f1 = prmt(__float_as_uint(bs), 0u, 0x3232u), f2 = (max(sc, 130u) - 130u + 127u) * 0x00800080u;
+                  e2m1_to_bf16(x.x, f1, &y[0]);
+                  e2m1_to_bf16(x.y, f1, &y[4]);
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) y[k] = bf16x2_mul(y[k], f2);
+                }
+              }
+              put(i, y);
+            }
+          }
+          if (!(b & 1) && !in) c4.k_exp[slot][lt] = c.scales[rs][lt];
+          fence_proxy_async_smem();
+          mbar_arrive(&c.kv_full[s]);
+          mbar_arrive(&c.raw_empty[rs]);
+          if (b != 1) continue;
+          // The queries, a row a thread: f16 in place, with a power of two that puts
+          // the row's largest element at 2^12 to 2^13 (what f16 cannot hold lies 2^-37
+          // below it).  After the first two tiles, which need not wait for them.
+          for (int hf = 0; ok && hf < 2; ++hf) {
+            if ((hf ? f.n1 : f.n0) == 0) continue;
+            if (!(ok = mbar_wait_warp(&c.q_full[hf], q_uses[hf] & 1, abort_flag, hdr, 0x817))) break;
+            ++q_uses[hf];
+            uint8_t* qt = tl.q[hf];
+            auto at_piece = [&](int k) { return reinterpret_cast<uint4*>(qt + (k / 8) * 128 * 128 + sw128_off(lt, k % 8)); };
+            uint32_t top = 0;
+#pragma unroll 4
+            for (int k = 0; k < D / 8; ++k) {
+              const uint4 x = *at_piece(k);
+              top = max_u16x2(max_u16x2(top, max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)),
+                              max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+            }
+            const int E = min(max((int)(max(top & 0xFFFFu, top >> 16) >> 7), 13), 254);
+            const float up = exp2i(139 - E);
+            c4.q_exp[n & 3][hf][lt] = (uint8_t)E;
+#pragma unroll 4
+            for (int k = 0; k < D / 8; ++k) {
+              uint4 x = *at_piece(k);
+              uint32_t* wd = &x.x;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) wd[j] = pack_f16x2(bf16_lo(wd[j]) * up, bf16_hi(wd[j]) * up);
+              *at_piece(k) = x;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&c4.q_ready[hf]);
+          }
+        }
+      } else if constexpr (FP8) {
         for (int b = 0; ok && b < 2 * f.load; ++b, ++it) {
           const int rs = it % C::kRaw, s = it % C::kStages;
           const int keys = f.kv_len - (f.kb0 + b / 2) * kChunkBlk;  // rows from here on are cleared
@@ -492,28 +660,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int kRawCh = D / 16, kStep = 128 / kRawCh, kBatch = kRawCh;
           const int ch = lt % kRawCh, row0 = lt / kRawCh;
           const int flip = (ch >> 2) & 1;
-          const uint8_t* src = tl.raw[rs] + row0 * C::kCodeB + ch * (C::kCodeB / (D / 16));
-          using Raw = std::conditional_t<C::kFp4, uint2, uint4>;  // 16 channels' codes
+          const uint8_t* src = tl.raw[rs] + row0 * D + ch * 16;
           uint8_t* dst = tl.kv[s] + (ch / 4) * 128 * 128 + row0 * 128;
           const uint32_t at0 = (((2 * ch) & 7) ^ (row0 & 7)) << 4, at1 = at0 ^ 16;
-          // sc <= 134: times 2^(sc - 127)
-          auto convert = [&](const Raw& x, int i, uint32_t sc, uint32_t (&y)[8]) {
-            if constexpr (C::kFp4) {
-              // 2^112 undoes the conversion's bias
-              const uint32_t b = tl.raw[rs][128 * C::kCodeB + (row0 + i * kStep) * C::kBlkB + ch];
-              const float s = unpack_e4m3x2((uint16_t)b).x * __uint_as_float((sc + 112u) << 23);
-              const uint32_t f = prmt(__float_as_uint(s), 0u, 0x3232u);
-              e2m1_to_bf16(x.x, f, &y[0]);
-              e2m1_to_bf16(x.y, f, &y[4]);
-            } else {
-              // 2^120 undoes the conversion's bias: (byte + 120) << 7 in both halves
-              const uint32_t f = sc * 0x00800080u + 120u * 0x00800080u;
-              const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+          auto convert = [](const uint4& x, uint32_t f, uint32_t (&y)[8]) {
+            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                y[2 * k] = bf16x2_mul(e4m3_to_bf16x2(prmt(wd[k], 0u, 0x4140u)), f);
-                y[2 * k + 1] = bf16x2_mul(e4m3_to_bf16x2(prmt(wd[k], 0u, 0x4342u)), f);
-              }
+            for (int k = 0; k < 4; ++k) {
+              y[2 * k] = bf16x2_mul(e4m3_to_bf16x2(prmt(wd[k], 0u, 0x4140u)), f);
+              y[2 * k + 1] = bf16x2_mul(e4m3_to_bf16x2(prmt(wd[k], 0u, 0x4342u)), f);
             }
           };
           auto put = [&](int i, const uint32_t (&y)[8]) {
@@ -532,13 +687,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
             for (int i0 = 0; i0 < kRawCh; i0 += kBatch) {
-              Raw x[kBatch];
+              uint4 x[kBatch];
 #pragma unroll
-              for (int i = 0; i < kBatch; ++i) x[i] = *reinterpret_cast<const Raw*>(src + (i0 + i) * kStep * C::kCodeB);
+              for (int i = 0; i < kBatch; ++i) x[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * kStep * D);
 #pragma unroll
               for (int i = 0; i < kBatch; ++i) {
                 uint32_t y[8];
-                convert(x[i], i0 + i, sb[i0 + i], y);
+                // 2^120 undoes the conversion's bias: (byte + 120) << 7 in both halves
+                convert(x[i], sb[i0 + i] * 0x00800080u + 120u * 0x00800080u, y);
                 put(i0 + i, y);
               }
             }
@@ -552,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 8; ++k) y[k] = 0u;
               if (row < keys) {
                 if (sc != 255u) {  // a scale above 2^7: in two factors
-                  convert(*reinterpret_cast<const Raw*>(src + i * kStep * C::kCodeB), i, min(sc, 134u), y);
+                  convert(*reinterpret_cast<const uint4*>(src + i * kStep * D), min(sc, 134u) * 0x00800080u + 120u * 0x00800080u, y);
                   const uint32_t f2 = ((max(sc, 134u) - 134u + 127u) << 7) * 0x10001u;
 #pragma unroll
                   for (int k = 0; k < 8; ++k) y[k] = bf16x2_mul(y[k], f2);
@@ -619,10 +775,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hf = warp >> 2, row = tid & 127;
     const uint32_t ts = taddr(tb, (warp & 3) * 32, kColS + 128 * hf), to = taddr(tb, (warp & 3) * 32, kColO + 128 * hf);
     uint32_t sc = 0, oc = 0, wgc = 0;
+    [[maybe_unused]] uint32_t next_blk = 0;  // key blocks, as the loaders and the MMA issuer count them
     bool ok = true;
     Frag f;
     for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x810); ++n) {
       const int R = 128 * hf + row;
+      [[maybe_unused]] const uint32_t blk0 = next_blk;
+      next_blk += f.load;
       if (hf * p.half_toks >= f.toks) continue;  // the half is empty
       const int n_blk = hf ? f.n1 : f.n0;
       const int tok = hf * p.half_toks + row / p.G, hq = f.h * p.G + row % p.G;
@@ -630,11 +789,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int vis = row_ok ? min(f.kv_len, visible_keys(p.causal, f.q_len, f.kv_len, f.tok0 + tok)) : f.kv_len;
       const int vis_min = __reduce_min_sync(0xffffffffu, vis);
       float m = -INFINITY, l = 0.f;
+      float c_row = p.c_log2;  // of this row's scores, to base-2 logarithms
       for (int b = 0; ok && b < n_blk; ++b, ++sc) {
         if (!(ok = mbar_wait_warp(&c.s_full[hf], sc & 1, abort_flag, hdr, 0x811))) break;
         tc_fence_after();
         const int key0 = (f.kb0 + b) * kChunkBlk, nv = vis - key0;
         const bool masked = key0 + kChunkBlk > vis_min;
+        if constexpr (C::kFp4) {
+          const int slot = (blk0 + b) & 3;
+          // K is 16 times itself; above 0: a masked -inf stays one
+          if (b == 0) c_row = fmaxf(p.c_log2 * 0x1p-16f * exp2i((int)c4.q_exp[n & 3][hf][row] - 127), 1.17549435e-38f);
+          const int odd_k = *reinterpret_cast<volatile int*>(&c4.odd_k[slot]);
+          if (odd_k | *reinterpret_cast<volatile int*>(&c4.odd_v[slot])) {
+            // Rare, and slow: through tensor memory twice, a quarter at a time
+            // (its code within the usual one's: 1,007 us for 2,048 over 32,768).
+            // K without its exponents: the factors below, less 2^12
+            const float c_blk =
+                odd_k ? fminf(fmaxf(p.c_log2 * exp2i((int)c4.q_exp[n & 3][hf][row] - 127), 1.17549435e-38f), 3.4e38f) : c_row;
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t x[32];
+              tmem_ld32(ts + 32 * q, x);
+              tmem_ld_wait_regs(x);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float f = odd_k ? ue8m0(c4.k_exp[slot][32 * q + j]) * 0x1p-12f : 1.f;
+                x[j] = 32 * q + j >= nv ? 0xFF800000u : __float_as_uint(__uint_as_float(x[j]) * f);
+                top = fmaxf(top, __uint_as_float(x[j]));
+              }
+              tmem_st32(ts + 32 * q, x);
+            }
+            tmem_st_wait();
+            top *= c_blk;
+            const bool up = top > m + 8.f;
+            if (__any_sync(0xffffffffu, up)) {
+              const float a = up ? ex2_approx(m - top) : 1.f;  // 0 from an empty reference
+              if (up) m = top;
+              l *= a;
+#pragma unroll 1
+              for (int j = 0; b > 0 && j < D / 16; ++j) {  // s_full follows this half's previous P V
+                uint32_t o[16];
+                tmem_ld16(to + 16 * j, o);
+                tmem_ld_wait_regs(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                tmem_st16(to + 16 * j, o);
+              }
+            }
+            const float mref = m == -INFINITY ? 0.f : m;
+            const bool v_f16 = *reinterpret_cast<volatile int*>(&c4.odd_v[slot]) == 0;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t x[32], w0[16];
+              tmem_ld32(ts + 32 * q, x);
+              tmem_ld_wait_regs(x);
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float a0 = ex2_approx(__fmaf_rn(__uint_as_float(x[j]), c_blk, -mref));
+                const float a1 = ex2_approx(__fmaf_rn(__uint_as_float(x[j + 1]), c_blk, -mref));
+                l += a0 + a1;
+                w0[j / 2] = v_f16 ? pack_f16x2(a0, a1) : pack_bf16x2(a0, a1);
+              }
+              tmem_st16(ts + 16 * q, w0);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&c.p_full[hf]);
+            continue;
+          }
+        }
         if (FP8 && masked) {
           // through tensor memory, a quarter at a time: a fourth of the code.
           // The E4M3 kernel's roles fill the instruction cache (4 x 4,096: 312
@@ -675,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           t2 = fmax3(t2, __uint_as_float(s2[j]), __uint_as_float(s2[j + 1]));
           t3 = fmax3(t3, __uint_as_float(s3[j]), __uint_as_float(s3[j + 1]));
         }
-        const float top = fmaxf(fmax3(t0, t1, t2), t3) * p.c_log2;
+        const float top = fmaxf(fmax3(t0, t1, t2), t3) * c_row;
         const bool up = top > m + 8.f;
         if (__any_sync(0xffffffffu, up)) {
           const float a = up ? ex2_approx(m - top) : 1.f;  // 0 from an empty reference
@@ -696,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float mref = m == -INFINITY ? 0.f : m;
-        const uint64_t c2 = f2_pack(p.c_log2, p.c_log2), m2 = f2_pack(-mref, -mref);
+        const uint64_t c2 = f2_pack(c_row, c_row), m2 = f2_pack(-mref, -mref);
         uint64_t sum0 = 0, sum1 = 0;
         auto weights = [&](uint32_t (&x)[32], uint32_t* out) {
 #pragma unroll
@@ -707,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             a1 = ex2_approx(a1);
             if (j & 2) sum1 = f2_add(sum1, f2_pack(a0, a1));
             else sum0 = f2_add(sum0, f2_pack(a0, a1));
-            out[j / 2] = pack_bf16x2(a0, a1);
+            out[j / 2] = C::kFp4 ? pack_f16x2(a0, a1) : pack_bf16x2(a0, a1);
           }
         };
         uint32_t w0[32];
@@ -796,7 +1020,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      auto inverse = [](float x) { return x > 0.f ? 1.f / x : (x == 0.f ? 0.f : x); };  // a NaN sum stays
+      constexpr float kUnit = C::kFp4 ? 0.0625f : 1.f;  // E2M1: V is 16 times itself
+      auto inverse = [](float x) { return x > 0.f ? kUnit / x : (x == 0.f ? 0.f : x); };  // a NaN sum stays
       const int64_t slot = f.starts ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x;
       const float inv_l = inverse(l);
 #pragma unroll 1  // unrolled, the code outgrows the instruction cache (E4M3 4 x 4,096: 310 -> 367 us)

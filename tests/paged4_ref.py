@@ -50,9 +50,10 @@ def values4(codes, blocks, scales):
 
 
 class Step4(Step):
-    """A serving step over a 4-bit cache.  shift(n_pages, Hkv, ps) -> exponents added to the rows of V."""
+    """A serving step over a 4-bit cache.  shift(n_pages, Hkv, ps) -> exponents added to the rows of V; k_shift: to the
+    rows of K, and taken from the queries."""
 
-    def __init__(self, q, kv, *, strided=False, poison=False, shift=None, **kw):
+    def __init__(self, q, kv, *, strided=False, poison=False, shift=None, k_shift=0, **kw):
         super().__init__(q, kv, cache="bf16", **kw)
         dev = self.dev
         kf, vf = self.k.cpu(), self.v.cpu()
@@ -61,6 +62,9 @@ class Step4(Step):
         codes = [packed(c) for c in codes]
         if shift is not None:
             scales[1] = (scales[1].int() + shift(*scales[1].shape)).clamp(0, 254).to(torch.uint8)
+        if k_shift:
+            scales[0] = (scales[0].int() + k_shift).clamp(0, 254).to(torch.uint8)
+            self.q_rows.copy_((self.q_rows.double() * 2.0 ** -k_shift).bfloat16())
         if poison:  # what earlier owners left in slots that hold no token
             free = torch.ones(self.n_pages, self.ps, dtype=torch.bool)
             for r in range(self.n_req):
@@ -88,5 +92,12 @@ class Step4(Step):
                      for c, b, s in ((self.k, self.kb, self.ks), (self.v, self.vb, self.vs)))
 
     def rounding(self):
-        """As over an E4M3 cache: a value is up to 6 * 448 of its row's power of two, in place of 448."""
-        return (HALF_BF16, 0.0) if self.chunk_path() else (torch.finfo(torch.float16).eps / 2, 6.0 * 2.0 ** -32)
+        """As over an E4M3 cache, but that a value is up to 6 * 448 of its row's power of two, in place of 448, and that the
+        tile kernel's weights are f16 where all of V's exponent bytes are 112 to 127: off by 2^-25 of a reference that the
+        sum is at least 1 of below f16's normal range."""
+        half = torch.finfo(torch.float16).eps / 2
+        if not self.chunk_path():
+            return half, 6.0 * 2.0 ** -32
+        used = [self.vs[self.table_host[r][j // self.ps], :, j % self.ps] for r in range(self.n_req) for j in range(self.kv_len[r])]
+        used = torch.stack(used) if used else torch.full((1,), 127)
+        return (half, 6.0 * 2.0 ** -25) if int(used.min()) >= 112 and int(used.max()) <= 127 else (HALF_BF16, 6.0 * 2.0 ** -25)

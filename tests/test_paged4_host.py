@@ -1,4 +1,7 @@
 """The 4-bit cache without a GPU: refusals before any launch, and the tests' own model of its rows."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -93,6 +96,26 @@ def test_model_holds_every_row_within_a_step():
     s = torch.ldexp(blocks.view(torch.float8_e4m3fn).double(), (scales.int() - 127)[..., None]).repeat_interleave(16, -1)
     assert ((v - x.float().double()).abs() <= s).all()  # half the largest step, 2
     assert (v.abs() <= 6 * s).all()
+
+
+@pytest.mark.parametrize("M,N,a_mn,b_mn", [(128, 128, 0, 0), (128, 128, 0, 1), (128, 64, 0, 1)])
+def test_f16_instruction_descriptor(lib, M, N, a_mn, b_mn):
+    """Bit fields of the kind::f16 instruction descriptor with f16 operands, each read back by itself."""
+    x = fl.flamia_debug_mma_idesc(fl.MMA_F16, M, N, a_mn, b_mn)
+    field = lambda lo, hi: (x >> lo) & ((1 << (hi - lo + 1)) - 1)  # noqa: E731
+    assert field(0, 3) == 0 and field(6, 6) == 0 and field(13, 14) == 0
+    assert field(4, 5) == 1  # fp32 accumulator
+    assert field(7, 9) == 0 and field(10, 12) == 0  # f16, both operands
+    assert (field(15, 15), field(16, 16)) == (a_mn, b_mn)
+    assert field(17, 22) == N >> 3 and field(24, 28) == M >> 4 and field(23, 23) == 0 and field(29, 31) == 0
+    assert x == fl.flamia_debug_mma_idesc(fl.MMA_BF16, M, N, a_mn, b_mn) & ~0x1F80
+    with pytest.raises(fl.FlamiaError):
+        fl.flamia_debug_mma_idesc(fl.MMA_F16, M, N, a_mn, b_mn, 1, 0)
+
+
+def test_kernels_use_the_checked_f16_descriptors():
+    src = open(os.path.join(os.path.dirname(fl.__file__), "csrc", "paged_chunk.cu")).read()
+    assert set(re.findall(r"\bf16_idesc\([^()]*\)", src)) == {"f16_idesc(128, 128, 0, 0)", "f16_idesc(128, D, 0, 1)"}
 
 
 def test_paged_call_holds_the_pools_of_each_type():
