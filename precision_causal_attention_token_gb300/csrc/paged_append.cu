@@ -29,41 +29,67 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 // largest E2M1 value times the largest block scale), at least -127; 0 for 0.
 __device__ __forceinline__ int e2m1_row_exp(float amax) {
   const uint32_t b = __float_as_uint(amax);
-  if (b == 0u) return 0;
-  const int E = (int)(b >> 23);
-  return E == 0 ? -127 : max(-127, (b & 0x7FFFFFu) <= 0x280000u ? E - 138 : E - 137);
+  // a mantissa above that of 1.3125 (0x280000) carries into the exponent
+  const int e = max(-127, (int)((b + 0x57FFFFu) >> 23) - 138);
+  return b == 0u ? 0 : e;
 }
-// The smallest E4M3 value with 6 s >= bm (0 <= bm <= 2688), as its code and value.
-// RNE of bm / 6 is that value or the one below; 6 s is exact in fp32.
+// The smallest E4M3 value s with 6 s >= bm (0 <= bm <= 2688), as its code; 6 s is
+// exact in fp32.  Up from a little above bm / 6 to three bits behind the first,
+// and one back where that was too far; with subnormal values, from the nearest.
 __device__ __forceinline__ uint32_t e2m1_block_scale(float bm, float& s) {
+  if (bm >= 0.095f) {  // 6 * 2^-6 and a little
+    uint32_t b = (__float_as_uint(bm * 0.16666675f) + 0xFFFFFu) & 0xFFF00000u;  // (1 + 2^-21) / 6
+    if (6.f * __uint_as_float(b - 0x100000u) >= bm) b -= 0x100000u;
+    s = __uint_as_float(b);
+    return (b >> 20) - (120u << 3);
+  }
   uint32_t c = pack_e4m3x2(bm * (1.f / 6.f), 0.f) & 0xFFu;
   s = unpack_e4m3x2((uint16_t)c).x;
   if (6.f * s < bm) s = unpack_e4m3x2((uint16_t)++c).x;
   return c;
 }
-// Eight of a bf16 row's elements (or four of an fp32 one's) over their block
-// scale, rounded to E2M1.  The codes are those of the exact quotient.  fp32: a
-// rounded quotient never reaches a border between two codes that the exact one
-// misses (a border has at most 3 significant bits, the scale 4).  bf16: times
-// the rounded reciprocal, and the product rounded to 16 significant bits.
-// Quotients of an 8-bit by a 4-bit number lie on a border or 2^-9 of it away,
-// and the product is off by less than 2^-22, so the second rounding puts the
-// first kind on the border and moves no other over it.  (The division took 4
-// times the instructions.)
-template <bool BF16, int N>
-__device__ __forceinline__ uint32_t e2m1_codes(const float (&y)[N], float s) {
-  uint32_t c = 0;
-  if (s == 0.f) return c;
-  const float r = 1.f / s;
+// The E2M1 codes of a lane's elements f times inv over their block scale s: those
+// of the exact quotients.  A border between two codes has at most 3 significant
+// bits and the scale 4, so an element on a border has at most 7.
+// bf16 (8 elements): times a reciprocal, which is off by less than 2^-21, and
+// rounded to multiples of 2^-11 by adding 4096.  An 8-bit element that is not on
+// a border lies at least 2^-8 of it, so 2^-10, away: the rounding puts the
+// others on it and moves none over it.
+// fp32 (4 elements): the correctly rounded quotient, which reaches no border that
+// the exact one misses; from the correctly rounded reciprocal by one step on the
+// quotient's remainder (Markstein, Computation of elementary functions on the IBM
+// RISC System/6000 processor, 1990).
+template <bool BF16>
+__device__ __forceinline__ uint32_t e2m1_codes(const float (&f)[BF16 ? 8 : 4], float inv, float s) {
+  uint32_t c;
+  if constexpr (BF16) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    if (s == 0.f) r = 0.f;
+    const uint64_t inv2 = f2_pack(inv, inv), r2 = f2_pack(r, r), up = f2_pack(4096.f, 4096.f), down = f2_pack(-4096.f, -4096.f);
+    float q[8];
 #pragma unroll
-  for (int k = 0; k < N; k += 2) {
-    float q[2];
+    for (int k = 0; k < 8; k += 2) f2_unpack(f2_add(f2_fma(f2_mul(f2_pack(f[k], f[k + 1]), inv2), r2, up), down), q[k], q[k + 1]);
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(c) : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  } else {
+    const float r = s == 0.f ? 0.f : __frcp_rn(s);
+    const uint64_t r2 = f2_pack(r, r), s2 = f2_pack(-s, -s), inv2 = f2_pack(inv, inv);
+    float q[4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if constexpr (BF16) q[e] = __uint_as_float((__float_as_uint(y[k + e] * r) + 0x80u) & 0xFFFFFF00u);
-      else q[e] = __fdiv_rn(y[k + e], s);
+    for (int k = 0; k < 4; k += 2) {
+      const uint64_t y = f2_mul(f2_pack(f[k], f[k + 1]), inv2), q0 = f2_mul(y, r2);
+      f2_unpack(f2_fma(f2_fma(q0, s2, y), r2, q0), q[k], q[k + 1]);
     }
-    c |= pack_e2m1x2(q[0], q[1]) << (4 * k);
+    uint16_t h;
+    asm("{\n\t.reg .b8 a, b;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "mov.b16 %0, {a, b};\n\t}"
+        : "=h"(h) : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]));
+    c = h;
   }
   return c;
 }
@@ -102,6 +128,11 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParam
     const int64_t page = slot >> p.page_shift;
     const int at = (int)(slot & (p.page_size - 1));
     uint8_t* pool = (is_v ? p.v : p.k) + page * p.page_bytes;
+    // E2M1: this lane's places in the row of head h0; a head further is a page's length on
+    [[maybe_unused]] const int64_t row0 = E2M1 ? page * p.Hkv * p.page_size + (int64_t)h0 * p.page_size + at : 0;
+    [[maybe_unused]] uint8_t* codes4 = pool + ((int64_t)h0 * p.page_size + at) * (D / 2) + sub * (kEl / 2);
+    [[maybe_unused]] uint8_t* blocks4 = (is_v ? p.v_blocks : p.k_blocks) + row0 * (D / 16) + sub / kBlkLanes;
+    [[maybe_unused]] uint8_t* scales4 = (is_v ? p.v_scales : p.k_scales) + row0;
 #pragma unroll
     for (int u = 0; u < kHeads; ++u) {
       const bool write = slot >= 0 && h0 + u < p.Hkv;
@@ -131,21 +162,21 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParam
         }
         const bool finite = top < 0x7F800000u;
         const int e = !finite ? 0 : E2M1 ? e2m1_row_exp(__uint_as_float(top)) : noclamp_exp_clamped(__uint_as_float(top));
-        const float inv = exp2i(max(-e, -126));  // 2^-e; e = 127 does not occur
+        const float inv = E2M1 ? exp2i(-e) : exp2i(max(-e, -126));  // 2^-e; e = 127 does not occur (E2M1: nor does 118)
         if constexpr (E2M1) {
-          float y[kEl], s;
-#pragma unroll
-          for (int k = 0; k < kEl; k += 2) f2_unpack(f2_mul(f2_pack(f[k], f[k + 1]), f2_pack(inv, inv)), y[k], y[k + 1]);
-          uint32_t blk = finite ? e2m1_block_scale(__uint_as_float(top_blk) * inv, s) : 0u;
-          const uint32_t c = finite ? e2m1_codes<BF16>(y, s) : 0u;
+          float s;
+          uint32_t blk = e2m1_block_scale(__uint_as_float(top_blk) * inv, s);
+          uint32_t c = e2m1_codes<BF16>(f, inv, s);
+          if (!finite) blk = c = 0u;
           if (write) {
-            uint8_t* dst = pool + in_page * (D / 2) + sub * (kEl / 2);
-            if constexpr (kEl == 8) *reinterpret_cast<uint32_t*>(dst) = c;
-            else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)c;
-            const int64_t row = page * p.Hkv * p.page_size + in_page;
-            if (sub % kBlkLanes == 0) (is_v ? p.v_blocks : p.k_blocks)[row * (D / 16) + sub / kBlkLanes] = (uint8_t)blk;
-            if (sub == 0) (is_v ? p.v_scales : p.k_scales)[row] = (uint8_t)(finite ? e + 127 : 255);
+            if constexpr (kEl == 8) *reinterpret_cast<uint32_t*>(codes4) = c;
+            else *reinterpret_cast<uint16_t*>(codes4) = (uint16_t)c;
+            if (sub % kBlkLanes == 0) *blocks4 = (uint8_t)blk;
+            if (sub == 0) *scales4 = (uint8_t)(finite ? e + 127 : 255);
           }
+          codes4 += p.page_size * (D / 2);
+          blocks4 += p.page_size * (D / 16);
+          scales4 += p.page_size;
         } else {
           uint32_t c[kEl / 4];
 #pragma unroll
