@@ -341,11 +341,14 @@ def flamia_paged_copy(prob: Paged, src, dst, copies, n_copies, pages_ws, stream=
     n = len(src)
     if n == 0 or len(dst) != n:
         raise FlamiaError(ERR_INVALID_ARG, "flamia_paged_copy")
+    page, n_pages = (prob.Hkv, prob.page_size, prob.d, prob.cache_dtype), prob.n_pages
     for cache in src if dst is src else (*src, *dst):
-        _check_pool(prob, cache, "flamia_paged_copy")
+        pool = cache.pool
+        if pool is not None and (pool[0] != page or pool[1] < n_pages):
+            raise FlamiaError(ERR_INVALID_ARG, "flamia_paged_copy")
     _words("flamia_paged_copy", (copies, 0), (n_copies, 1))
-    a = (Cache * n)(*src)
-    b = a if dst is src else (Cache * n)(*dst)
+    a = (Cache * n).from_buffer_copy(b"".join(src))  # (Cache * n)(*src) takes three times as long
+    b = a if dst is src else (Cache * n).from_buffer_copy(b"".join(dst))
     _paged_call("flamia_paged_copy", pages_ws, stream, prob, n, a, b, copies.data_ptr(), copies.numel() // 2,
                 n_copies.data_ptr())
 

@@ -156,8 +156,7 @@ PagesLayout pages_layout(const flamia_paged_t& p) {
   size_t o = a256(L.pages + sizeof(PageRec) * (size_t)p.n_pages);
   L.staged = o; o = a256(o + table);
   L.freed = o; o = a256(o + table);
-  L.n_freed = o; o = a256(o + sizeof(int32_t) * p.n_req);
-  L.copy = o; o = a256(o + sizeof(int32_t) * p.n_req);
+  L.counts = o; o = a256(o + sizeof(int4) * p.n_req);
   L.total = o;
   return L;
 }
@@ -184,8 +183,7 @@ flamia_status_t fill_pages(const flamia_paged_t* p, void* pages_ws, size_t bytes
   a->pages = reinterpret_cast<PageRec*>(b + L.pages);
   a->staged = reinterpret_cast<int32_t*>(b + L.staged);
   a->freed = reinterpret_cast<int32_t*>(b + L.freed);
-  a->n_freed = reinterpret_cast<int32_t*>(b + L.n_freed);
-  a->copy = reinterpret_cast<int32_t*>(b + L.copy);
+  a->counts = reinterpret_cast<int4*>(b + L.counts);
   a->bits = reinterpret_cast<uint32_t*>(b + L.pages);
   a->rank = reinterpret_cast<int32_t*>(b + L.pages + 4 * (size_t)p->n_pages);
   return FLAMIA_OK;

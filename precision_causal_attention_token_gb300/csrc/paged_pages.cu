@@ -32,7 +32,7 @@ namespace flamia {
 namespace {
 
 constexpr int kThreads = kPagesThreads;
-constexpr int kSpinLimit = 1 << 23;  // of 64 ns or more each
+constexpr int kSpinLimit = 1 << 23;  // polls of 32 ns or more each, but for the first
 
 __device__ __forceinline__ int pages_of(int len, int shift) { return (len + (1 << shift) - 1) >> shift; }
 
@@ -49,7 +49,7 @@ __device__ bool grid_barrier(const PagesParams& p, uint32_t nth) {
     while (true) {
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(&p.hdr->arrived) : "memory");
       if (seen >= nth * gridDim.x || --left == 0) break;
-      __nanosleep(64);
+      if (left < kSpinLimit - 100) __nanosleep(32);
     }
     if (left == 0) report(&p.hdr->base, FLAMIA_ERR_TIMEOUT, 0x740);
     __threadfence();
@@ -101,9 +101,17 @@ __device__ __forceinline__ Row row_of(const PagesParams& p, int r) {
   x.write_at = q > 0 && (kept & (p.page_size - 1)) && kept < kv && at < x.keep ? at : -1;
   return x;
 }
+// One of the CTA's own rows (every gridDim.x-th), read once.
+struct __align__(16) OwnRow {
+  Row row;
+  int lost, held;  // the entries that it lets go of: [lost, held)
+  int copy, pad;
+};
 
-// smem: heir [n], taken [n + 1], given [n + 1], copied [n + 1]
-constexpr size_t share_smem(int n) { return (size_t)(4 * n + 4) * 4; }
+// smem: heir [n], taken [n], given [n + 1], copied [n] and, on a 16-byte border, the CTA's own rows
+constexpr size_t share_smem(int n, int ctas) {
+  return ((size_t)(4 * n + 1) * 4 + 15) / 16 * 16 + sizeof(OwnRow) * (size_t)((n + ctas - 1) / ctas);
+}
 
 __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesParams p) {
   extern __shared__ __align__(16) int32_t smi[];
@@ -112,8 +120,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
   const int n = p.n_req, mp = p.max_pages, tid = threadIdx.x, sh = p.page_shift;
   int32_t* heir = smi;  // the first row that continues a row; INT_MAX: none
   int32_t* taken = heir + n;
-  int32_t* given = taken + n + 1;
+  int32_t* given = taken + n;
   int32_t* copied = given + n + 1;
+  OwnRow* own = reinterpret_cast<OwnRow*>(smi + (4 * n + 1 + 3) / 4 * 4);
+  const int n_own = (n - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   const bool first = blockIdx.x == 0;
 
   auto give_up = [&](uint32_t why) {  // no page has moved
@@ -144,18 +154,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
     atomicOr(&p.hdr->bad, 1u);
     return false;
   };
-  // entries that row s lets go of: [x, y)
-  auto released = [&](int s, int& x, int& y) {
-    const int h = heir[s];
-    y = pages_of(p.old_len[s], sh);
-    x = h == INT_MAX ? 0 : min(y, row_of(p, h).keep);
-  };
+  for (int j = tid; j < n_own; j += kThreads) {
+    const int r = blockIdx.x + j * gridDim.x, h = heir[r];
+    OwnRow x;
+    x.row = row_of(p, r);
+    x.held = pages_of(p.old_len[r], sh);
+    x.lost = h == INT_MAX ? 0 : min(x.held, h == r ? x.row.keep : row_of(p, h).keep);
+    x.copy = x.pad = 0;
+    own[j] = x;
+  }
+  __syncthreads();
   // ------------------------------------------------ 1: holders gained and lost
-  for (int r = blockIdx.x; r < n; r += gridDim.x) {
-    const Row row = row_of(p, r);
+  for (int j = 0; j < n_own; ++j) {
+    const int r = blockIdx.x + j * gridDim.x;
+    const OwnRow& x = own[j];
+    const Row& row = x.row;
     if (row.src >= 0 && (row.src != r || heir[r] != r)) {
       const int32_t* from = p.block_table + (int64_t)row.src * mp;
       const bool more = heir[row.src] != r;
+#pragma unroll 4
       for (int k = tid; k < row.keep; k += kThreads) {
         const int id = from[k];
         if (row.src != r) p.staged[(int64_t)r * mp + k] = id;
@@ -169,9 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
         atomicMax(&p.pages[id].writer, n - r);
       }
     }
-    int x, y;
-    released(r, x, y);
-    for (int k = x + tid; k < y; k += kThreads) {
+#pragma unroll 4
+    for (int k = x.lost + tid; k < x.held; k += kThreads) {
       const int id = p.block_table[(int64_t)r * mp + k];
       if (page_ok(id)) {
         atomicAdd(&p.pages[id].delta, -1);
@@ -187,37 +203,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
     return PageRec{v.x, v.y, v.z, v.w};
   };
   uint32_t wrong = 0;  // counts that do not cover the tables' entries
-  for (int r = blockIdx.x; r < n; r += gridDim.x) {
-    if (tid == 0) {
-      const Row row = row_of(p, r);
-      int copy = 0;
-      if (row.write_at >= 0) {
-        const int id = p.block_table[(int64_t)row.src * mp + row.write_at];
-        const PageRec rec = rec_of(id);
-        const int total = p.refs[id] + rec.delta;
-        wrong |= total < rec.writers;
-        copy = !(total == rec.writers && rec.writer == n - r);
+  for (int j = tid; j < n_own; j += kThreads) {
+    const Row row = own[j].row;
+    if (row.write_at < 0) continue;
+    const int r = blockIdx.x + j * gridDim.x, id = p.block_table[(int64_t)row.src * mp + row.write_at];
+    const PageRec rec = rec_of(id);
+    const int total = p.refs[id] + rec.delta;
+    wrong |= total < rec.writers;
+    own[j].copy = !(total == rec.writers && rec.writer == n - r);
+  }
+  __syncthreads();
+  for (int j = 0; j < n_own; ++j) {
+    const int r = blockIdx.x + j * gridDim.x, x = own[j].lost, y = own[j].held;
+    int out = 0;
+    constexpr int kPer = 4;  // entries of a thread at a time, in table order
+    for (int k0 = x; k0 < y; k0 += kPer * kThreads) {
+      int id[kPer], mine = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int k = k0 + kPer * tid + i;
+        id[i] = k < y ? p.block_table[(int64_t)r * mp + k] : -1;
       }
-      p.copy[r] = copy;
-    }
-    int x, y, out = 0;
-    released(r, x, y);
-    for (int k0 = x; k0 < y; k0 += kThreads) {
-      const int k = k0 + tid;
-      int id = -1;
-      if (k < y) {
-        id = p.block_table[(int64_t)r * mp + k];
-        const PageRec rec = rec_of(id);
-        const int total = p.refs[id] + rec.delta;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (id[i] < 0) continue;
+        const PageRec rec = rec_of(id[i]);
+        const int total = p.refs[id[i]] + rec.delta;
         wrong |= total < 0;
-        if (total != 0 || rec.first != INT_MAX - (r * mp + k)) id = -1;
+        if (total != 0 || rec.first != INT_MAX - (r * mp + k0 + kPer * tid + i)) id[i] = -1;
+        mine += id[i] >= 0;
       }
       int all;
-      const int at = block_scan(id >= 0 ? 1 : 0, sm32, &all);
-      if (id >= 0) p.freed[(int64_t)r * mp + out + at] = id;
+      int at = out + block_scan(mine, sm32, &all);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (id[i] >= 0) p.freed[(int64_t)r * mp + at++] = id[i];
       out += all;
     }
-    if (tid == 0) p.n_freed[r] = out;
+    if (tid == 0) p.counts[r] = make_int4(max(0, own[j].row.need - own[j].row.keep) + own[j].copy, out, own[j].copy, 0);
   }
   if (wrong) atomicOr(&p.hdr->bad, 1u);
   if (!grid_barrier(p, 2)) return;
@@ -226,28 +249,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
   const int seg = (n + kThreads - 1) / kThreads, r0 = min(n, tid * seg), r1 = min(n, r0 + seg);
   int64_t mine = 0, sum, at;
   int mine_c = 0, n_copied;
-  auto taken_by = [&](int r, int& copy, int& free) {
-    const Row row = row_of(p, r);
-    copy = __ldcg(p.copy + r);
-    free = __ldcg(p.n_freed + r);
-    return max(0, row.need - row.keep) + copy;
-  };
   for (int r = r0; r < r1; ++r) {
-    int copy, free;
-    const int t = taken_by(r, copy, free);
-    mine += ((int64_t)t << 32) + free;
-    mine_c += copy;
+    const int4 c = __ldcg(p.counts + r);
+    mine += ((int64_t)c.x << 32) + c.y;
+    mine_c += c.z;
   }
   at = block_scan(mine, sm, &sum);
   int at_c = block_scan(mine_c, sm32, &n_copied);
   for (int r = r0; r < r1; ++r) {
-    int copy, free;
-    const int t = taken_by(r, copy, free);
+    const int4 c = __ldcg(p.counts + r);
     taken[r] = (int)(at >> 32);
     given[r] = (int)(at & 0xFFFFFFFF);
     copied[r] = at_c;
-    at += ((int64_t)t << 32) + free;
-    at_c += copy;
+    at += ((int64_t)c.x << 32) + c.y;
+    at_c += c.z;
   }
   const int64_t n_taken = sum >> 32, n_given = sum & 0xFFFFFFFF;
   if (tid == 0) given[n] = (int)n_given;
@@ -268,16 +283,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
     const int k = top - 1 - i;
     return k < n_free ? p.free_pages[k] : given_page(k - n_free);
   };
-  for (int r = blockIdx.x; r < n; r += gridDim.x) {
+  for (int j = 0; j < n_own; ++j) {
+    const int r = blockIdx.x + j * gridDim.x;
     int32_t* table = p.block_table + (int64_t)r * mp;
-    int x, y;
-    released(r, x, y);  // from the row's table as it was
-    for (int k = x + tid; k < y; k += kThreads) atomicAdd(p.refs + table[k], -1);
-    __syncthreads();
-    const Row row = row_of(p, r);
+    const Row row = own[j].row;
+    const int copy = own[j].copy;
+    if (own[j].lost < own[j].held) {  // from the row's table as it was
+#pragma unroll 4
+      for (int k = own[j].lost + tid; k < own[j].held; k += kThreads) atomicAdd(p.refs + table[k], -1);
+      __syncthreads();
+    }
     const bool moved = row.src >= 0 && row.src != r, more = row.src >= 0 && heir[row.src] != r;
-    const int copy = __ldcg(p.copy + r);
     if (moved || more || copy) {
+#pragma unroll 4
       for (int k = tid; k < row.keep; k += kThreads) {
         const bool mine = copy && k == row.write_at;
         if (!moved && !more && !mine) continue;
@@ -322,14 +340,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_compact_kernel(const PagesP
   int bad = 0;
   const int cap = mp << sh;
   for (int r = tid; r < n; r += kThreads) bad |= p.old_len[r] < 0 || p.old_len[r] > cap;
+  // pages of the CTA's own rows (every gridDim.x-th) and of those before each
+  extern __shared__ __align__(16) int64_t before_own[];
+  const int n_own = (n - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  for (int j = tid; j < n_own; j += kThreads) before_own[j + 1] = pages_of(max(0, p.old_len[blockIdx.x + j * gridDim.x]), sh);
+  if (tid == 0) before_own[0] = 0;
+  __syncthreads();
+  if (tid == 0)
+    for (int j = 0; j < n_own; ++j) before_own[j + 1] += before_own[j];
+  // use(entry) for all table entries of these rows, several on their way at a time
+  auto entries = [&](auto use) {
+    const int64_t all = before_own[n_own];
+#pragma unroll 4
+    for (int64_t i = tid; i < all; i += kThreads) {
+      int lo = 0, hi = n_own - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before_own[mid] <= i) lo = mid; else hi = mid - 1;
+      }
+      use(p.block_table + (int64_t)(blockIdx.x + lo * gridDim.x) * mp + (i - before_own[lo]));
+    }
+  };
   if (__syncthreads_or(bad)) return give_up(FLAMIA_ERR_BAD_SEQLENS);
   const int n_free = *p.n_free;
   if (n_free < 0 || n_free > p.n_pages) return give_up(FLAMIA_ERR_BAD_PAGE);
   const int used = p.n_pages - n_free;  // U
   // ------------------------------------------------ the free pages, each once
+#pragma unroll 4
   for (int64_t i = i0; i < n_free; i += step) {
     const int id = p.free_pages[i];
-    if ((unsigned)id >= (unsigned)p.n_pages || (atomicOr(&p.bits[id >> 5], 1u << (id & 31)) >> (id & 31) & 1u)) atomicOr(&p.hdr->bad, 1u);
+    if ((unsigned)id < (unsigned)p.n_pages) atomicOr(&p.bits[id >> 5], 1u << (id & 31));
+    else atomicOr(&p.hdr->bad, 1u);
   }
   if (!grid_barrier(p, 1)) return;
   // ------------------------------------------------ counts; the tables hold no free page
@@ -339,21 +380,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_compact_kernel(const PagesP
   for (int w = w0 + tid; w < w1; w += kThreads) mine += __popc(__ldcg(p.bits + w));
   block_scan(mine, sm32, &all);
   if (tid == 0) p.hdr->count[blockIdx.x] = all;
-  for (int r = blockIdx.x; r < n; r += gridDim.x) {
-    const int held = pages_of(p.old_len[r], sh);
-    for (int k = tid; k < held; k += kThreads) {
-      const int id = p.block_table[(int64_t)r * mp + k];
-      if ((unsigned)id >= (unsigned)p.n_pages || (__ldcg(p.bits + (id >> 5)) >> (id & 31) & 1u)) atomicOr(&p.hdr->bad, 1u);
-    }
-  }
+  int held_free = 0;
+  entries([&](const int32_t* at) {
+    const int id = *at;
+    held_free |= (unsigned)id >= (unsigned)p.n_pages || (__ldcg(p.bits + (id >> 5)) >> (id & 31) & 1u);
+  });
+  if (held_free) atomicOr(&p.hdr->bad, 1u);
   if (!grid_barrier(p, 2)) return;
   if (__ldcg(&p.hdr->bad)) return give_up(FLAMIA_ERR_BAD_PAGE);
   // ------------------------------------------------ ranks: F(x) = free pages before x
   // before: F of this CTA's first word; below: F(U)
   const int uw = used >> 5, last = uw / max(per, 1);  // U's word and the CTA whose part it is in (or behind all)
-  int v = 0, b = 0;
+  int v = 0, b = 0, c = 0;
   if (tid < gridDim.x) {
-    const int c = (int)__ldcg(&p.hdr->count[tid]);
+    c = (int)__ldcg(&p.hdr->count[tid]);
     if (tid < blockIdx.x) b = c;
     if (tid < last) v = c;
   }
@@ -361,20 +401,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_compact_kernel(const PagesP
     const uint32_t x = __ldcg(p.bits + w);
     v += __popc(w < uw ? x : x & ((1u << (used & 31)) - 1u));
   }
-  int before, below;
+  int before, below, distinct;
+  block_scan(c, sm32, &distinct);
+  if (distinct != n_free) return give_up(FLAMIA_ERR_BAD_PAGE);  // a page twice on the stack
   block_scan(b, sm32, &before);
   block_scan(v, sm32, &below);
+  __shared__ int f_word[kThreads];  // F of a word's first page
   for (int k0 = w0; k0 < w1; k0 += kThreads) {
     const int w = k0 + tid;
-    const uint32_t x = w < w1 ? __ldcg(p.bits + w) : 0u;
     int total;
-    const int f0 = before + block_scan(__popc(x), sm32, &total);
+    f_word[tid] = before + block_scan(w < w1 ? __popc(__ldcg(p.bits + w)) : 0, sm32, &total);
     before += total;
-    if (w >= w1) continue;
-    for (int i = 0; i < 32; ++i) {
-      const int id = 32 * w + i, f = f0 + __popc(x & ((1u << i) - 1u));
-      if (id >= p.n_pages) break;
-      if (x >> i & 1u) {
+    __syncthreads();
+    const int ids = min(32 * min(w1 - k0, kThreads), p.n_pages - 32 * k0);
+#pragma unroll 4
+    for (int i = tid; i < ids; i += kThreads) {  // a word a warp
+      const uint32_t x = __ldcg(p.bits + k0 + (i >> 5));
+      const int id = 32 * k0 + i, f = f_word[i >> 5] + __popc(x & ((1u << (i & 31)) - 1u));
+      if (x >> (i & 31) & 1u) {
         if (id < used) p.copies[2 * (int64_t)f + 1] = id;
       } else if (id >= used) {
         const int k = (id - used) - (f - below);
@@ -382,18 +426,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_compact_kernel(const PagesP
         p.rank[id] = k;
       }
     }
+    __syncthreads();
   }
   for (int64_t i = i0; i < n_free; i += step) p.free_pages[i] = p.n_pages - 1 - (int)i;
   if (first && tid == 0) *p.n_copies = below;
   if (!grid_barrier(p, 3)) return;
   // ------------------------------------------------ tables and counts follow
-  for (int r = blockIdx.x; r < n; r += gridDim.x) {
-    const int held = pages_of(p.old_len[r], sh);
-    for (int k = tid; k < held; k += kThreads) {
-      int32_t* at = p.block_table + (int64_t)r * mp + k;
-      if (*at >= used) *at = __ldcg(p.copies + 2 * (int64_t)__ldcg(p.rank + *at) + 1);
-    }
-  }
+  entries([&](int32_t* at) {
+    const int id = *at;
+    if (id >= used) *at = __ldcg(p.copies + 2 * (int64_t)__ldcg(p.rank + id) + 1);
+  });
   if (p.refs) {
     for (int64_t k = i0; k < below; k += step) {
       const int2 c = __ldcg(reinterpret_cast<const int2*>(p.copies) + k);
@@ -421,30 +463,32 @@ cudaError_t launch(K kernel, const PagesParams& p, int ctas, size_t smem, cudaSt
 }  // namespace
 
 cudaError_t launch_paged_share(const PagesParams& p, int sms, cudaStream_t st) {
+  int ctas = sms < kMaxPagesCtas ? sms : kMaxPagesCtas;
+  if (p.n_req < ctas) ctas = p.n_req;
+  const size_t smem = share_smem(p.n_req, ctas);
   static bool attr_set[64] = {};  // per device: raised once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(paged_share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)share_smem(kMaxReq));
+    e = cudaFuncSetAttribute(paged_share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)share_smem(kMaxReq, 128));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   e = cudaMemsetAsync(p.hdr, 0, sizeof(PagesHeader) + sizeof(PageRec) * (size_t)p.n_pages, st);
   if (e != cudaSuccess) return e;
-  int ctas = sms < kMaxPagesCtas ? sms : kMaxPagesCtas;
-  if (p.n_req < ctas) ctas = p.n_req;
-  return launch(paged_share_kernel, p, ctas, share_smem(p.n_req), st);
+  return launch(paged_share_kernel, p, ctas, smem, st);
 }
 
 cudaError_t launch_paged_compact(const PagesParams& p, int sms, cudaStream_t st) {
   const size_t words = ((size_t)p.n_pages + 31) / 32;
   cudaError_t e = cudaMemsetAsync(p.hdr, 0, sizeof(PagesHeader) + 4 * words, st);
   if (e != cudaSuccess) return e;
-  int ctas = sms < kMaxPagesCtas ? sms : kMaxPagesCtas;
-  const int64_t work = (int64_t)p.n_pages / kThreads + 1 > p.n_req ? (int64_t)p.n_pages / kThreads + 1 : p.n_req;
-  if (work < ctas) ctas = (int)work;
-  return launch(paged_compact_kernel, p, ctas, 0, st);
+  int64_t ctas = p.n_pages / kThreads + 1;
+  if (ctas < p.n_req) ctas = p.n_req;
+  if (ctas > sms) ctas = sms;
+  if (ctas > kMaxPagesCtas) ctas = kMaxPagesCtas;
+  return launch(paged_compact_kernel, p, (int)ctas, sizeof(int64_t) * (size_t)((p.n_req + ctas - 1) / ctas + 1), st);
 }
 
 }  // namespace flamia

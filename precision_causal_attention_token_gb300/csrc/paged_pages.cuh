@@ -27,7 +27,7 @@ struct __align__(16) PageRec {
 static_assert(sizeof(PageRec) == 16, "one sector for two");
 
 struct PagesLayout {
-  size_t header, pages, staged, freed, n_freed, copy, total;
+  size_t header, pages, staged, freed, counts, total;
 };
 
 struct PagesParams {
@@ -47,8 +47,7 @@ struct PagesParams {
   PageRec* pages;          // [n_pages]
   int32_t* staged;         // [n_req][max_pages] pages that a row takes over from another's
   int32_t* freed;          // [n_req][max_pages] pages without a holder, by the row that let go of them first
-  int32_t* n_freed;        // [n_req]
-  int32_t* copy;           // [n_req] whether the row's partly filled page is replaced by a copy
+  int4* counts;            // [n_req] pages that the row takes, its freed ones, whether its partly filled one is copied
   // compact, in the place of `pages`
   uint32_t* bits;          // free pages
   int32_t* rank;           // [n_pages] of the pages that move
