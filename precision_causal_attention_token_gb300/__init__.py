@@ -66,6 +66,7 @@ class Cache(ctypes.Structure):
                 ("v_scales", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("k_blocks", ctypes.c_void_p),
                 ("v_blocks", ctypes.c_void_p)]
     pool = None  # (Hkv, page_size, d, cache_dtype), n_pages of the tensors that paged_cache was given
+    device = -1  # and where they are
 
 
 _lib = None
@@ -282,6 +283,7 @@ def paged_cache(k, v, k_scales=None, v_scales=None, k_blocks=None, v_blocks=None
     cache = Cache(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), 2 * stride if e2m1 else stride, _ptr(k_blocks),
                   _ptr(v_blocks))
     dtype = E2M1 if e2m1 else {torch.bfloat16: BF16, torch.uint8: E4M3, torch.float8_e4m3fn: E4M3}.get(k.dtype)
+    cache.device = k.get_device()
     cache.pool = (*k.shape[1:3], k.shape[3] * (2 if e2m1 else 1), dtype), k.shape[0]
     return cache
 
@@ -317,11 +319,11 @@ def flamia_paged_pages_workspace_size(prob: Paged) -> int:
     return int(load_library().flamia_paged_pages_workspace_size(ctypes.byref(prob)))
 
 
-def _words(where, *pairs):
-    """int32 tensors of at least so many words in a row (None passes)."""
+def _words(where, device, *pairs):
+    """int32 tensors of at least so many words in a row on the device (None passes)."""
     import torch
     for t, n in pairs:
-        if t is not None and (t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous()):
+        if t is not None and (t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous() or t.get_device() != device):
             raise FlamiaError(ERR_INVALID_ARG, where)
 
 
@@ -329,8 +331,10 @@ def flamia_paged_plan_shared(prob: Paged, ws, pages_ws, slot_map, src, old_len, 
                              n_copies, stream=None):
     """Once per step of requests that share pages: forks (src), counts, copies on write, then as flamia_paged_plan.
     copies [n_req, 2] and n_copies list the pages that flamia_paged_copy must copy before anything is appended."""
-    _words("flamia_paged_plan_shared", (slot_map, prob.T), (src, prob.n_req), (old_len, prob.n_req), (refs, prob.n_pages),
+    _words("flamia_paged_plan_shared", ws.get_device(), (slot_map, prob.T), (src, prob.n_req), (old_len, prob.n_req), (refs, prob.n_pages),
            (free_pages, prob.n_pages), (n_free, 1), (n_free_out, 1), (copies, 2 * prob.n_req), (n_copies, 1))
+    if pages_ws.get_device() != ws.get_device():
+        raise FlamiaError(ERR_INVALID_ARG, "flamia_paged_plan_shared")
     _paged_call("flamia_paged_plan_shared", ws, stream, prob, _ptr(slot_map), _ptr(src), _ptr(old_len), _ptr(refs),
                 _ptr(free_pages), _ptr(n_free), _ptr(n_free_out), _ptr(copies), _ptr(n_copies), pages_ws.data_ptr(),
                 pages_ws.nbytes)
@@ -341,12 +345,12 @@ def flamia_paged_copy(prob: Paged, src, dst, copies, n_copies, pages_ws, stream=
     n = len(src)
     if n == 0 or len(dst) != n:
         raise FlamiaError(ERR_INVALID_ARG, "flamia_paged_copy")
-    page, n_pages = (prob.Hkv, prob.page_size, prob.d, prob.cache_dtype), prob.n_pages
+    page, n_pages, device = (prob.Hkv, prob.page_size, prob.d, prob.cache_dtype), prob.n_pages, pages_ws.get_device()
     for cache in src if dst is src else (*src, *dst):
         pool = cache.pool
-        if pool is not None and (pool[0] != page or pool[1] < n_pages):
+        if pool is not None and (pool[0] != page or pool[1] < n_pages or cache.device != device):
             raise FlamiaError(ERR_INVALID_ARG, "flamia_paged_copy")
-    _words("flamia_paged_copy", (copies, 0), (n_copies, 1))
+    _words("flamia_paged_copy", device, (copies, 0), (n_copies, 1))
     a = (Cache * n).from_buffer_copy(b"".join(src))  # (Cache * n)(*src) takes three times as long
     b = a if dst is src else (Cache * n).from_buffer_copy(b"".join(dst))
     _paged_call("flamia_paged_copy", pages_ws, stream, prob, n, a, b, copies.data_ptr(), copies.numel() // 2,
@@ -356,7 +360,7 @@ def flamia_paged_copy(prob: Paged, src, dst, copies, n_copies, pages_ws, stream=
 def flamia_paged_compact(prob: Paged, pages_ws, length, refs, free_pages, n_free, copies, n_copies, stream=None):
     """The pages in use to the low end of the pool: tables, counts (refs may be None) and stack rewritten, the moves
     listed in copies [n_pages, 2] and n_copies for flamia_paged_copy."""
-    _words("flamia_paged_compact", (length, prob.n_req), (refs, prob.n_pages), (free_pages, prob.n_pages), (n_free, 1),
+    _words("flamia_paged_compact", pages_ws.get_device(), (length, prob.n_req), (refs, prob.n_pages), (free_pages, prob.n_pages), (n_free, 1),
            (copies, 2 * prob.n_pages), (n_copies, 1))
     _paged_call("flamia_paged_compact", pages_ws, stream, prob, _ptr(length), _ptr(refs), _ptr(free_pages), _ptr(n_free),
                 _ptr(copies), _ptr(n_copies))

@@ -37,7 +37,8 @@ constexpr int kSpinLimit = 1 << 23;  // polls of 32 ns or more each, but for the
 __device__ __forceinline__ int pages_of(int len, int shift) { return (len + (1 << shift) - 1) >> shift; }
 
 // All CTAs of the launch (they are resident together); `nth` counts a launch's
-// barriers from 1.  False, for the whole CTA, where the wait ran out.
+// barriers from 1.  False, for the whole CTA, where the wait ran out (a CTA that
+// comes to the barrier later finds `bad` set).
 __device__ bool grid_barrier(const PagesParams& p, uint32_t nth) {
   __shared__ int sm_ok;
   __syncthreads();
@@ -51,7 +52,13 @@ __device__ bool grid_barrier(const PagesParams& p, uint32_t nth) {
       if (seen >= nth * gridDim.x || --left == 0) break;
       if (left < kSpinLimit - 100) __nanosleep(32);
     }
-    if (left == 0) report(&p.hdr->base, FLAMIA_ERR_TIMEOUT, 0x740);
+    if (left == 0) {  // no page moves, and what follows on the stream has nothing to do
+      report(&p.hdr->base, FLAMIA_ERR_TIMEOUT, 0x740);
+      p.hdr->fail = FLAMIA_ERR_TIMEOUT;
+      atomicOr(&p.hdr->bad, 1u);
+      if (p.n_free_out) *p.n_free_out = *p.n_free;
+      *p.n_copies = 0;
+    }
     __threadfence();
     sm_ok = left > 0;
   }

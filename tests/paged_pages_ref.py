@@ -20,12 +20,11 @@ class Pool:
         ps, n = self.ps, len(q)
         old = [row[:] for row in self.table]
         keep = [min(up(self.held[s], ps), up(max(0, kv[r] - q[r]), ps)) if s >= 0 else 0 for r, s in enumerate(src)]
-        total, seen = self.refs[:], []
+        total, seen = self.refs[:], {}
         for r in range(n):
             for page in old[r][:up(self.held[r], ps)]:
                 total[page] -= 1
-                if page not in seen:
-                    seen.append(page)
+                seen.setdefault(page)
         rows = [old[src[r]][:keep[r]] if src[r] >= 0 else [] for r in range(n)]
         for row in rows:
             for page in row:

@@ -109,7 +109,7 @@ def test_drafted_tokens(causal, H, Hkv, d, ps, max_q):
 
 
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("H,Hkv,d,ps", [(2, 1, 128, 16), (4, 4, 64, 32), (10, 2, 128, 64), (3, 1, 64, 128)])
+@pytest.mark.parametrize("H,Hkv,d,ps", [(2, 1, 128, 16), (4, 4, 64, 32), (10, 2, 128, 64), (3, 1, 64, 128), (12, 1, 128, 32), (34, 2, 64, 16)])
 @pytest.mark.parametrize("q,kv", [([300], [300]), ([129, 1, 70], [500, 333, 70]), ([64, 200, 5, 1], [1000, 210, 3, 0]), ([257, 33], [2000, 40])])
 def test_chunks_and_mixed(causal, H, Hkv, d, ps, q, kv):
     Step4(q, kv, H=H, Hkv=Hkv, d=d, ps=ps, causal=causal, pad=5, poison=True, seed=sum(q)).check()

@@ -111,6 +111,53 @@ def test_steps_follow_the_model(n, pages, cols, ps, max_q, beams):
     assert refused or n != 17
 
 
+def test_as_many_requests_as_there_can_be():
+    """8,192 requests, most continued by others or ended, in two steps."""
+    n, r = 8192, random.Random(9)
+    m = Pool(n, 40000, 4, 16)
+    gpu = Gpu(m, n, 4 * n, 4)
+    q, kv = [1 + i % 4 for i in range(n)], [20 + i % 29 if i % 5 else 3 for i in range(n)]
+    q = [min(a, b) for a, b in zip(q, kv)]
+    for src in (list(range(n)), [r.randrange(-1, n) if i % 3 else i for i in range(n)]):
+        if m.held != [0] * n:
+            kv = [(m.held[s] if s >= 0 else 0) + a for s, a in zip(src, q)]
+        gpu.inputs(q, kv, src, m.held)
+        seen = m.step(q, kv, src)
+        assert gpu.step() == fl.OK
+        gpu.same(seen)
+        assert gpu.slots.tolist() == m.slots(q, kv, 4 * n)
+    gpu.old.copy_(torch.tensor(m.held, dtype=torch.int32))
+    moves = m.compact()
+    assert gpu.compact() == fl.OK
+    gpu.same(moves)
+
+
+def test_two_streams_at_once():
+    """Steps and compactions on two streams with buffers of their own, launched side by side."""
+    r = random.Random(4)
+    sets = []
+    for i in range(2):
+        m = Pool(700, 9000, 12, 16)
+        sets.append((m, Gpu(m, 700, 700 * 8, 8), torch.cuda.Stream()))
+    for it in range(12):
+        want = []
+        for m, gpu, stream in sets:
+            q, kv, src = _random_step(r, m, 700, 700 * 8, 8, True)
+            gpu.inputs(q, kv, src, m.held)
+            want.append((m.step(q, kv, src), q, kv))
+            assert want[-1][0] is not None
+        torch.cuda.synchronize()
+        for m, gpu, stream in sets:
+            with torch.cuda.stream(stream):
+                fl.flamia_paged_plan_shared(gpu.prob, gpu.ws, gpu.pages_ws, gpu.slots, gpu.src, gpu.old, gpu.refs, gpu.free, gpu.n_free,
+                                            gpu.n_free, gpu.copies, gpu.n_copies)
+        torch.cuda.synchronize()
+        for (m, gpu, stream), (copies, q, kv) in zip(sets, want):
+            assert fl.flamia_get_device_status(gpu.ws) == fl.OK
+            gpu.same(copies)
+            assert gpu.slots.tolist() == m.slots(q, kv, 700 * 8)
+
+
 def test_without_sources_each_continues_itself():
     m, T = Pool(2, 9, 4, 16), 30
     gpu = Gpu(m, 2, T)

@@ -96,9 +96,30 @@ def test_binding_checks_the_arrays(monkeypatch):
     pool = torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16)
     c, small = fl.paged_cache(pool, pool.clone()), fl.paged_cache(pool[:7], pool[:7])
     fl.flamia_paged_copy(p, [c, c], [c, c], i(3, 2), i(1), ws)
-    for src, dst in (([c], [c, c]), ([], []), ([c], [small]), ([small], [c])):
+    away = fl.paged_cache(pool.to("meta"), pool.to("meta"))
+    away.device = 1  # as of a pool on another GPU
+    for src, dst in (([c], [c, c]), ([], []), ([c], [small]), ([small], [c]), ([away], [c]), ([c], [away])):
         with pytest.raises(fl.FlamiaError):
             fl.flamia_paged_copy(p, src, dst, i(3, 2), i(1), ws)
+
+    class Away:  # a tensor of another GPU
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def get_device(self):
+            return 1
+
+    for k in share:
+        with pytest.raises(fl.FlamiaError):
+            fl.flamia_paged_plan_shared(p, ws, ws, **{**share, k: Away(share[k])})
+    with pytest.raises(fl.FlamiaError):
+        fl.flamia_paged_plan_shared(p, ws, Away(ws), **share)
+    for k in comp:
+        with pytest.raises(fl.FlamiaError):
+            fl.flamia_paged_compact(p, ws, **{**comp, k: Away(comp[k])})
     assert calls == ["flamia_paged_plan_shared"] * 2 + ["flamia_paged_compact"] * 2 + ["flamia_paged_copy"]
 
 
