@@ -3,10 +3,14 @@
 // A row (token, key/value head) is read by a group of lanes, 16 bytes a lane,
 // and written as one contiguous run of its page: rounded to bf16, as E4M3
 // codes with the row's own no-clamp exponent, whose maximum the group forms by
-// shuffles, or as E2M1 codes with an E4M3 scale for each 16 channels (the
-// maximum of two or four lanes) under the row's exponent.  Every byte is read and written once; HBM bound at large sizes, a
-// launch's latency at small ones: 46 us for 46,806 tokens of 8 heads x 128 from
-// bf16 to E4M3 (289 MB, 6.3 TB/s), 2.6 us for 65.  A CTA takes a few consecutive tokens and
+// shuffles, or as E2M1 codes with an E4M3 scale for each 16 channels under the
+// row's exponent (32 bytes a lane).  Every byte is read and written once; HBM
+// bound at large sizes, a launch's latency at small ones: 46 us for 46,806
+// tokens of 8 heads x 128 from bf16 to E4M3 (289 MB, 6.3 TB/s), 2.6 us for 65;
+// to E2M1 35 us for 40,900 tokens (221 MB, 6.4 TB/s; from fp32 5.8), 17 us for
+// 17,900 (5.6), 4.6 us for 67, and there the instructions count almost as much
+// (71% of the issue slots; with a division an element and 16 bytes a lane it
+// took 73 us for 40,900).  A CTA takes a few consecutive tokens and
 // heads at a time, so that what it reads is contiguous (tokens of all heads)
 // and so is what it writes (a head's tokens: with a token's rows in a row
 // instead, the stores came in 128-byte pieces and the same call took 83 us); a

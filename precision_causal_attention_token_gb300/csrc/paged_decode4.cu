@@ -19,6 +19,14 @@
 // Scales of queries and keys, f16 weights relative to the largest exponent of
 // V and the careful second pass (bf16 values, two bf16 terms a weight) where
 // exponents lie more than kSpread apart: as for E4M3, see paged_decode.cu.
+//
+// Measured (152 SMs, H = 32, Hkv = 8, d = 128): 64 requests, 281,000 tokens, 80 us
+// (4.1 TB/s, 61% of the copy rate; the E4M3 kernel 109 us for 1.76 times the
+// bytes; its own code with E2M1 operands took 104); one request of 65,522 tokens
+// 29 us; 32 requests of 2 to 4 drafted tokens 70 us, 16 of 2 to 8 (32 rows) 66.
+// Of a long tile's 113,000 cycles of loop, the loads alone take 95,000 and the
+// instructions alone 97,000; 6 us go by before a CTA's first chunk is there and
+// 3 to 4 with each tile's join.  With d = 64: 55 us for 166 MB.
 #include <type_traits>
 
 #include "paged_decode.cuh"
