@@ -365,7 +365,8 @@ flamia_status_t flamia_plan_noalloc(const flamia_problem_t* p, int2* fwd_items, 
  *               reads as NaN.  (A NaN code 0x7F or 0xFF under any other byte is
  *               not written by flamia_paged_append and must not occur.)
  *   blocks      [n_pages][Hkv][page_size][d/16]  E2M1 only: the E4M3 scale of
- *               each 16 channels of a row, not negative: the value is
+ *               each 16 channels of a row, not negative and (but under byte
+ *               255) not the NaN code 0x7F: the value is
  *               code * block scale * 2^(byte - 127).  The exponent is a power of
  *               two, unlike gscale4 of flamia_operand_t, so that a value keeps
  *               at most six significant bits and is exact in bf16 and f16.

@@ -89,6 +89,43 @@ def test_appended_rows_at_borders(dtype):
         _same_rows(c, packed(wc), "codes")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,Hkv", [(64, 3), (128, 5), (64, 9)])
+def test_append_from_a_fused_projection_into_chosen_slots(dtype, d, Hkv):
+    """Rows at a stride, K and V of one buffer; slots in any order, skipped ones, one outside the pool (reported)."""
+    T, ps, n, i32 = 45, 32, 7, dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(d)
+    width = (4 * Hkv + 2 * Hkv) * d
+    rows = torch.randn(T, width, generator=g).to(dtype).cuda()
+    k, v = rows[:, 4 * Hkv * d:5 * Hkv * d], rows[:, 5 * Hkv * d:]
+    cu, kv, table = torch.tensor([0, T], **i32), torch.tensor([T], **i32), torch.zeros(1, 4, **i32)
+    prob = fl.make_paged(T, 4 * Hkv, Hkv, d, cu, kv, table, page_size=ps, n_pages=n, cache_dtype=fl.E2M1, kv_stride=width,
+                         in_dtype=fl.F32 if dtype == torch.float32 else fl.BF16)
+    ws = torch.zeros(fl.flamia_paged_workspace_size(prob), dtype=torch.uint8, device="cuda")
+    fl.flamia_paged_plan(prob, ws)
+    slots = torch.randperm(n * ps, generator=g)[:T].int()
+    slots[::7] = -1
+    bad = slots.clone()
+    bad[10], bad[11] = n * ps, -2
+    pools = [torch.full((n, Hkv, ps, w), 0xEE, dtype=torch.uint8, device="cuda") for w in (d // 2, d // 2, 1, 1, d // 16, d // 16)]
+    cache = fl.paged_cache(pools[0], pools[1], pools[2][..., 0], pools[3][..., 0], pools[4], pools[5])
+    for s, status in ((slots, fl.OK), (bad, fl.ERR_BAD_PAGE)):
+        for x in pools:
+            x.fill_(0xEE)
+        fl.flamia_paged_append(prob, k, v, s.cuda(), cache, ws)
+        assert fl.flamia_get_device_status(ws) == status
+        for x, (c, b, e) in ((k, (0, 4, 2)), (v, (1, 5, 3))):
+            wc, wb, we = quantize4(x.reshape(T, Hkv, d).cpu())
+            flat = [pools[i].transpose(1, 2).reshape(n * ps, Hkv, -1).cpu() for i in (c, b, e)]
+            live = (s >= 0) & (s < n * ps)
+            at = s[live].long()
+            _same_rows(flat[0][at], packed(wc)[live], "codes")
+            assert torch.equal(flat[1][at], wb[live]) and torch.equal(flat[2][at][..., 0], we[live])
+            rest = torch.ones(n * ps, dtype=torch.bool)
+            rest[at] = False
+            assert all((y[rest] == 0xEE).all() for y in flat)
+
+
 LENS = {  # (new tokens, cached after them)
     "one": ([1], [1]), "first": ([1, 1, 1], [1, 16, 17]), "decode": ([1] * 7, [3, 64, 65, 200, 1000, 1, 257]),
     "idle": ([1, 0, 1, 1], [0, 40, 33, 0]), "long": ([1], [9000]), "many": ([1] * 40, [37 * i % 300 + 1 for i in range(40)])}
