@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
   OwnRow* own = reinterpret_cast<OwnRow*>(smi + (4 * n + 1 + 3) / 4 * 4);
   const int n_own = (n - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   const bool first = blockIdx.x == 0;
+  // the plan that follows reads its lengths meanwhile and waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;");
 
   auto give_up = [&](uint32_t why) {  // no page has moved
     if (first && tid == 0) {

@@ -282,6 +282,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     }
   }
   bad = __syncthreads_or(bad);
+  // launched while the page management before it may still run (p.before): its
+  // verdict and the tables come after this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   uint32_t why = bad ? FLAMIA_ERR_BAD_SEQLENS : p.before ? *p.before : (uint32_t)FLAMIA_OK;
   int n_free = 0, n_taken = 0, n_given = 0;
   if (manage && !bad) {
@@ -376,8 +379,17 @@ cudaError_t launch_paged_plan(const PagedParams& p, cudaStream_t st) {
     if (p.old_len && helpers < (p.n_req + 31) / 32) helpers = (p.n_req + 31) / 32;
     helpers = helpers < 1 ? 1 : helpers > 151 ? 151 : helpers;
   }
-  paged_plan_kernel<<<1 + helpers, kPlanThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1 + helpers);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = p.before ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_plan_kernel, p);
 }
 
 }  // namespace flamia
