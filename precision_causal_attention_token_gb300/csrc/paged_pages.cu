@@ -255,10 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
     }
     if (tid == 0) p.counts[r] = make_int4(max(0, own[j].row.need - own[j].row.keep) + own[j].copy, out, own[j].copy, 0);
   }
-  if (wrong) atomicOr(&p.hdr->bad, 1u);
+  if (wrong) atomicOr(&p.hdr->wrong, 1u);
   if (!grid_barrier(p, 2)) return;
   // ------------------------------------------------ 3: where each row's pages come from and go to
-  if (__ldcg(&p.hdr->bad)) return give_up(FLAMIA_ERR_BAD_PAGE);
+  if (__ldcg(&p.hdr->bad) || __ldcg(&p.hdr->wrong)) return give_up(FLAMIA_ERR_BAD_PAGE);
   const int seg = (n + kThreads - 1) / kThreads, r0 = min(n, tid * seg), r1 = min(n, r0 + seg);
   int64_t mine = 0, sum, at;
   int mine_c = 0, n_copied;

@@ -237,6 +237,24 @@ def test_bad_steps_move_nothing(name, what, status):
     assert (pool == 3).all() and (O == 9).all() and (lse == 9).all()
 
 
+def test_counts_that_fall_short_end_every_cta_alike():
+    """One CTA finds them while others may still be leaving the barrier before: none may wait for those that left."""
+    n = 150
+    m = Pool(n, 900, 6, 16)
+    gpu = Gpu(m, n, 64 * n, 64)
+    q = kv = [20 + i % 40 for i in range(n)]
+    m.step(q, kv, list(range(n)))
+    gpu.inputs(q, kv, list(range(n)), [0] * n)
+    assert gpu.step() == fl.OK
+    gpu.inputs([1] * n, [k + 1 for k in kv], list(range(n)), m.held)
+    table = gpu.table.clone()
+    for i in [i for i in range(300) if kv[i % n] % 16]:  # at a page's border a row reads no count
+        gpu.refs.copy_(torch.tensor(m.refs, dtype=torch.int32))
+        gpu.refs[int(gpu.table[i % n, kv[i % n] // 16])] = 0
+        assert gpu.step() == fl.ERR_BAD_PAGE == fl.flamia_get_device_status(gpu.pages_ws)
+    assert torch.equal(gpu.table, table) and int(gpu.n_free) == len(m.free) and int(gpu.n_copies) == 0
+
+
 @pytest.mark.parametrize("what,status", [
     (lambda g: _set(g.old, 0, -1), fl.ERR_BAD_SEQLENS), (lambda g: _set(g.old, 0, 65), fl.ERR_BAD_SEQLENS),
     (lambda g: _set(g.n_free, 0, 13), fl.ERR_BAD_PAGE), (lambda g: _set(g.n_free, 0, -1), fl.ERR_BAD_PAGE),
