@@ -562,20 +562,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (in && keys >= kChunkBlk) {
-            // Two rows' loads before their stores, which they could not pass (the compiler
-            // does not know that they are apart).  Rolled: with the code of more rows the
-            // roles outgrow the instruction cache (four and eight 4,096: 320, 339 us; two: 308).
+            // Four rows' loads before their stores, which they could not pass (the compiler
+            // does not know that they are apart).  Rolled: the code of more rows
+            // pushes the other roles' out of the instruction cache (2,048 over 32,768 and
+            // four times 4,096: two rows 882 and 286 us, four 863 and 291, eight 863 and 303).
 #pragma unroll 1
-            for (int i0 = 0; i0 < kCh; i0 += 2) {
-              uint2 x[2];
-              uint32_t fac[2];
+            for (int i0 = 0; i0 < kCh; i0 += 4) {
+              uint2 x[4];
+              uint32_t fac[4];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
+              for (int i = 0; i < 4; ++i) {
                 x[i] = *reinterpret_cast<const uint2*>(src + (i0 + i) * kStep * C::kCodeB);
                 fac[i] = factor(blk[(i0 + i) * kStep * C::kBlkB], exps[(i0 + i) * kStep]);
               }
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
+              for (int i = 0; i < 4; ++i) {
                 uint32_t y[8];
                 to_f16(x[i], fac[i], y);
                 put(i0 + i, y);
@@ -934,14 +935,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             out[j / 2] = C::kFp4 ? pack_f16x2(a0, a1) : pack_bf16x2(a0, a1);
           }
         };
-        uint32_t w0[32];
-        weights(s0, w0);
-        weights(s1, w0 + 16);
-        tmem_st32(ts, w0);
-        uint32_t w1[32];
-        weights(s2, w1);
-        weights(s3, w1 + 16);
-        tmem_st32(ts + 32, w1);
+        if constexpr (C::kFp4) {
+          // Half the code, for a second read of the second half: the roles share the
+          // instruction cache (2,048 over 32,768 and four times 4,096 875 -> 863 and
+          // 308 -> 291 us; quarters 937 and 294 with two rows a loader's step, the
+          // read on its way meanwhile 923 and 296).
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w0[16], w1[16];
+            if (q) {
+              tmem_ld32(ts + 64, s0);
+              tmem_ld32(ts + 96, s1);
+              tmem_ld_wait_regs(s0, s1);
+            }
+            weights(s0, w0);
+            tmem_st16(ts + 32 * q, w0);
+            weights(s1, w1);
+            tmem_st16(ts + 32 * q + 16, w1);
+          }
+        } else {
+          uint32_t w0[32];
+          weights(s0, w0);
+          weights(s1, w0 + 16);
+          tmem_st32(ts, w0);
+          uint32_t w1[32];
+          weights(s2, w1);
+          weights(s3, w1 + 16);
+          tmem_st32(ts + 32, w1);
+        }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&c.p_full[hf]);
