@@ -588,7 +588,9 @@ flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, cons
  *   chunk kernel, E2M1            f16, 2^-11, and below that at most 2^-25 of
  *                                 the row's largest weight; bf16 in blocks of
  *                                 128 keys where a V row's scale byte is not
- *                                 112 to 127
+ *                                 112 to 127, and from one with a byte of 192
+ *                                 or more (V of 2^66 or more) on for the rest
+ *                                 of the tile, where V is exact down to 2^-118
  *   decode kernel, bf16 cache     two bf16 terms, 2^-16
  *   decode kernel, E4M3 or E2M1   f16, 2^-11, and below that at most 2^-20 of
  *                                 the row's largest weight; two bf16 terms

@@ -50,7 +50,11 @@
 // are held 16 times themselves.  The loaders turn the queries into f16, with a
 // power of two a row.  A block with other rows: K goes without its rows' exponents
 // and the softmax warps multiply them into the scores; V, and the weights with it,
-// as bf16.  2,048 over 32,768 took 905 us when each row's scale was read after the
+// as bf16.  Accumulators that are 16 times the sums would overflow from V of 2^124 on,
+// and 0 x inf would reach the rows that do not see such a key.  So from a block on
+// whose V has a byte of kWideByte or more, V of the tile is held 2^-8 times itself, in
+// bf16, under weights of at most 1: two hundred of the largest rows add up.
+// 2,048 over 32,768 took 905 us when each row's scale was read after the
 // stores of the row before.
 #include <climits>
 #include <type_traits>
@@ -115,7 +119,12 @@ struct __align__(16) Ctl {
 // E2M1: that the queries as f16 are there; per row (of four fragments in turn)
 // the exponent field E of its largest element, which the f16 row holds times
 // 2^(139 - E); per key block (of four in turn) whether K lacks its rows'
-// exponents, which are then beside it, and whether V, and so the weights, are bf16.
+// exponents, which are then beside it, and what V is: 0 f16, 1 bf16 (and so the
+// weights), 2 bf16 and wide.  Below kWideByte V is below 2^77: 2^4 times that, weights
+// up to 2^8 (and 2^25 keys) stay far below 2^128.
+constexpr uint32_t kWideByte = 192;
+static_assert(kWideByte == 0xC0, "told by the two upper bits of a byte");
+constexpr float kUnit4 = 0x1p-4f, kUnitWide = 0x1p8f;  // O in units of the accumulators
 struct __align__(16) Ctl4 {
   uint64_t q_ready[2];
   uint8_t q_exp[4][2][128];
@@ -504,7 +513,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lt = tid - 256;
     uint32_t it = 0;
     [[maybe_unused]] uint32_t q_uses[2] = {0, 0};
-    [[maybe_unused]] bool v_in = true;  // E2M1: V of the present block can be f16
     bool ok = true;
     Frag f;
     for (uint32_t n = 0; ok && next_frag(n, f, ok, 0x80a); ++n) {
@@ -515,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lt == 0) c.odd_key[(n + 4) % 8] = INT_MAX;
       int* odd_key = &c.odd_key[n % 8];
       if constexpr (C::kFp4) {
+        int v_kind = 0;  // odd_v of the present block; 2 stays to the fragment's end
         for (int b = 0; ok && b < 2 * f.load; ++b, ++it) {
           const int rs = it % C::kRaw, s = it % C::kStages, slot = (it >> 1) & 3;
           const int keys = f.kv_len - (f.kb0 + b / 2) * kChunkBlk;  // rows from here on are cleared
@@ -552,23 +561,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Whether all rows that count have exponent bytes 112 to 127.  V's are looked
           // at before K goes out, so that the softmax warps know with the scores what
           // V will be.
-          auto in_range = [&](int r) {
+          auto bytes_of = [&](int r) {
             uint32_t e4 = *reinterpret_cast<const uint32_t*>(&c.scales[r][4 * lane]);
             if (keys < kChunkBlk) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 if (4 * lane + k >= keys) e4 = (e4 & ~(255u << (8 * k))) | 0x70u << (8 * k);
             }
-            return (bool)__all_sync(0xffffffffu, (e4 & 0xF0F0F0F0u) == 0x70707070u);
+            return e4;
           };
-          const bool in = b & 1 ? v_in : in_range(rs);
+          auto in_range = [](uint32_t e4) { return (bool)__all_sync(0xffffffffu, (e4 & 0xF0F0F0F0u) == 0x70707070u); };
+          const bool in = b & 1 ? v_kind == 0 : in_range(bytes_of(rs));
           if (!(b & 1)) {
             const int rv = (it + 1) % C::kRaw;
             if (!(ok = mbar_wait_warp(&c.raw_full[rv], ((it + 1) / C::kRaw) & 1, abort_flag, hdr, 0x819))) break;
-            v_in = in_range(rv);
+            const uint32_t e4 = bytes_of(rv), not_ff = ~e4;
+            if (v_kind != 2) {
+              v_kind = 0;
+              if (!in_range(e4))  // wide: a byte from kWideByte to 254
+                v_kind = 1 + __any_sync(0xffffffffu, e4 & (e4 << 1) & (((not_ff & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | not_ff) & 0x80808080u);
+            }
             if (lt == 0) {
               c4.odd_k[slot] = !in;
-              c4.odd_v[slot] = !v_in;
+              c4.odd_v[slot] = v_kind;
             }
           }
           if (in && keys >= kChunkBlk) {
@@ -610,9 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int k = 0; k < 8; ++k) y[k] = sc == 255u ? 0x7E007E00u : y[k];
                 } else if (sc == 255u) {
                   atomicMin(odd_key, (f.kb0 + b / 2) * kChunkBlk + row);
-                } else {  // V as bf16, times 16 like the others; a scale above 2^3 in two factors
-                  const float bs = unpack_e4m3x2((uint16_t)blk[i * kStep * C::kBlkB]).x * __uint_as_float((min(sc, 130u) + 116u) << 23);
-                  const uint32_t f1 = prmt(__float_as_uint(bs), 0u, 0x3232u), f2 = (max(sc, 130u) - 130u + 127u) * 0x00800080u;
+                } else {  // V as bf16, times 16 like the others or 2^-8; a scale above 2^3 (2^15) in two factors
+                  const uint32_t most = v_kind == 2 ? 142u : 130u;
+                  const float bs = unpack_e4m3x2((uint16_t)blk[i * kStep * C::kBlkB]).x * __uint_as_float((min(sc, most) + 246u - most) << 23);
+                  const uint32_t f1 = prmt(__float_as_uint(bs), 0u, 0x3232u), f2 = (max(sc, most) - most + 127u) * 0x00800080u;
                   e2m1_to_bf16(x.x, f1, &y[0]);
                   e2m1_to_bf16(x.y, f1, &y[4]);
 #pragma unroll
@@ -801,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int vis_min = __reduce_min_sync(0xffffffffu, vis);
       float m = -INFINITY, l = 0.f;
       float c_row = p.c_log2;  // of this row's scores, to base-2 logarithms
+      [[maybe_unused]] bool wide = false;  // the accumulators' unit is kUnitWide
       for (int b = 0; ok && b < n_blk; ++b, ++sc) {
         if (!(ok = mbar_wait_warp(&c.s_full[hf], sc & 1, abort_flag, hdr, 0x811))) break;
         tc_fence_after();
@@ -833,11 +850,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_wait();
             top *= c_blk;
-            const bool up = top > m + 8.f;
-            if (__any_sync(0xffffffffu, up)) {
-              const float a = up ? ex2_approx(m - top) : 1.f;  // 0 from an empty reference
+            const int v_kind = *reinterpret_cast<volatile int*>(&c4.odd_v[slot]);
+            const bool up = top > m + (v_kind == 2 ? 0.f : 8.f), widen = v_kind == 2 && !wide;
+            if (__any_sync(0xffffffffu, up) || widen) {
+              float a = up ? ex2_approx(m - top) : 1.f;  // 0 from an empty reference
               if (up) m = top;
               l *= a;
+              if (widen) a *= kUnit4 / kUnitWide;
+              wide |= widen;
 #pragma unroll 1
               for (int j = 0; b > 0 && j < D / 16; ++j) {  // s_full follows this half's previous P V
                 uint32_t o[16];
@@ -849,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const float mref = m == -INFINITY ? 0.f : m;
-            const bool v_f16 = *reinterpret_cast<volatile int*>(&c4.odd_v[slot]) == 0;
+            const bool v_f16 = v_kind == 0;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
               uint32_t x[32], w0[16];
@@ -1051,10 +1071,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      constexpr float kUnit = C::kFp4 ? 0.0625f : 1.f;  // E2M1: V is 16 times itself
-      auto inverse = [](float x) { return x > 0.f ? kUnit / x : (x == 0.f ? 0.f : x); };  // a NaN sum stays
+      auto inverse = [](float x, float unit) { return x > 0.f ? unit / x : (x == 0.f ? 0.f : x); };  // a NaN sum stays
+      const float unit = !C::kFp4 ? 1.f : wide ? kUnitWide : kUnit4;
+      constexpr float kPartUnit = C::kFp4 ? kUnitWide : 1.f;  // partials have one unit whatever V was
       const int64_t slot = f.starts ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x;
-      const float inv_l = inverse(l);
+      const float inv_l = inverse(l, unit);
 #pragma unroll 1  // unrolled, the code outgrows the instruction cache (E4M3 4 x 4,096: 310 -> 367 us)
       for (int j = 0; j < D / 32; ++j) {
         float v[32];
@@ -1063,6 +1084,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           emit(j, v, inv_l);
         } else if (row_ok) {
           float4* po = reinterpret_cast<float4*>(p.chunk_o) + (slot * (D / 4) + 8 * j) * kChunkRows + R;
+          if constexpr (C::kFp4) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= unit / kPartUnit;
+          }
 #pragma unroll
           for (int k = 0; k < 8; ++k) __stcg(po + k * kChunkRows, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
         }
@@ -1102,7 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += (x.x == m ? 1.f : ex2_approx(x.x - m)) * x.y;
         }
       }
-      const float inv = inverse(l);
+      const float inv = inverse(l, kPartUnit);
 #pragma unroll 1
       for (int j = 0; j < D / 32; ++j) {
         float v[32];
