@@ -585,7 +585,7 @@ flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, cons
  * statistics and accumulators are fp32.  Rounding of the weights for the P V
  * product, relative to each:
  *   chunk kernel                  bf16, 2^-8
- *   chunk kernel, E2M1            f16, 2^-11, and below that at most 2^-25 of
+ *   chunk kernel, E2M1            f16, 2^-11, and below that at most 2^-32 of
  *                                 the row's largest weight; bf16 in blocks of
  *                                 128 keys where a V row's scale byte is not
  *                                 112 to 127, and from one with a byte of 192

@@ -121,9 +121,12 @@ struct __align__(16) Ctl {
 // 2^(139 - E); per key block (of four in turn) whether K lacks its rows'
 // exponents, which are then beside it, and what V is: 0 f16, 1 bf16 (and so the
 // weights), 2 bf16 and wide.  Below kWideByte V is below 2^77: 2^4 times that, weights
-// up to 2^8 (and 2^25 keys) stay far below 2^128.
+// up to 2^15 (and 2^25 keys) stay far below 2^128.
 constexpr uint32_t kWideByte = 192;
 static_assert(kWideByte == 0xC0, "told by the two upper bits of a byte");
+// f16 weights: the reference lies 2^7 below where the others have it, so that the
+// largest weight is 2^7 to 2^15 and what f16 rounds away is 2^-32 of it at most.
+constexpr float kHead4 = 7.f;
 constexpr float kUnit4 = 0x1p-4f, kUnitWide = 0x1p8f;  // O in units of the accumulators
 struct __align__(16) Ctl4 {
   uint64_t q_ready[2];
@@ -851,10 +854,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
             top *= c_blk;
             const int v_kind = *reinterpret_cast<volatile int*>(&c4.odd_v[slot]);
-            const bool up = top > m + (v_kind == 2 ? 0.f : 8.f), widen = v_kind == 2 && !wide;
+            const bool widen = v_kind == 2 && !wide;
+            float a = widen ? ex2_approx(-kHead4) : 1.f;
+            if (widen) m += kHead4;
+            const float head = v_kind == 2 ? 0.f : kHead4;
+            const bool up = top > m + (v_kind == 2 ? 0.f : kHead4 + 8.f);
             if (__any_sync(0xffffffffu, up) || widen) {
-              float a = up ? ex2_approx(m - top) : 1.f;  // 0 from an empty reference
-              if (up) m = top;
+              if (up) {
+                a *= ex2_approx(m - (top - head));  // 0 from an empty reference
+                m = top - head;
+              }
               l *= a;
               if (widen) a *= kUnit4 / kUnitWide;
               wide |= widen;
@@ -931,10 +940,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           t3 = fmax3(t3, __uint_as_float(s3[j]), __uint_as_float(s3[j + 1]));
         }
         const float top = fmaxf(fmax3(t0, t1, t2), t3) * c_row;
-        const bool up = top > m + 8.f;
+        constexpr float kHead = C::kFp4 ? kHead4 : 0.f;
+        const bool up = top > m + (kHead + 8.f);
         if (__any_sync(0xffffffffu, up)) {
-          const float a = up ? ex2_approx(m - top) : 1.f;  // 0 from an empty reference
-          if (up) m = top;
+          const float a = up ? ex2_approx(m - (top - kHead)) : 1.f;  // 0 from an empty reference
+          if (up) m = top - kHead;
           l *= a;
           if (b > 0) {  // s_full follows this half's previous P V
             // 16 columns at a time: the 128 scores stay in registers meanwhile

@@ -78,3 +78,41 @@ def test_large_and_small_values_in_turn():
     tO[:250] += FLOOR * sums[1400:1650][:, None]
     compare(O[:250], wO[:250], tO[:250], "O")
     compare(lse, wl, tl, "lse")
+
+
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("every,kv,q,H,Hkv,ps", [(128, 2500, 200, 2, 1, 16), (640, 6000, 140, 8, 2, 64), (10 ** 6, 20000, 130, 8, 8, 128)])
+def test_many_small_weights_beside_a_dominant_key(every, kv, q, H, Hkv, ps, odd):
+    """Keys that take nearly all weight and hold nothing (attention sinks); the others lie 2^-25 to 2^-29 below them and make
+    up the result.  f16 weights: half a step, 2^-25, of a reference that the largest weight is at least 2^7 of.  odd: a
+    key whose exponent byte a tile of f16 does not hold, every other block."""
+    s = Step4([q], [kv], H=H, Hkv=Hkv, d=64, ps=ps, scale=1.0, seed=every)
+    g = torch.Generator().manual_seed(kv)
+    at = lambda j: (torch.tensor(s.table_host[0])[j // ps].cuda(), (j % ps).cuda())  # noqa: E731
+    s.k.zero_()
+    s.kb.fill_(0x38)  # 1
+    s.ks.fill_(127)
+    page, off = at(torch.arange(0, kv, every))
+    s.k[page, :, off, 0] = 7  # 6 in the first channel
+    # 6 q log2(e) from 25.1 to 29.4
+    s.q_rows.copy_((2.9 + 0.5 * torch.rand(s.q_rows.shape, generator=g)).bfloat16())
+    s.v.copy_(torch.tensor([0x12, 0x24, 0x46, 0x33], dtype=torch.uint8)[torch.randint(0, 4, s.v.shape, generator=g)])  # 0.5 to 4
+    s.vb.fill_(0x38)
+    s.vs.fill_(127)
+    s.v[page, :, off] = 0
+    if odd:
+        j = torch.arange(57, kv, 256)
+        p2, o2 = at(j)
+        s.ks[p2, :, o2] = 100  # rows of zeros: the scores stay
+    O, lse = s.run()
+    torch.cuda.synchronize()
+    assert fl.flamia_get_device_status(s.ws) == fl.OK
+    wO, wl, tO, tl = s.reference(2.0 ** -11)
+    for h in range(H):
+        K, V = s.rows_of(0, h * Hkv // H)
+        see = torch.arange(kv, device="cuda")[None] <= torch.arange(kv - q, kv, device="cuda")[:, None]
+        x = torch.where(see, s.q.view(q, H, 64)[:, h].double() @ K.T, -torch.inf)
+        p = torch.exp(x - x.amax(1, keepdim=True))
+        tO[:, h] += 2.0 ** -32 * (see.double() @ V.abs()) / p.sum(1, keepdim=True)
+    compare(O, wO, tO, "O")
+    compare(lse, wl, tl, "lse")
