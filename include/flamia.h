@@ -275,7 +275,10 @@ size_t flamia_debug_workspace_offset(const flamia_problem_t* p, int32_t region);
  * bounded-wait limit (about 2 s): the kernel records FLAMIA_ERR_TIMEOUT in the
  * device status word, every role leaves its loop and the CTA releases its
  * tensor memory and exits (nothing was issued, so no copy or MMA is in
- * flight).  The outputs of such a call are undefined.  Process-wide (not per
+ * flight).  The outputs of such a call are undefined.  Of flamia_paged_plan_shared
+ * and flamia_paged_compact a CTA stays away from the last of the launch's
+ * barriers over its CTAs, whose wait runs out likewise (about 2 s): no
+ * page moves.  Process-wide (not per
  * workspace); flamia_plan switches it off.  Always returns FLAMIA_OK. */
 flamia_status_t flamia_debug_withhold_first_item(int32_t on);
 
@@ -529,7 +532,8 @@ size_t flamia_paged_pages_workspace_size(const flamia_paged_t* p);
  * entry that the step reads outside [0, n_pages), counts below the entries
  * that it sees, more pages freed than the stack has room for),
  * FLAMIA_ERR_NO_PAGES.  Then nothing moves, *n_free_out = *n_free, *n_copies =
- * 0, every slot is -1, and launches that use `ws` write nothing.
+ * 0, every slot is -1, and launches that use `ws` write nothing.  So too after
+ * FLAMIA_ERR_TIMEOUT (a CTA did not come to one of the launch's barriers).
  * FLAMIA_ERR_UNSUPPORTED (from the host) where the sizes allow a step that
  * flamia_paged_plan would refuse with it. */
 flamia_status_t flamia_paged_plan_shared(const flamia_paged_t* p, int32_t* slot_map, const int32_t* src,
@@ -560,7 +564,8 @@ flamia_status_t flamia_paged_copy(const flamia_paged_t* p, int32_t n_layers, con
  * Conditions, checked before anything is written but `copies` (in pages_ws):
  * FLAMIA_ERR_BAD_SEQLENS (len), FLAMIA_ERR_BAD_PAGE (*n_free out of range, a
  * free page out of range or twice on the stack, a table entry out of range or
- * on the stack).  Then nothing moves and *n_copies = 0. */
+ * on the stack).  Then, and after FLAMIA_ERR_TIMEOUT, nothing moves and *n_copies
+ * = 0. */
 flamia_status_t flamia_paged_compact(const flamia_paged_t* p, const int32_t* len, int32_t* refs, int32_t* free_pages,
                                      const int32_t* n_free, int32_t* copies, int32_t* n_copies, void* pages_ws,
                                      size_t pages_ws_bytes, cudaStream_t stream);

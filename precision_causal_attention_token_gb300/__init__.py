@@ -208,7 +208,8 @@ def flamia_debug_workspace_offset(prob: Problem, region: int) -> int:
 
 def flamia_debug_withhold_first_item(on: bool):
     """Test hook: the next attention launches withhold each CTA's first work
-    item, so that their bounded waits run out (see include/flamia.h)."""
+    item, and the page calls an arrival at their last barrier, so that their
+    bounded waits run out (see include/flamia.h)."""
     _check(load_library().flamia_debug_withhold_first_item(int(bool(on))), "flamia_debug_withhold_first_item")
 
 

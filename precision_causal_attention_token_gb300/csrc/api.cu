@@ -143,6 +143,8 @@ bool operand_ok(const flamia_operand_t* o) {
 
 }  // namespace
 
+bool flamia::debug_withhold() { return g_dbg_withhold.load() != 0; }
+
 extern "C" {
 
 size_t flamia_workspace_size(const flamia_problem_t* p) {

@@ -28,6 +28,8 @@ cudaError_t launch_quantize(const QuantBatch& qb, int d, int in_bf16, int o_bf16
                             const int32_t* cu, const int32_t* blk_prefix, int n_seq, WsHeader* hdr, int max_units,
                             int n_sms, cudaStream_t st);
 int sm_count();
+// Test hook (flamia_debug_withhold_first_item): whether it is on.
+bool debug_withhold();
 
 // Grid of an attention kernel over `work` items: one CTA per SM (persistent,
 // items from a global counter) or, with cluster launch control, one CTA per

@@ -280,6 +280,7 @@ flamia_status_t flamia_paged_plan_shared(const flamia_paged_t* p, int32_t* slot_
   b.n_free_out = n_free_out;
   b.copies = copies;
   b.n_copies = n_copies;
+  b.dbg_withhold = debug_withhold() ? kShareBarriers : 0;
   a.slot_map = slot_map;
   a.before = &b.hdr->fail;
   const cudaError_t e = launch_paged_share(b, sm_count(), stream);
@@ -300,6 +301,7 @@ flamia_status_t flamia_paged_compact(const flamia_paged_t* p, const int32_t* len
   b.n_free = n_free;
   b.copies = copies;
   b.n_copies = n_copies;
+  b.dbg_withhold = debug_withhold() ? kCompactBarriers : 0;
   return of(launch_paged_compact(b, sm_count(), stream));
 }
 

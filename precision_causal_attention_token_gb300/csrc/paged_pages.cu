@@ -41,30 +41,37 @@ constexpr int kSpinLimit = 1 << 23;  // polls of 32 ns or more each, but for the
 __device__ __forceinline__ int pages_of(int len, int shift) { return (len + (1 << shift) - 1) >> shift; }
 
 // All CTAs of the launch (they are resident together); `nth` counts a launch's
-// barriers from 1.  False, for the whole CTA, where the wait ran out (a CTA that
-// comes to the barrier later finds `bad` set).
+// barriers from 1.  False, for the whole CTA, where the wait ran out.  A CTA whose
+// wait has run out closes the barrier, unless it is complete by then: so either
+// every CTA passes it or none does, those that come later included, and what stands
+// behind a launch's last barrier happens whole or not at all.
+constexpr uint32_t kClosed = 1u << 31;
 __device__ bool grid_barrier(const PagesParams& p, uint32_t nth) {
   __shared__ int sm_ok;
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    atomicAdd(&p.hdr->arrived, 1u);
+    if (!(nth == (uint32_t)p.dbg_withhold && blockIdx.x == 0)) atomicAdd(&p.hdr->arrived, 1u);
+    const uint32_t all = nth * gridDim.x;
     int left = kSpinLimit;
     uint32_t seen;
     while (true) {
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(&p.hdr->arrived) : "memory");
-      if (seen >= nth * gridDim.x || --left == 0) break;
+      if (seen >= all || --left == 0) break;  // closed: above all counts
       if (left < kSpinLimit - 100) __nanosleep(32);
     }
-    if (left == 0) {  // no page moves, and what follows on the stream has nothing to do
+    while (seen < all) {
+      const uint32_t was = atomicCAS(&p.hdr->arrived, seen, seen | kClosed);
+      seen = was == seen ? seen | kClosed : was;
+    }
+    sm_ok = seen < kClosed;
+    if (!sm_ok) {  // no page moves, and what follows on the stream has nothing to do
       report(&p.hdr->base, FLAMIA_ERR_TIMEOUT, 0x740);
       p.hdr->fail = FLAMIA_ERR_TIMEOUT;
-      atomicOr(&p.hdr->bad, 1u);
       if (p.n_free_out) *p.n_free_out = *p.n_free;
       *p.n_copies = 0;
     }
     __threadfence();
-    sm_ok = left > 0;
   }
   __syncthreads();
   return sm_ok != 0;
@@ -441,10 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_compact_kernel(const PagesP
     }
     __syncthreads();
   }
-  for (int64_t i = i0; i < n_free; i += step) p.free_pages[i] = p.n_pages - 1 - (int)i;
-  if (first && tid == 0) *p.n_copies = below;
   if (!grid_barrier(p, 3)) return;
-  // ------------------------------------------------ tables and counts follow
+  // ------------------------------------------------ stack, tables and counts
+  if (first && tid == 0) *p.n_copies = below;
+  for (int64_t i = i0; i < n_free; i += step) p.free_pages[i] = p.n_pages - 1 - (int)i;
   entries([&](int32_t* at) {
     const int id = *at;
     if (id >= used) *at = __ldcg(p.copies + 2 * (int64_t)__ldcg(p.rank + id) + 1);

@@ -6,13 +6,14 @@
 namespace flamia {
 
 constexpr int kPagesThreads = 512, kMaxPagesCtas = 160;
+constexpr int kShareBarriers = 2, kCompactBarriers = 3;  // of a launch
 constexpr int kCopyLayers = 32;  // of a launch: its parameters stay below 4 KB
 
 struct PagesHeader {
   WsHeader base;         // status words first, as flamia_get_device_status reads them
   uint32_t fail;         // why the step moved no page: flamia_paged_plan_shared's plan reads it
   uint32_t bad;          // found by some CTA before anything is written
-  uint32_t arrived;      // CTAs at the grid's barriers, all of the launch together
+  uint32_t arrived;      // CTAs at the grid's barriers, all of the launch together; its top bit: a wait ran out
   uint32_t wrong;        // counts that do not cover the tables' entries; apart from `bad`, which a slow CTA may
                          // still have to read at one barrier while a fast one is at the next
   uint32_t pad[12];
@@ -50,6 +51,7 @@ struct PagesParams {
   int32_t* staged;         // [n_req][max_pages] pages that a row takes over from another's
   int32_t* freed;          // [n_req][max_pages] pages without a holder, by the row that let go of them first
   int4* counts;            // [n_req] pages that the row takes, its freed ones, whether its partly filled one is copied
+  int dbg_withhold;        // test hook: the barrier, from 1, at which one CTA's arrival is withheld
   // compact, in the place of `pages`
   uint32_t* bits;          // free pages
   int32_t* rank;           // [n_pages] of the pages that move
