@@ -184,6 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
     own[j] = x;
   }
   __syncthreads();
+  // the free stack, all of it: which of its pages the step takes is known after both barriers
+#pragma unroll 4
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < n_free; i += (int64_t)gridDim.x * kThreads) page_ok(p.free_pages[i]);
   // ------------------------------------------------ 1: holders gained and lost
   for (int j = 0; j < n_own; ++j) {
     const int r = blockIdx.x + j * gridDim.x;
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
           p.copies[2 * (int64_t)copied[r]] = id;
           p.copies[2 * (int64_t)copied[r] + 1] = to;
           atomicAdd(p.refs + id, -1);
-          if ((unsigned)to < (unsigned)p.n_pages) atomicAdd(p.refs + to, 1);
+          atomicAdd(p.refs + to, 1);
           id = to;
         }
         if (moved || mine) table[k] = id;
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
     for (int k = row.keep + tid; k < row.need; k += kThreads) {
       const int id = fresh(taken[r] + copy + k - row.keep);
       table[k] = id;
-      if ((unsigned)id < (unsigned)p.n_pages) atomicAdd(p.refs + id, 1);
+      atomicAdd(p.refs + id, 1);
     }
   }
   for (int64_t j = (int64_t)blockIdx.x * kThreads + tid; j < n_given - n_taken; j += (int64_t)gridDim.x * kThreads)
