@@ -187,7 +187,9 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedParam
         const float inv = E2M1 ? exp2i(-e) : exp2i(max(-e, -126));  // 2^-e; e = 127 does not occur (E2M1: nor does 118)
         if constexpr (E2M1) {
           float s;
-          uint32_t blk = e2m1_block_scale(__uint_as_float(top_blk) * inv, s);
+          // (a block so far below its row that the product underflows still has the smallest scale)
+          const float bm = __uint_as_float(top_blk);
+          uint32_t blk = e2m1_block_scale(fmaxf(bm * inv, fminf(bm, 1.17549435e-38f)), s);
           const float r = e2m1_reciprocal<BF16>(s);
           uint32_t c0 = e2m1_codes<BF16>(f, inv, s, r), c1 = e2m1_codes<BF16>(f + kEl / 2, inv, s, r);
           if (!finite) blk = c0 = c1 = 0u;
