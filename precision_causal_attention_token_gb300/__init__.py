@@ -479,7 +479,11 @@ class PagedCall:
 
     With ``shared`` requests may hold the same pages: ``plan(cu_q, kv_len, src)`` says which request (as it was before
     the step) each one continues, -1 none; forks share pages, and one that is written to is copied first.  ``compact()``
-    moves the pages in use to the low end of the pools."""
+    moves the pages in use to the low end of the pools.
+
+    ``status`` (a word on the device) is the last plan's and its appends' and attentions', ``pages_status`` (``shared``
+    only) that of the last plan's page management and copies or, after ``compact()``, of the compaction: read the latter
+    before a pool is cut, a compaction that was refused has moved nothing."""
 
     n_req: int
     T: int           # new tokens of a step at most
@@ -533,6 +537,7 @@ class PagedCall:
             self.src = self.same.clone()
             self.copies, self.n_copies = torch.zeros(max(self.n_req, self.n_pages), 2, **i32), torch.zeros(1, **i32)
             self.pages_ws = torch.zeros(flamia_paged_pages_workspace_size(self.prob), dtype=torch.uint8, device=self.device)
+            self.pages_status = self.pages_ws[:4].view(torch.int32)
         self.O = torch.zeros(self.T, self.H, self.d, dtype=torch.bfloat16, device=self.device)
         self.lse = torch.zeros(self.H, self.T, dtype=torch.float32, device=self.device)
         self.kv_dtype = torch.bfloat16 if self.in_dtype == BF16 else torch.float32
@@ -566,7 +571,7 @@ class PagedCall:
 
     def compact(self):
         """The pages in use to ids 0 .. n_pages - n_free - 1 of every layer's pools, tables and data (``shared`` only).
-        Between steps: the next plan must follow before append and attend."""
+        Between steps: the next plan must follow before append and attend.  ``pages_status`` says whether it was done."""
         if not self.shared:
             raise FlamiaError(ERR_INVALID_ARG, "PagedCall.compact")
         flamia_paged_compact(self.prob, self.pages_ws, self.held_len, self.refs, self.free_pages, self.n_free, self.copies,
