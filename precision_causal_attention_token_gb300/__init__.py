@@ -260,8 +260,8 @@ def paged_cache(k, v, k_scales=None, v_scales=None, k_blocks=None, v_blocks=None
     """One layer's pool: k, v [n_pages, Hkv, page_size, d] (bf16, or uint8 E4M3 codes with uint8 scales
     [n_pages, Hkv, page_size]), or uint8 [n_pages, Hkv, page_size, d / 2] (two E2M1 codes a byte) with such scales and
     block scales [n_pages, Hkv, page_size, d / 16] (uint8 or float8_e4m3fn).  Pages may be strided (k = pool[:, 0],
-    v = pool[:, 1]); a page is contiguous.  The calls refuse a pool of another type or page shape than the problem's, or
-    of fewer pages."""
+    v = pool[:, 1]); a page is contiguous.  The calls refuse a pool of another type or page shape than the problem's, of
+    fewer pages or on another device than the workspace's."""
     import torch
     if k.shape != v.shape or k.stride() != v.stride() or k.dim() != 4 or k.dtype != v.dtype:
         raise ValueError("k and v must be [n_pages, Hkv, page_size, d] of one type and layout")
@@ -280,6 +280,8 @@ def paged_cache(k, v, k_scales=None, v_scales=None, k_blocks=None, v_blocks=None
                 raise ValueError("block scales must be contiguous bytes [n_pages, Hkv, page_size, d / 16]")
         if k.dtype != torch.uint8 or k_scales is None or v_scales is None:
             raise ValueError("block scales go with uint8 codes and their scales")
+    if any(t is not None and t.device != k.device for t in (v, k_scales, v_scales, k_blocks, v_blocks)):
+        raise ValueError("a pool's tensors must be on one device")
     stride = k.stride(0) if k.shape[0] > 1 else 0
     cache = Cache(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), 2 * stride if e2m1 else stride, _ptr(k_blocks),
                   _ptr(v_blocks))
@@ -298,6 +300,8 @@ def _paged_call(name, ws, stream, *args):
     host time is what a small serving step costs."""
     import torch
     dev = ws.get_device()
+    if dev < 0:
+        raise FlamiaError(ERR_INVALID_ARG, name)
     s = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
@@ -367,22 +371,23 @@ def flamia_paged_compact(prob: Paged, pages_ws, length, refs, free_pages, n_free
                 _ptr(copies), _ptr(n_copies))
 
 
-def _check_pool(prob, cache, where):
+def _check_pool(prob, cache, where, ws):
     if cache.pool is not None:
         page, n_pages = cache.pool
-        if page != (prob.Hkv, prob.page_size, prob.d, prob.cache_dtype) or n_pages < prob.n_pages:
+        if (page != (prob.Hkv, prob.page_size, prob.d, prob.cache_dtype) or n_pages < prob.n_pages or
+                cache.device != ws.get_device()):
             raise FlamiaError(ERR_INVALID_ARG, where)
 
 
 def flamia_paged_append(prob: Paged, k, v, slot_map, cache: Cache, ws, stream=None):
     """The step's K and V rows into their slots of one layer's cache."""
-    _check_pool(prob, cache, "flamia_paged_append")
+    _check_pool(prob, cache, "flamia_paged_append", ws)
     _paged_call("flamia_paged_append", ws, stream, prob, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), cache)
 
 
 def flamia_paged_fwd(prob: Paged, q, cache: Cache, O, lse, ws, stream=None):
     """Attention of the step's queries over one layer's cache (lse may be None)."""
-    _check_pool(prob, cache, "flamia_paged_fwd")
+    _check_pool(prob, cache, "flamia_paged_fwd", ws)
     _paged_call("flamia_paged_fwd", ws, stream, prob, q.data_ptr(), cache, O.data_ptr(), _ptr(lse))
 
 
