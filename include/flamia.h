@@ -600,7 +600,9 @@ flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, cons
  *   decode kernel, E4M3 or E2M1   f16, 2^-11, and below that at most 2^-20 of
  *                                 the row's largest weight; two bf16 terms
  *                                 where the scale bytes of the V rows that a
- *                                 warp takes lie more than 12 apart
+ *                                 warp takes lie more than 12 apart (E2M1,
+ *                                 with a byte of 192 or more among them: V is
+ *                                 exact down to 2^-102)
  * Keys that a row does not see, and what slots behind a request's last token
  * hold, change no row's precision beyond that.
  *   q    device bf16 [T][H][d] (q_stride)

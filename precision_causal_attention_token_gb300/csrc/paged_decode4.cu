@@ -18,7 +18,13 @@
 //
 // Scales of queries and keys, f16 weights relative to the largest exponent of
 // V and the careful second pass (bf16 values, two bf16 terms a weight) where
-// exponents lie more than kSpread apart: as for E4M3, see paged_decode.cu.
+// exponents lie more than kSpread apart: as for E4M3, see paged_decode.cu.  V near the
+// largest numbers: bf16 values of 2^128 (an append may round the largest row up to
+// there) would be infinite, and NaN times the weight 0 of a row that does not see them,
+// and sums of such values would overflow although their mean does not.  Once a warp has met an
+// exponent byte of kWideByte (V of 2^66 and more), its sums, and in the careful pass V, are
+// 2^-kWideShift times themselves, with the reference kWideShift higher: 32,000 of
+// the largest rows add up.
 //
 // Measured (152 SMs, H = 32, Hkv = 8, d = 128): 64 requests, 281,000 tokens, 80 us
 // (4.1 TB/s, 61% of the copy rate; the E4M3 kernel 109 us for 1.76 times the
@@ -52,6 +58,9 @@ __device__ __forceinline__ uint32_t lds1(uint32_t a) {
 }
 __device__ __forceinline__ float f16_lo(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v & 0xFFFFu))); }
 __device__ __forceinline__ float f16_hi(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v >> 16))); }
+
+constexpr int kWideByte = 192, kWideShift = 24;
+constexpr int kCareful = 134, kCarefulWide = 512;  // e_ref of the careful pass: no factor, 2^-kWideShift in V
 
 template <int D, int NT>
 struct Cfg {
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
 #pragma unroll
         for (int i = 0; i < C::kMT; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
       }
-      e_ref = careful ? 134 : 0;  // 134: no factor
+      e_ref = careful ? kCareful : 0;
       int e_low = 255;            // the smallest that this lane has read
       int st = 0;
       for (int it = 0; it < n_it; ++it) {
@@ -353,6 +362,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
               for (int i = 0; i < C::kMT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][nt][e] *= a;
+          } else if (e_ref == kCareful && __any_sync(0xffffffffu, e_top >= kWideByte)) {
+            e_ref = kCarefulWide;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < C::kMT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][nt][e] *= exp2i(-kWideShift);
           }
           if (nan_key) {
             // its block scales may be NaN too: the NaN comes with the weight, and
@@ -546,11 +563,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
           else add(std::false_type{});
         } else {
           // V as bf16 values (six significant bits: exact), two bf16 terms a weight
+          const float v_unit = e_ref == kCareful ? 1.f : exp2i(-kWideShift);
 #pragma unroll 1
           for (int i = 0; i < kSub; ++i) {
             float fv[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) fv[k] = ue8m0(min(lds1(sv + 16 * i + 2 * t + (k & 1) + 8 * (k >> 1)), 254u));
+            for (int k = 0; k < 4; ++k) fv[k] = ue8m0(min(lds1(sv + 16 * i + 2 * t + (k & 1) + 8 * (k >> 1)), 254u)) * v_unit;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               uint32_t ph[2], pl[2];
@@ -598,7 +616,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas)
 
     // ------------------------------------------------ join the warps
     {  // the accumulators hold 2^(134 - e_ref) times the sum; in two normal factors
-      const float f0 = exp2i((e_ref - 134) / 2), f1 = exp2i(e_ref - 134 - (e_ref - 134) / 2);
+      const int shift = e_ref >= kWideByte ? kWideShift : 0, x = e_ref == kCarefulWide ? 0 : e_ref - 134 - shift;
+      const float f0 = exp2i(x / 2), f1 = exp2i(x - x / 2), unit = exp2i(-shift);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m[nt][e] += (float)shift;
+          l[nt][e] *= unit;
+        }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
