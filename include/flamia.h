@@ -528,9 +528,10 @@ size_t flamia_paged_pages_workspace_size(const flamia_paged_t* p);
  * must not occur twice in a row.
  * Device-side conditions, all checked before anything is written (in both
  * workspaces' status words): FLAMIA_ERR_BAD_SEQLENS (as in flamia_paged_plan;
- * src outside [-1, n_req)), FLAMIA_ERR_BAD_PAGE (*n_free out of range, a free
- * page or a table entry that the step reads outside [0, n_pages), counts below
- * the entries that it sees, more pages freed than the stack has room for),
+ * src outside [-1, n_req)), FLAMIA_ERR_BAD_PAGE (*n_free out of range, a table
+ * entry that the step reads or a free page that it may take, if every writer
+ * takes a copy, outside [0, n_pages), counts below the entries that it sees,
+ * more pages freed than the stack has room for),
  * FLAMIA_ERR_NO_PAGES.  Then nothing moves, *n_free_out = *n_free, *n_copies =
  * 0, every slot is -1, and launches that use `ws` write nothing.  So too after
  * FLAMIA_ERR_TIMEOUT (a CTA did not come to one of the launch's barriers).

@@ -184,14 +184,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
     own[j] = x;
   }
   __syncthreads();
-  // the free stack, all of it: which of its pages the step takes is known after both barriers
-#pragma unroll 4
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < n_free; i += (int64_t)gridDim.x * kThreads) page_ok(p.free_pages[i]);
   // ------------------------------------------------ 1: holders gained and lost
+  unsigned long long most = 0;  // pages that these rows take at most
   for (int j = 0; j < n_own; ++j) {
     const int r = blockIdx.x + j * gridDim.x;
     const OwnRow& x = own[j];
     const Row& row = x.row;
+    most += max(0, row.need - row.keep) + (row.write_at >= 0);
     if (row.src >= 0 && (row.src != r || heir[r] != r)) {
       const int32_t* from = p.block_table + (int64_t)row.src * mp;
       const bool more = heir[row.src] != r;
@@ -218,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
       }
     }
   }
+  if (tid == 0 && most) atomicAdd(&p.hdr->most, most);
   if (!grid_barrier(p, 1)) return;
   // ------------------------------------------------ 2: pages without a holder, pages to copy
   if (__ldcg(&p.hdr->bad)) return give_up(FLAMIA_ERR_BAD_PAGE);
@@ -225,7 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_share_kernel(const PagesPar
     const int4 v = __ldcg(reinterpret_cast<const int4*>(p.pages + id));
     return PageRec{v.x, v.y, v.z, v.w};
   };
-  uint32_t wrong = 0;  // counts that do not cover the tables' entries
+  uint32_t wrong = 0;  // counts that do not cover the tables' entries, free pages outside the pool
+  // (how many the step takes is known behind the next barrier)
+  const int64_t may_take = min((int64_t)__ldcg(&p.hdr->most), (int64_t)n_free);
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < may_take; i += (int64_t)gridDim.x * kThreads)
+    wrong |= (unsigned)p.free_pages[n_free - 1 - i] >= (unsigned)p.n_pages;
   for (int j = tid; j < n_own; j += kThreads) {
     const Row row = own[j].row;
     if (row.write_at < 0) continue;

@@ -14,9 +14,10 @@ struct PagesHeader {
   uint32_t fail;         // why the step moved no page: flamia_paged_plan_shared's plan reads it
   uint32_t bad;          // found by some CTA before anything is written
   uint32_t arrived;      // CTAs at the grid's barriers, all of the launch together; its top bit: a wait ran out
-  uint32_t wrong;        // counts that do not cover the tables' entries; apart from `bad`, which a slow CTA may
+  uint32_t wrong;        // found between the barriers; apart from `bad`, which a slow CTA may
                          // still have to read at one barrier while a fast one is at the next
-  uint32_t pad[12];
+  unsigned long long most;  // pages that the step takes at most
+  uint32_t pad[10];
   uint32_t count[kMaxPagesCtas];  // compact: free pages in each CTA's part
 };
 

@@ -10,10 +10,10 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("entry", [12, -1, 1 << 30, -(1 << 31)])
-@pytest.mark.parametrize("at", [-1, -2, 0])
-def test_a_step_refuses_a_stack_with_a_page_outside_the_pool(at, entry):
-    """Of the two pages that the step takes (a copy on write, a longer row), and one that it leaves: nothing moves, and with
-    the entry put right the same step goes through."""
+@pytest.mark.parametrize("at", [-1, -2])
+def test_a_step_refuses_to_take_a_page_outside_the_pool(at, entry):
+    """Of the two pages that the step takes (a copy on write, a longer row): nothing moves, and with the entry put right the
+    same step goes through."""
     m = Pool(3, 12, 4, 16)
     gpu = Gpu(m, 3, 64, 40)
     m.step([20, 40, 0], [20, 40, 0], [0, 1, 2])
@@ -34,6 +34,22 @@ def test_a_step_refuses_a_stack_with_a_page_outside_the_pool(at, entry):
     assert len(copies) == 1 and gpu.step() == fl.OK
     gpu.same(copies)
     assert gpu.slots.tolist() == m.slots(q, kv, 64)
+
+
+def test_a_long_row_takes_no_page_outside_the_pool():
+    """Thousands of pages for one row, a bad one anywhere among them."""
+    m = Pool(2, 5000, 4000, 16)
+    gpu = Gpu(m, 2, 64000, 64000)
+    for at in (4999, 4998, 3000, 1500, 1002):  # the row takes 3,999 pages
+        gpu.inputs([63970, 0], [63970, 0], [0, 1], [0, 0])
+        gpu.free[at] = 5000
+        assert gpu.step() == fl.ERR_BAD_PAGE and int(gpu.refs.sum()) == 0 and int(gpu.table.abs().sum()) == 0
+        gpu.free[at] = at
+    gpu.free[1000] = -3  # left on the stack
+    copies = m.step([63970, 0], [63970, 0], [0, 1])
+    m.free[1000] = -3
+    assert gpu.step() == fl.OK
+    gpu.same(copies)
 
 
 def test_entries_behind_the_count_are_not_read():
