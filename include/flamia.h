@@ -457,7 +457,8 @@ size_t flamia_paged_workspace_size(const flamia_paged_t* p);
  * entries are written; what is left of S stays in free_pages and its length
  * goes to *n_free_out.  So a finished request passes kv_len 0, one whose
  * drafted tokens were rejected a smaller kv_len.  Pages must belong to one
- * request only (flamia_paged_plan_shared: to several).  Table entries outside the taken pages are not written.
+ * request only (flamia_paged_plan_shared: to several).  Table entries outside
+ * the taken pages are not written.
  *   old_len     int32 [n_req]
  *   free_pages  int32 [n_pages] stack of free page ids
  *   n_free, n_free_out  int32 [1]; may be the same word
@@ -578,9 +579,10 @@ flamia_status_t flamia_paged_compact(const flamia_paged_t* p, const int32_t* len
  * finite rows; or as E2M1 codes: e is the smallest exponent with max|x| <=
  * 2688 2^e (2688 = 6 * 448; clamped alike, 0 for a zero row), a block scale s
  * the smallest E4M3 value with 6 s 2^e >= its 16 channels' max|x|, a code
- * RNE(x 2^-e / s) (0 where s is 0), of the exact quotient.  A slot of -1 skips the row; slots must be distinct.  Any
- * other slot outside the pool is skipped and sets FLAMIA_ERR_BAD_PAGE.  Requires
- * flamia_paged_plan on the same workspace. */
+ * RNE(x 2^-e / s) (0 where s is 0), of the exact quotient (values of a row
+ * above 3.3e38 may so pass 2^128).  A slot of -1 skips the row; slots must be
+ * distinct.  Any other slot outside the pool is skipped and sets
+ * FLAMIA_ERR_BAD_PAGE.  Requires flamia_paged_plan on the same workspace. */
 flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, const void* v, const int32_t* slot_map,
                                     const flamia_cache_t* cache, void* ws, size_t ws_bytes, cudaStream_t stream);
 
@@ -605,7 +607,10 @@ flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, cons
  *                                 with a byte of 192 or more among them: V is
  *                                 exact down to 2^-102)
  * Keys that a row does not see, and what slots behind a request's last token
- * hold, change no row's precision beyond that.
+ * hold, change no row's precision beyond that.  Ranges: scores over a cache of
+ * codes are formed from queries scaled to 2^13 and may overflow from K rows of
+ * 2^116 on; sums of weights (at most 2^8 of the first ones) times V are fp32 in
+ * all kernels, over E2M1 with V of 2^66 and more in units in which V of any size fits.
  *   q    device bf16 [T][H][d] (q_stride)
  *   O    device bf16 [T][H][d], contiguous
  *   lse  device float [H][T], natural logarithm (may be NULL)

@@ -23,12 +23,6 @@ namespace {
 
 constexpr int kThreads = 256, kHeads = 4;
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // The smallest integer e with amax <= 2688 2^e (2688 = 6 * 448 = 1.3125 * 2^11, the
 // largest E2M1 value times the largest block scale), at least -127; 0 for 0.
 __device__ __forceinline__ int e2m1_row_exp(float amax) {

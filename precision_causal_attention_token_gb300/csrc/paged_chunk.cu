@@ -12,12 +12,12 @@
 //   warps 0-3, 4-7  softmax of half 0 and 1: a thread owns a row.  It reads
 //              the row's 128 scores from tensor memory, masks, moves its
 //              reference when a score passes it by 2^8 (then it rescales the
-//              row's accumulator), and writes the weights back as bf16 over
-//              the scores, from where the P V product reads them as its A
+//              row's accumulator), and writes the weights back as bf16 (E2M1:
+//              f16) over the scores, from where the P V product reads them as its A
 //              operand: P never touches shared memory.
 //   warps 8-11 loaders.  E4M3, E2M1: each block's codes from the raw ring into
-//              bf16 tiles, times the row's scale (and the block's; exact).  All: zeros in rows past
-//              the request's last key, where pages hold what an earlier owner
+//              bf16 (f16) tiles, times the row's scale (and the block's; exact).
+//              All: zeros in rows past the request's last key, where pages hold what an earlier owner
 //              left: 0 x NaN is NaN.  For the same reason they take infinities
 //              and NaN out of V in the blocks that some row sees in part, and
 //              leave word of the first such key, so that the rows that do see
@@ -30,13 +30,14 @@
 //   warp 15    the queries of each half, as soon as its last scores of the
 //              tile before are formed: one box of G heads x tokens for 64
 //              channels, whose rows come in the tile's order whatever G is.
-// The row's weights are rounded to bf16 once (2^-8 relative); sums use the
+// The row's weights are rounded once, to bf16 (2^-8 relative) or, E2M1, to f16
+// (2^-11, and 2^-32 of the row's largest below f16's normal range); sums use the
 // unrounded ones.
 //
 // Measured (152 SMs, H = 32, Hkv = 8, d = 128): 2,048 new tokens over 32,768 in
 // bf16 720 us (1,575 TFLOP/s; 808 back to back under the power limit), in E4M3
 // 850, in E2M1 863; four times 4,096 from nothing (16 heads each) 231 us in bf16,
-// 294 in E4M3, 291 in E2M1.  bf16 is bound by the tensor cores, and by 3 to 4 us
+// 294 in E4M3 and in E2M1.  bf16 is bound by the tensor cores, and by 3 to 4 us
 // between one tile's last product and the next one's first; E4M3 by shared memory,
 // which conversion and the MMAs' operands share: a step's operands take 1,536 of
 // its 2,048 tensor cycles, codes and converted tiles 1,024 more; E2M1 (half the
@@ -180,11 +181,6 @@ __device__ __forceinline__ void e2m1_to_bf16(uint32_t w, uint32_t f, uint32_t* y
     const uint32_t t = h[k] >> 3;
     y[k] = bf16x2_mul(t + (t & 0x10001000u) * 7u, f);
   }
-}
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 
 // S[half] = Q[half] K^T: both K-major, 128-byte swizzled rows of 64 channels.

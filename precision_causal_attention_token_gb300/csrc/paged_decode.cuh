@@ -62,8 +62,9 @@ struct Join {
 // query rows in columns; kWide: a lane's channels in two runs of eight) are
 // added up, and the tile's result goes to O and lse, or, where the tile is
 // shared, to the workspace, from where the last of its workers adds the
-// partials up in worker order.  `sm` and `wt_buf` (the partials' weights) lie in
-// the place of the warps' rings.
+// partials up in worker order.  `sm` and `wt_buf` (the partials' weights) may lie
+// in the place of the warps' rings only if no copy into these is in flight: a kernel
+// that asks for its next tile's chunks before the join has them elsewhere.
 template <int D, int NT, int kWarps, bool kWide>
 __device__ __forceinline__ void join_tile(const PagedParams& p, const ReqRec& rq, int h, int w, int blk, int nb, int blocks,
                                           const float (&o)[D / 16][NT][4], const float (&m)[NT][2], const float (&l)[NT][2],
@@ -72,7 +73,7 @@ __device__ __forceinline__ void join_tile(const PagedParams& p, const ReqRec& rq
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rows = rq.q_len * p.G;
   PagedHeader* hdr = p.hdr;
-  __syncthreads();  // every warp is done with its ring
+  __syncthreads();  // every warp is done with its ring's chunks of this tile
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

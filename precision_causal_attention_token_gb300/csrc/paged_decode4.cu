@@ -9,8 +9,8 @@
 // multiplication by the block scale, both exact in f16 (1 + 1 mantissa bits
 // times 1 + 3, up to 6 * 448).  A chunk's copies are asynchronous 16-byte
 // copies, 512 contiguous bytes an instruction, into a ring of the warp's own
-// (boxes by TMA, a lane each, took 55 instructions a key tile more: their operands are
-// per warp, so the lanes' boxes are issued one after the other).  Slots behind a
+// (boxes by TMA, a lane each, took 415 instructions a key tile against 390 then: their
+// operands are per warp, so the lanes' boxes are issued one after the other).  Slots behind a
 // request's last token hold what an earlier owner left: V's block scales there
 // are replaced by zeros (codes are always finite).
 // In V two keys' codes are interleaved by nibbles before they are converted,
@@ -29,7 +29,7 @@
 // Measured (152 SMs, H = 32, Hkv = 8, d = 128): 64 requests, 281,000 tokens, 80 us
 // (4.1 TB/s, 61% of the copy rate; the E4M3 kernel 109 us for 1.76 times the
 // bytes; its own code with E2M1 operands took 104); one request of 65,522 tokens
-// 29 us; 32 requests of 2 to 4 drafted tokens 70 us, 16 of 2 to 8 (32 rows) 66.
+// 28 us; 32 requests of 2 to 4 drafted tokens 70 us (205 MB), 16 of 2 to 8 (32 rows) 68 (96 MB).
 // Of a long tile's 113,000 cycles of loop, the loads alone take 95,000 and the
 // instructions alone 97,000; 6 us go by before a CTA's first chunk is there and
 // 3 to 4 with each tile's join.  With d = 64: 55 us for 166 MB.
