@@ -609,8 +609,9 @@ flamia_status_t flamia_paged_append(const flamia_paged_t* p, const void* k, cons
  * Keys that a row does not see, and what slots behind a request's last token
  * hold, change no row's precision beyond that.  Ranges: scores over a cache of
  * codes are formed from queries scaled to 2^13 and may overflow from K rows of
- * 2^116 on; sums of weights (at most 2^8 of the first ones) times V are fp32 in
- * all kernels, over E2M1 with V of 2^66 and more in units in which V of any size fits.
+ * 2^116 on; sums of weights (at most 2^8 of the first ones) times V are fp32,
+ * over E2M1 with V of 2^66 and more in units in which V of any size fits.  A
+ * value of 2^128 of an E4M3 row counts as bf16's largest number.
  *   q    device bf16 [T][H][d] (q_stride)
  *   O    device bf16 [T][H][d], contiguous
  *   lse  device float [H][T], natural logarithm (may be NULL)

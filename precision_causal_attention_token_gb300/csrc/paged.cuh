@@ -166,6 +166,13 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// Infinities become bf16's largest numbers: E4M3 rows hold values of 2^128 (255 *
+// 2^120, bf16's largest number, rounds to 256 * 2^120), and 0 x inf is NaN.
+__device__ __forceinline__ uint32_t bf16x2_finite(uint32_t a) {
+  uint32_t r;
+  asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x7F7F7F7Fu));
+  return r;
+}
 // Two fp32 -> bf16x2 (RNE), `lo` in the low half.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;

@@ -738,6 +738,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint32_t f2 = ((max(sc, 134u) - 134u + 127u) << 7) * 0x10001u;
 #pragma unroll
                   for (int k = 0; k < 8; ++k) y[k] = bf16x2_mul(y[k], f2);
+                  if (sc >= 247u) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = bf16x2_finite(y[k]);
+                  }
                 } else if (b & 1) {
                   atomicMin(odd_key, (f.kb0 + b / 2) * kChunkBlk + row);
                 } else {

@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_decode_kernel(const Pag
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const uint32_t two = prmt(w[k & 2], w[(k & 2) + 1], 0x5410u + 0x2222u * half) >> (8 * (k & 1)) & 0x00FF00FFu;
-                  a[k] = bf16x2_mul(bf16x2_mul(e4m3_to_bf16x2(two), f[k >> 1][0]), f[k >> 1][1]);
+                  a[k] = bf16x2_finite(bf16x2_mul(bf16x2_mul(e4m3_to_bf16x2(two), f[k >> 1][0]), f[k >> 1][1]));
                 }
                 mma_bf16(o[2 * x + half][nt], a[0], a[1], a[2], a[3], ph[0], ph[1]);
                 mma_bf16(o[2 * x + half][nt], a[0], a[1], a[2], a[3], pl[0], pl[1]);
