@@ -36,7 +36,7 @@
 //
 // Measured (152 SMs, H = 32, Hkv = 8, d = 128): 2,048 new tokens over 32,768 in
 // bf16 720 us (1,575 TFLOP/s; 808 back to back under the power limit), in E4M3
-// 850, in E2M1 863; four times 4,096 from nothing (16 heads each) 231 us in bf16,
+// 857, in E2M1 863; four times 4,096 from nothing (16 heads each) 231 us in bf16,
 // 294 in E4M3 and in E2M1.  bf16 is bound by the tensor cores, and by 3 to 4 us
 // between one tile's last product and the next one's first; E4M3 by shared memory,
 // which conversion and the MMAs' operands share: a step's operands take 1,536 of
